@@ -1,0 +1,424 @@
+"""Measured cases of the expert-layer operators: routing, the experts' products and gradient clipping.
+
+Each case is one call (or one forward and backward pair) as a user's program makes it.  The plain forms
+are elementary torch operations in 32 bits, rounded once at the end.
+"""
+import math
+
+import torch
+
+own = False
+
+_TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+_BYTES = {"f32": 4, "bf16": 2, "f16": 2}
+
+
+# ---------------------------------------------------------------- the cases
+
+def listed():
+    return [
+        # One token of one request: the router's latency inside a decode step.
+        _route("route_token", 1, 64, 6, "bf16", "softmax"),
+        # A prompt chunk through a balanced sigmoid router with expert groups.
+        _route("route_chunk", 16384, 256, 8, "f32", "sigmoid", bias=True, groups=8, top=4, scale=2.5),
+        # A training batch: an odd number of tokens and experts, padded rows, weights that are not renormalised,
+        # forward and backward.
+        _route("route_train", 8191, 60, 4, "bf16", "softmax", renorm=False, idle=0.03, back=True),
+        # One token through an expert layer: streams the weights of its experts.
+        _experts("experts_token", 1, 64, 6, 2048, 1024, "bf16"),
+        # A decode batch: most experts have a few tokens each.
+        _experts("experts_batch", 48, 128, 8, 2048, 768, "bf16"),
+        # Ragged middle: odd token count, widths that end inside every tile, rows without experts.
+        _experts("experts_ragged", 1777, 24, 3, 1000, 344, "f16", idle=0.05),
+        # A long prompt chunk: bound by the matrix cores.
+        _experts("experts_chunk", 16384, 64, 8, 2048, 1024, "bf16"),
+        # A small training step, odd sizes.
+        _experts("experts_train_small", 509, 16, 2, 512, 264, "f16", idle=0.02, back=True),
+        # A training step of an expert layer: forward, and every gradient.
+        _experts("experts_train", 8192, 64, 8, 2048, 1024, "bf16", back=True),
+        # The gradients of a small model: few tensors, odd lengths.
+        _clip("clip_small", 37, 100_003, "f32"),
+        # The gradients of several expert layers with their routers and norms: 16-bit and 32-bit tensors together.
+        _clip("clip_layers", 300, 800_000_000, "bf16", mixed=True),
+    ]
+
+
+def _route(name, T, E, k, dtype, scores, bias=False, groups=1, top=1, renorm=True, scale=1.0, idle=0.0, back=False):
+    c = dict(kind="route", T=T, E=E, k=k, dtype=dtype, scores=scores, bias=bias, groups=groups, top=top, renorm=renorm,
+             scale=scale, idle=idle, back=back)
+    return {"name": name, **c} if name else c
+
+
+def _experts(name, T, E, k, D, F, dtype, idle=0.0, back=False):
+    c = dict(kind="experts", T=T, E=E, k=k, D=D, F=F, dtype=dtype, idle=idle, back=back)
+    return {"name": name, **c} if name else c
+
+
+def _clip(name, tensors, total, dtype, mixed=False):
+    c = dict(kind="clip", tensors=tensors, total=total, dtype=dtype, mixed=mixed)
+    return {"name": name, **c} if name else c
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(["route", "experts", "experts", "train", "clip"])
+    if kind == "route":
+        groups = rng.choice([1, 1, 2, 4, 8])
+        per = _log(rng, 4, 48)
+        top = rng.randint(1, groups)
+        k = rng.randint(1, min(10, per * top))
+        scores = rng.choice(["softmax", "sigmoid"])
+        return _route("", _log(rng, 1, 16384), per * groups, k, rng.choice(["f32", "bf16", "f16"]), scores,
+                      bias=rng.random() < 0.5, groups=groups, top=top, renorm=rng.random() < 0.6,
+                      scale=rng.choice([1.0, 2.5]), idle=rng.choice([0.0, 0.04]), back=rng.random() < 0.5)
+    if kind == "clip":
+        return _clip("", _log(rng, 1, 400), _log(rng, 10_000, 600_000_000), rng.choice(["f32", "bf16", "f16"]),
+                     mixed=rng.random() < 0.3)
+    E = _log(rng, 4, 128)
+    k = rng.randint(1, min(8, E))
+    D, F = 8 * _log(rng, 16, 320), 8 * _log(rng, 16, 200)
+    T = _log(rng, 1, 12288) if kind == "experts" else _log(rng, 32, 6144)
+    # No more weights, and no more products, than the largest listed case.
+    T = max(1, min(T, int(16384 * 8 * 2048 * 1024 / 2 / (k * D * F))))
+    E = max(k, min(E, int(64 * 2048 * 1024 / (D * F))))
+    return _experts("", T, E, k, D, F, rng.choice(["bf16", "f16"]), idle=rng.choice([0.0, 0.05]), back=kind == "train")
+
+
+# ---------------------------------------------------------------- inputs
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale=1.0, dtype=torch.float32):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=dtype).mul_(scale)
+
+    def share(n, p):
+        return torch.rand(n, generator=gen, device="cuda") < p
+
+    state = dict(case)
+    if case["kind"] == "clip":
+        state.update(_prepare_clip(case, normal, seed))
+        return state
+    T, E, k, t = case["T"], case["E"], case["k"], _TYPES[case["dtype"]]
+    logits = normal(T, E) + normal(1, E, scale=0.3)  # some experts are liked more
+    active = ~share(T, case["idle"]) if case["idle"] else None
+    if case["kind"] == "route":
+        state["logits"] = logits.to(t)
+        state["bias"] = normal(E, scale=0.1) if case["bias"] else None
+        state["active"] = active
+        state["grad"] = normal(T, k) if case["back"] else None
+        return state
+    D, F = case["D"], case["F"]
+    best, col = torch.topk(logits, k, dim=1)
+    col, at = torch.sort(col, dim=1)
+    val = torch.softmax(best, dim=1).gather(1, at)
+    if active is not None:
+        col = torch.where(active[:, None], col, -1)
+        val = torch.where(active[:, None], val, 0.0)
+    state["col"], state["val"] = col.to(torch.int32).contiguous(), val.contiguous()
+    state["x"] = normal(T, D).to(t)
+    state["w_in"] = normal(E, 2 * F, D, scale=D ** -0.5, dtype=t)
+    state["w_out"] = normal(E, D, F, scale=F ** -0.5, dtype=t)
+    state["grad"] = normal(T, D).to(t) if case["back"] else None
+    return state
+
+
+def _lengths(case):
+    """Tensor lengths that add up to about the total, spread over a factor of 30 (routers, norms, experts)."""
+    n, total = case["tensors"], case["total"]
+    w = [30.0 ** ((7 * i % n) / n) for i in range(n)]
+    return [max(1, int(total * x / sum(w))) for x in w]
+
+
+def _clip_type(case, i):
+    return "f32" if case["mixed"] and i % 3 == 0 else case["dtype"]
+
+
+def _prepare_clip(case, normal, seed):
+    # One allocation per type, as a training program keeps its gradients; every tensor begins at a multiple of 64 elements.
+    n = _lengths(case)
+    at, size = [], {}
+    for i, m in enumerate(n):
+        t = _clip_type(case, i)
+        at.append((t, size.get(t, 0)))
+        size[t] = size.get(t, 0) + (m + 63) // 64 * 64
+    flat = {t: normal(m, scale=0.01, dtype=_TYPES[t]) for t, m in size.items()}
+    clipped = {t: torch.zeros_like(v) for t, v in flat.items()}
+    views = [[f[t][o:o + m] for (t, o), m in zip(at, n)] for f in (flat, clipped)]
+    return {"grads": views[0], "out": views[1], "flat": clipped, "max_norm": 1.0 if seed % 4 else 1e6}
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(state):
+    if own:
+        return _run_own(state)
+    return {"route": _plain_route, "experts": _plain_experts, "clip": _plain_clip}[state["kind"]](state)
+
+
+def _run_own(s):
+    import spgemm_symbolic_row_amd as sg
+
+    if s["kind"] == "route":
+        r = sg.route(s["logits"], s["k"], scores=s["scores"], bias=s["bias"], groups=s["groups"], top_groups=s["top"],
+                     renormalise=s["renorm"], scale=s["scale"], active=s["active"])
+        out = {"col": r.col, "val": r.val}
+        if s["grad"] is not None:
+            out["grad_logits"] = sg.route_backward(s["logits"], r, s["grad"])
+        return out
+    if s["kind"] == "clip":
+        norm = sg.clip_grad_norm(s["grads"], s["max_norm"], out=s["out"])
+        return {"norm": norm, **s["flat"]}
+    if s["grad"] is None:
+        return {"y": sg.experts(s["x"], s["w_in"], s["w_out"], s["col"], s["val"])}
+    y, kept = sg.experts(s["x"], s["w_in"], s["w_out"], s["col"], s["val"], keep=True)
+    dx, dw_in, dw_out, dval = sg.experts_backward(s["grad"], kept)
+    return {"y": y, "grad_x": dx, "grad_w_in": dw_in, "grad_w_out": dw_out, "grad_val": dval}
+
+
+def _plain_route(s):
+    z = s["logits"].float()
+    T, E = z.shape
+    k, inf = s["k"], float("inf")
+    sig = 1.0 / (1.0 + torch.exp(-z))
+    key = z if s["scores"] == "softmax" else sig
+    if s["bias"] is not None:
+        key = key + s["bias"]
+    fits = (z > -inf) & (key == key)
+    if s["active"] is not None:
+        fits = fits & s["active"][:, None]
+    allowed = fits
+    if s["groups"] > 1:
+        G = s["groups"]
+        by = torch.where(fits, key, -inf).view(T, G, E // G)
+        best = torch.sort(by, dim=2, descending=True).values
+        score = best[:, :, 0]
+        if s["scores"] == "sigmoid" and E // G > 1:
+            score = score + torch.where(best[:, :, 1] > -inf, best[:, :, 1], 0.0)
+        first = torch.sort(score, dim=1, descending=True, stable=True).indices[:, :s["top"]]
+        chosen = torch.zeros(T, G, dtype=torch.bool, device=z.device).scatter_(1, first, True)
+        allowed = fits & chosen.repeat_interleave(E // G, dim=1)
+    ranked, at = torch.sort(torch.where(allowed, key, -inf), dim=1, descending=True, stable=True)
+    there = torch.gather(allowed, 1, at)[:, :k]
+    col, order = torch.sort(torch.where(there, at[:, :k], E), dim=1)
+    there = torch.gather(there, 1, order)
+    pick = torch.where(there, col, 0)
+    # The weights, and what the gradient needs of them.
+    if s["scores"] == "softmax":
+        among = torch.where(there, torch.gather(z, 1, pick), -inf)
+        every = among if s["renorm"] else torch.where(fits, z, -inf)
+        top = every.amax(1, keepdim=True)
+        top = torch.where(top > -inf, top, 0.0)
+        total = torch.exp(every - top).sum(1, keepdim=True)
+        w = torch.where(there, torch.exp(among - top) / total, 0.0)
+    else:
+        w = torch.where(there, torch.gather(sig, 1, pick), 0.0)
+        total = w.sum(1, keepdim=True) + 1e-20 if s["renorm"] else 1.0
+        w = w / total
+    out = {"col": torch.where(there, col, -1).to(torch.int32), "val": w * s["scale"]}
+    if s["grad"] is not None:
+        dw = torch.where(there, s["grad"], 0.0) * s["scale"]
+        mean = (w * dw).sum(1, keepdim=True)
+        if s["scores"] == "softmax" and not s["renorm"]:
+            p = torch.where(fits, torch.exp(every - top) / total, 0.0)
+            dz = -p * mean
+            dz = dz.scatter_add(1, pick, w * dw)
+        else:
+            if s["scores"] == "softmax":
+                d = w * (dw - mean)
+            else:
+                q = torch.gather(sig, 1, pick)
+                d = (dw - mean) / total if s["renorm"] else dw
+                d = torch.where(there, d * q * (1.0 - q), 0.0)
+            dz = torch.zeros_like(z).scatter_add(1, pick, torch.where(there, d, 0.0))
+        out["grad_logits"] = dz.to(s["logits"].dtype)
+    return out
+
+
+def _plain_experts(s):
+    x, w_in, w_out, col, val = s["x"].float(), s["w_in"], s["w_out"], s["col"].long(), s["val"]
+    (T, D), E, F, k = x.shape, w_in.shape[0], w_out.shape[2], s["k"]
+    n = T * k
+    flat = col.reshape(-1)
+    there = flat >= 0
+    few = n <= E and s["grad"] is None
+    if few:  # the weights of each entry's expert
+        block, cap, slot = torch.where(there, flat, 0), 1, torch.where(there, torch.arange(n, device=x.device), n)
+        w1, w2 = w_in[block].float(), w_out[block].float()
+    else:    # every expert's rows side by side, filled up to the longest
+        key = torch.where(there, flat, E)
+        order = torch.sort(key, stable=True).indices
+        count = torch.bincount(key, minlength=E + 1)
+        first = torch.cumsum(count, 0) - count
+        cap = max(1, int(count[:E].max()))
+        rank = torch.empty_like(flat)
+        rank[order] = torch.arange(n, device=x.device) - first[key[order]]
+        slot = torch.where(there, key * cap + rank, E * cap)
+        w1, w2 = w_in.float(), w_out.float()
+    B = w1.shape[0]
+    token = torch.arange(n, device=x.device) // k
+    xs = x.new_zeros(B * cap + 1, D)
+    xs[slot] = x[token]
+    xs = xs[:-1].view(B, cap, D)
+    gu = torch.bmm(xs, w1.transpose(1, 2))
+    g, u = gu[:, :, :F], gu[:, :, F:]
+    sg = 1.0 / (1.0 + torch.exp(-g))
+    h = g * sg * u
+    o = torch.cat([torch.bmm(h, w2.transpose(1, 2)).view(B * cap, D), x.new_zeros(1, D)])
+    y = (o[slot].view(T, k, D) * val[:, :, None]).sum(1).to(s["x"].dtype)
+    if s["grad"] is None:
+        return {"y": y}
+    dy = s["grad"].float()
+    ds = x.new_zeros(B * cap + 1, D)
+    ds[slot] = dy[token]
+    ds = ds[:-1].view(B, cap, D)
+    ws = x.new_zeros(B * cap + 1)
+    ws[slot] = val.reshape(-1)
+    ws = ws[:-1].view(B, cap, 1)
+    q = torch.bmm(ds, w2)
+    dval = torch.cat([(h * q).sum(2).reshape(-1), x.new_zeros(1)])[slot].view(T, k)
+    dh = q * ws
+    dgu = torch.cat([dh * u * sg * (1.0 + g * (1.0 - sg)), dh * g * sg], dim=2)
+    dxs = torch.cat([torch.bmm(dgu, w1).view(B * cap, D), x.new_zeros(1, D)])
+    dx = dxs[slot].view(T, k, D).sum(1)
+    dw_in = torch.bmm(dgu.transpose(1, 2), xs)
+    dw_out = torch.bmm(ds.transpose(1, 2), h * ws)
+    t = s["x"].dtype
+    return {"y": y, "grad_x": dx.to(t), "grad_w_in": dw_in.to(t), "grad_w_out": dw_out.to(t), "grad_val": dval}
+
+
+def _plain_clip(s):
+    norm = torch.stack([g.float().square().sum() for g in s["grads"]]).sum().sqrt()
+    c = torch.clamp(s["max_norm"] / (norm + 1e-6), max=1.0)
+    [o.copy_(g.float() * c) for g, o in zip(s["grads"], s["out"])]
+    return {"norm": norm, **s["flat"]}
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+def work(case):
+    if case["kind"] == "clip":
+        n = _lengths(case)
+        size = sum(m * _BYTES[_clip_type(case, i)] for i, m in enumerate(n))
+        return {"bytes": 2 * size, "flops": 3 * sum(n)}
+    T, E, k, b = case["T"], case["E"], case["k"], _BYTES[case["dtype"]]
+    live = T * (1.0 - case["idle"])
+    if case["kind"] == "route":
+        size = T * E * b + T * k * 8
+        if case["back"]:
+            size += T * E * b + T * k * 4
+        return {"bytes": size, "flops": T * E * 4 * (2 if case["back"] else 1)}
+    D, F = case["D"], case["F"]
+    used = E * (1.0 - (1.0 - k / E) ** live)  # experts with a token, were the choice uniform
+    weights = 3 * D * F * b
+    size = used * weights + 2 * T * D * b + T * k * 8
+    flops = 6.0 * live * k * D * F
+    if case["back"]:
+        size += E * weights + 2 * T * D * b + T * k * 4
+        flops *= 3
+    return {"bytes": size, "flops": flops}
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["kind"] == "clip":
+        return _exact_clip(case, s)
+    return _exact_route(s) if case["kind"] == "route" else _exact_experts(s)
+
+
+def _exact_clip(case, s):
+    total = 0.0
+    for g in s["grads"]:
+        total += float(torch.linalg.vector_norm(g.double()) ** 2)
+    norm = math.sqrt(total)
+    c = min(1.0, s["max_norm"] / (norm + 1e-6))
+    out = {t: torch.zeros(v.shape, dtype=torch.float64, device=v.device) for t, v in s["flat"].items()}
+    done = {t: 0 for t in out}
+    for i, g in enumerate(s["grads"]):
+        t = _clip_type(case, i)
+        out[t][done[t]:done[t] + g.numel()] = g.double() * c
+        done[t] += (g.numel() + 63) // 64 * 64
+    return {"norm": torch.tensor(norm, dtype=torch.float64), **out}
+
+
+def _exact_route(s):
+    z = s["logits"].double()
+    T, E = z.shape
+    k, G = s["k"], s["groups"]
+    key = z if s["scores"] == "softmax" else torch.sigmoid(z)
+    if s["bias"] is not None:
+        key = key + s["bias"].double()
+    key = key.clone()
+    if s["active"] is not None:
+        key[~s["active"]] = -math.inf
+    alive = key > -math.inf
+    if G > 1:
+        cut = key.view(T, G, E // G)
+        two = 2 if s["scores"] == "sigmoid" and E // G > 1 else 1
+        score = cut.topk(two, dim=2).values.sum(2)
+        rank = score.argsort(dim=1, descending=True, stable=True).argsort(dim=1)
+        cut[rank >= s["top"]] = -math.inf
+    rank = key.argsort(dim=1, descending=True, stable=True).argsort(dim=1)
+    taken = (rank < k) & (key > -math.inf)
+    if s["scores"] == "softmax":
+        p = torch.softmax(z.masked_fill(~(taken if s["renorm"] else alive), -math.inf), dim=1).nan_to_num(0.0)
+    else:
+        p = torch.sigmoid(z) * taken
+        if s["renorm"]:
+            p = p / (p.sum(1, keepdim=True) + 1e-20)
+    full = p * taken * s["scale"]
+
+    def rows(v):  # the taken entries of every row, in the order of their columns
+        place = torch.where(taken, torch.cumsum(taken, 1) - 1, k)
+        return torch.zeros(T, k + 1, dtype=v.dtype, device=v.device).scatter_(1, place, v)[:, :k]
+
+    out = {"col": None, "val": rows(full)}
+    if s["grad"] is not None:
+        place = (torch.cumsum(taken, 1) - 1).clamp(min=0)
+        dp = torch.gather(s["grad"].double(), 1, place) * taken * s["scale"]
+        if s["scores"] == "softmax":
+            dz = p * (dp - (p * dp).sum(1, keepdim=True))
+        else:
+            q = torch.sigmoid(z)
+            if s["renorm"]:
+                total = (q * taken).sum(1, keepdim=True) + 1e-20
+                dp = (dp - (p * dp).sum(1, keepdim=True)) / total * taken
+            dz = dp * q * (1 - q)
+        out["grad_logits"] = dz
+    return out
+
+
+def _exact_experts(s):
+    x, col, val = s["x"].double(), s["col"], s["val"].double()
+    E, F = s["w_in"].shape[0], s["w_out"].shape[2]
+    y = torch.zeros_like(x)
+    out = {"y": y}
+    if s["grad"] is not None:
+        dy = s["grad"].double()
+        out["grad_x"], out["grad_val"] = torch.zeros_like(x), torch.zeros_like(val)
+        out["grad_w_in"] = torch.zeros(s["w_in"].shape, dtype=torch.float64, device=x.device)
+        out["grad_w_out"] = torch.zeros(s["w_out"].shape, dtype=torch.float64, device=x.device)
+    for e in range(E):
+        t, i = torch.nonzero(col == e, as_tuple=True)
+        if not len(t):
+            continue
+        w1, w2, xe, w = s["w_in"][e].double(), s["w_out"][e].double(), x[t], val[t, i][:, None]
+        g, u = (xe @ w1.T).split(F, dim=1)
+        a = torch.nn.functional.silu(g)
+        y.index_add_(0, t, w * ((a * u) @ w2.T))
+        if s["grad"] is None:
+            continue
+        d = dy[t]
+        q = d @ w2
+        out["grad_val"][t, i] = (a * u * q).sum(1)
+        s1 = torch.sigmoid(g)
+        dgu = torch.cat([w * q * u * (s1 + a * (1 - s1)), w * q * a], dim=1)
+        out["grad_x"].index_add_(0, t, dgu @ w1)
+        out["grad_w_in"][e] = dgu.T @ xe
+        out["grad_w_out"][e] = d.T @ (w * a * u)
+    return out
