@@ -187,7 +187,7 @@ def _plain_route(s):
     key = z if s["scores"] == "softmax" else sig
     if s["bias"] is not None:
         key = key + s["bias"]
-    fits = (z > -inf) & (key == key)
+    fits = (z > -inf) & (key > -inf)
     if s["active"] is not None:
         fits = fits & s["active"][:, None]
     allowed = fits
