@@ -52,7 +52,12 @@ typedef enum spgemm_status {
   SPGEMM_ERR_INTERNAL = -7        /* a device-side capacity check tripped    */
 } spgemm_status;
 
-typedef enum spgemm_dtype { SPGEMM_F32 = 0, SPGEMM_F64 = 1 } spgemm_dtype;
+typedef enum spgemm_dtype {
+  SPGEMM_F32 = 0, /* CSR values, logits, gradients */
+  SPGEMM_F64 = 1, /* CSR values                    */
+  SPGEMM_BF16 = 2, /* the expert layer's tensors   */
+  SPGEMM_F16 = 3
+} spgemm_dtype;
 
 /* Optional device allocator: return a device pointer of at least `bytes`
  * usable in stream order on `stream`, or NULL on failure.  With alloc == NULL
@@ -419,6 +424,125 @@ spgemm_status spgemm_transpose_noalloc(int64_t m, int64_t n, int64_t nnz,
                                        spgemm_dtype dtype, void *dT_row_ptr,
                                        int32_t t_rowptr64, int32_t *dT_col,
                                        void *dT_val, void *stream);
+
+/* ---- The sparse expert layer ----------------------------------------------
+ * A router picks k experts for every token: a sparse routing matrix R
+ * (tokens x experts) whose row t holds the picked experts, columns rising,
+ * and their weights.  Rows have k slots; a slot that holds no entry has
+ * column -1 and value 0 and comes last, so with every slot taken (col, val)
+ * and row_ptr[t] = t * k are R in CSR.  The experts' layer is the product
+ * y_t = sum over row t of R[t,e] f_e(x_t).
+ *
+ * These calls are asynchronous on `stream`, allocate nothing and can be
+ * captured in a graph.  Workspaces belong to the caller and hold nothing
+ * between calls, but for the `kept` block that a forward pass leaves for its
+ * backward pass. */
+
+typedef struct spgemm_route_options {
+  int32_t sigmoid;        /* scores: 0 softmax, 1 sigmoid (1 / (1 + exp(-z)))  */
+  int32_t groups;         /* expert groups of equal size, 0 = 1, at most 64    */
+  int32_t top_groups;     /* groups that may be picked from, 0 = all           */
+  int32_t no_renormalise; /* 0: the weights of a row sum to `scale`            */
+  float scale;            /* factor on the weights, 0 = 1                      */
+} spgemm_route_options;
+
+/* Routing: row t of dCol / dVal (T x k) from row t of the logits (T rows of E,
+ * row stride ld elements; fp32, bf16 or fp16).
+ *   key = z + bias (softmax) or sigmoid(z) + bias (sigmoid), in fp32; bias
+ *   (E, fp32) may be NULL and only enters the keys.  An expert is out where
+ *   its logit or key is minus infinity or NaN, and in rows whose byte of
+ *   dActive (T, may be NULL) is 0, whatever such a row holds.
+ *   Groups: the top_groups groups with the largest scores, a score being the
+ *   group's largest key (softmax) or the sum of its two largest (sigmoid).
+ *   Picked: the k largest keys left; of equal ones the lowest expert, and of
+ *   equal groups the lowest.
+ *   Weights: exp(z) over the sum of exp(z) of the picked experts, or, with
+ *   no_renormalise, of all that are not out; sigmoid(z), divided by the
+ *   picked ones' sum + 1e-20 unless no_renormalise.  Times scale.
+ * Errors: INVALID_ARG (E outside [1, 1024], k outside [1, 64] or above the
+ * experts of the chosen groups, groups that do not divide E, ld < E, bad
+ * dtype, null arrays), INDEX_OVERFLOW (T * k above INT32_MAX), HIP. */
+spgemm_status spgemm_route(int64_t T, int64_t E, int32_t k, const void *dLogits,
+                           int64_t ld, spgemm_dtype dtype, const float *dBias,
+                           const uint8_t *dActive,
+                           const spgemm_route_options *opts, int32_t *dCol,
+                           float *dVal, void *stream);
+
+/* The gradient of the logits (T x E, contiguous, in the logits' type; every
+ * element is written) for the gradient of the values (T x k).  dCol is what
+ * spgemm_route gave for the same arguments; the scores are computed again. */
+spgemm_status spgemm_route_backward(int64_t T, int64_t E, int32_t k,
+                                    const void *dLogits, int64_t ld,
+                                    spgemm_dtype dtype, const float *dBias,
+                                    const spgemm_route_options *opts,
+                                    const int32_t *dCol, const float *dGradVal,
+                                    void *dGradLogits, void *stream);
+
+/* Dispatch, the transpose of R: dRowPtr (E + 1) and dEntry (T * k), the
+ * entries t * k + i of every expert in rising order.  Columns outside [0, E)
+ * are no entries.  Work: spgemm_dispatch_workspace bytes. */
+int64_t spgemm_dispatch_workspace(int64_t T, int32_t k, int64_t E);
+spgemm_status spgemm_dispatch(int64_t T, int32_t k, int64_t E,
+                              const int32_t *dCol, int32_t *dRowPtr,
+                              int32_t *dEntry, void *dWork, int64_t work_bytes,
+                              void *stream);
+
+/* An expert layer: x is T x D, w_in E x 2F x D (an expert's F gate rows, then
+ * its F up rows), w_out E x D x F, all bf16 or fp16. */
+typedef struct spgemm_experts_desc {
+  int64_t tokens, experts, width, hidden; /* T, E, D, F                        */
+  int64_t x_ld;        /* row stride of x in elements, at least D              */
+  int64_t grad_ld;     /* row stride of grad_y (backward)                      */
+  int32_t k;           /* slots of a row of R                                  */
+  spgemm_dtype dtype;  /* SPGEMM_BF16 or SPGEMM_F16                            */
+  int32_t unaligned;   /* 1: a base address is no multiple of 16 bytes         */
+  int32_t reserved;
+} spgemm_experts_desc;
+
+/* Bytes of the kept block and of the two workspaces (any may be NULL).
+ * Operands whose rows do not begin at 16-byte boundaries (D, F or a stride no
+ * multiple of 8, or `unaligned`) are copied, and the copies counted. */
+spgemm_status spgemm_experts_sizes(const spgemm_experts_desc *desc,
+                                   int64_t *kept, int64_t *forward_work,
+                                   int64_t *backward_work);
+
+/* y_t = sum over row t of w * W_out[e] (silu(W_gate[e] x_t) * (W_up[e] x_t)),
+ * T x D contiguous; 0 for a row without entries.  Products and sums in fp32;
+ * the hidden vector is rounded once to the tensors' type, y once.  Columns
+ * outside [0, E) are no entries.  With dKept (the sizes call's bytes) the
+ * pass leaves what the backward pass needs there. */
+spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
+                                     const void *dX, const void *dWIn,
+                                     const void *dWOut, const int32_t *dCol,
+                                     const float *dVal, void *dY, void *dKept,
+                                     void *dWork, int64_t work_bytes,
+                                     void *stream);
+
+/* Gradients of x (T x D), w_in, w_out (in the tensors' type) and of the
+ * values (T x k, fp32, 0 in empty slots).  Every element is written: 0 for
+ * experts without tokens.  Sums in fp32, in an order that only the routing
+ * fixes: the same call gives the same bits. */
+spgemm_status spgemm_experts_backward(
+    const spgemm_experts_desc *desc, const void *dX, const void *dWIn,
+    const void *dWOut, const float *dVal, const void *dGradY,
+    const void *dKept, void *dGradX, void *dGradWIn, void *dGradWOut,
+    float *dGradVal, void *dWork, int64_t work_bytes, void *stream);
+
+/* The global norm of `count` tensors (fp32, bf16 or fp16, mixed at will) and
+ * its clipping: norm = sqrt(sum g^2) in fp64, rounded into dNorm (1 fp32);
+ * out = g * min(1, max_norm / (norm + 1e-6)), rounded once to out's type.
+ * out[i] may be grads[i] itself; other overlaps are not allowed.  A norm that
+ * is NaN makes every output NaN.  The tables of pointers, sizes (elements) and
+ * types are host arrays, read during the call.
+ * Errors: INVALID_ARG (null arrays, negative sizes, bad types, max_norm
+ * negative or NaN, a workspace too small), INDEX_OVERFLOW, HIP. */
+int64_t spgemm_clip_grad_norm_workspace(int64_t count);
+spgemm_status spgemm_clip_grad_norm(int64_t count, const void *const *dGrads,
+                                    void *const *dOut, const int64_t *sizes,
+                                    const int32_t *grad_types,
+                                    const int32_t *out_types, double max_norm,
+                                    float *dNorm, void *dWork,
+                                    int64_t work_bytes, void *stream);
 
 #ifdef __cplusplus
 }

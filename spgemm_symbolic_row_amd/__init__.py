@@ -20,6 +20,8 @@ from dataclasses import dataclass
 __all__ = [
     "lib", "Options", "Params", "Stats", "CsrDevice", "Plan", "matmul", "compute_params",
     "prune_colnorm", "SpgemmError", "to_device", "last_stats",
+    "Routing", "route", "route_backward", "dispatch", "experts", "experts_backward",
+    "clip_grad_norm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -147,6 +149,8 @@ def lib():
                                        c_vp, c_i32, c_vp, c_vp, c_vp]
         L.spgemm_transpose_noalloc.restype = st
         L.spgemm_transpose_noalloc.argtypes = L.spgemm_transpose.argtypes
+        from ._expert_abi import declare
+        declare(L)
         _lib = L
     return _lib
 
@@ -422,3 +426,17 @@ def transpose(A, out_rowptr64=False, pattern_only=False, no_alloc=False):
                                   1 if out_rowptr64 else 0, tcol.data_ptr(),
                                   None if tval is None else tval.data_ptr(), c_vp(stream)))
     return CsrDevice(trp, tcol, tval, X.n, X.m)
+
+
+_EXPERT_LAYER = ("Routing", "route", "route_backward", "dispatch", "experts", "experts_backward",
+                 "clip_grad_norm")
+
+
+def __getattr__(name):
+    # The expert layer is loaded on first use: it imports torch.
+    if name in _EXPERT_LAYER:
+        from . import expert_layer
+        for n in _EXPERT_LAYER:
+            globals()[n] = getattr(expert_layer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -30,6 +30,7 @@ COMMON = [
 SOURCES = ["k_util.hip", "k_light.hip", "k_outer.hip", "k_multisplit.hip", "k_heavy.hip",
            "k_chunks.hip", "k_chunkhist.hip", "k_prune.hip", "k_transpose.hip", "k_estimate.hip",
            "noalloc.hip",
+           "k_dispatch.hip", "k_route.hip", "k_experts.hip", "k_gradnorm.hip",
            "api.cpp",
            "params.cpp"]
 
