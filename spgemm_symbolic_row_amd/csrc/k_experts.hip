@@ -8,143 +8,174 @@
 //   dW_out[e] = sum_t dy_t (w h)^T.
 //
 // One kernel makes all six products.  A work group computes a BM x BN tile
-// from K-slices of 64 staged in LDS (two stages), its waves multiply 16x16x32
-// MFMA blocks with fp32 accumulators.  An operand tile lies in LDS in one of
+// from K-slices of 64 staged in LDS, its waves multiply 32x32x16 MFMA blocks
+// with fp32 accumulators.  An operand tile lies in LDS in one of
 // two forms, both filled by 16-byte global-to-LDS loads whose lane-linear
 // destination is permuted by choosing the source address:
 //   row form (K contiguous in memory): [row][64 k], 16-byte chunk c of row r
-//     at slot c ^ (r & 7); fragments are ds_read_b128.
+//     at slot c ^ (r >> 1 & 7); fragments are ds_read_b128.  With r & 7 the
+//     reads ran at 54% of the rate, without the xor at 14%.
 //   column form (K strided): [k][column], the 32-byte segment s of row k at
-//     segment s ^ f(k), f(k) = (k & 3) | (k >> 3 & 1) << 2; fragments are two
-//     transposing 8-byte reads.  The xor spreads the 16 k-rows that one read
-//     touches over the banks.
+//     segment s ^ 2 (k & 3); fragments are two transposing 8-byte reads.  With
+//     (k & 3) | (k >> 3 & 1) << 2 they ran at 74%, without the xor at 39%.
 // Rows that a tile has not, and K beyond its end, are read from a block of
 // zeros, so no tile ever multiplies foreign data.
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "expert_common.hpp"
 
 namespace sg {
 namespace {
 
-constexpr int kBK = 64;  // K of one stage
+constexpr int kBK = 64;    // K of one slice: a 128-byte line of a row
+constexpr int kWaves = 4;  // 2 x 2, each a quarter of the tile
+constexpr int kNT = kWaves * kWave;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
-template <typename T>
-struct Vec8 { typedef T type __attribute__((ext_vector_type(8))); };
+typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ f32x4 mfma(__bf16, s16x8 a, s16x8 b, f32x4 c) {
-  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a),
-                                                 __builtin_bit_cast(v8, b), c, 0, 0, 0);
+// c += a b (32 x 32 x 16), c in accumulation registers.  Written out because
+// the compiler, with 256 accumulators and two sets of fragments, moves
+// accumulators between the register files inside the loop.  It does not know
+// the instruction here, so the two wait states that a vector write of a, b or c
+// needs before it are part of it, and settle() stands between the last one and
+// reads of c.
+//
+// The forms with a load also send 64 lanes x 16 bytes from each lane's address
+// to LDS, lane-linear from lds + at (uniform).  Nothing waits for such a load
+// but wait_loads() and wait_slice(): the compiler, which would wait before the
+// next LDS read, does not see it.  The product stands between the write of M0
+// and the load, which must not follow at once.
+#define SG_MFMA_FORMS(T, NAME)                                                                  \
+  __device__ __forceinline__ void mfma(T, s16x8 a, s16x8 b, f32x16& c) {                        \
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_" NAME " %0, %1, %2, %0"                       \
+                 : "+a"(c)                                                                      \
+                 : "v"(a), "v"(b));                                                             \
+  }                                                                                             \
+  template <int kAt>                                                                            \
+  __device__ __forceinline__ void mfma_load(T, s16x8 a, s16x8 b, f32x16& c, uint32_t lds,       \
+                                            const void* p) {                                    \
+    asm volatile("s_add_u32 m0, %3, %5\n\ts_nop 0\n\tv_mfma_f32_32x32x16_" NAME               \
+                 " %0, %1, %2, %0\n\tglobal_load_lds_dwordx4 %4, off"                           \
+                 : "+a"(c)                                                                      \
+                 : "v"(a), "v"(b), "s"(lds), "v"(p), "n"(kAt)                                   \
+                 : "memory", "scc");                                                            \
+  }                                                                                             \
+  template <int kAt>                                                                            \
+  __device__ __forceinline__ void mfma_load(T, s16x8 a, s16x8 b, f32x16& c, uint32_t lds,       \
+                                            const void* base, uint32_t off) {                   \
+    asm volatile("s_add_u32 m0, %3, %6\n\ts_nop 0\n\tv_mfma_f32_32x32x16_" NAME               \
+                 " %0, %1, %2, %0\n\tglobal_load_lds_dwordx4 %4, %5"                            \
+                 : "+a"(c)                                                                      \
+                 : "v"(a), "v"(b), "s"(lds), "v"(off), "s"(base), "n"(kAt)                      \
+                 : "memory", "scc");                                                            \
+  }
+SG_MFMA_FORMS(__bf16, "bf16")
+SG_MFMA_FORMS(_Float16, "f16")
+#undef SG_MFMA_FORMS
+
+template <int MT, int NT>
+__device__ __forceinline__ void settle(f32x16 (&c)[MT][NT]) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) asm volatile("" : "+a"(c[m][n]));
 }
-__device__ __forceinline__ f32x4 mfma(_Float16, s16x8 a, s16x8 b, f32x4 c) {
-  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a),
-                                                __builtin_bit_cast(v8, b), c, 0, 0, 0);
-}
 
-static __device__ __align__(16) const uint32_t zeros16[4] = {0, 0, 0, 0};
-
-// 64 lanes x 16 bytes from each lane's address to LDS, lane-linear from
-// `lds` (uniform).  Nothing waits for it but wait_stage(): the compiler, which
-// would wait before the next LDS read, does not see it.  A load to LDS must
-// not follow a write of M0 at once, hence the s_nop.
-__device__ __forceinline__ void load_to_lds(const void* p, uint32_t lds) {
+// The load alone.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* p) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds),
                "v"(p)
                : "memory");
 }
-// The wave's loads to LDS and its LDS reads are done, then all waves' are.
-__device__ __forceinline__ void wait_stage() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// All but the wave's last kLeft vector memory operations are done; then all
+// waves' are.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLeft) : "memory");
+}
+// The same, and the wave's LDS reads are done.
+template <int kLeft>
+__device__ __forceinline__ void wait_slice() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-__device__ __forceinline__ s16x8 lds_read8(uint32_t a) {
-  return *(const __attribute__((address_space(3))) s16x8*)a;
+// 1 / (1 + exp(-g)) to about 2 ulp: exp by the native base-2 exponential, with
+// the rounding of its argument put back; the clamp keeps the argument finite.
+__device__ __forceinline__ float fast_sigmoid(float g) {
+  constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+  const float x = fminf(fmaxf(-g, -87.0f), 87.0f);
+  const float t = x * kLog2e;
+  const float r = fmaf(x, kLog2e, -t);
+  float e = __builtin_amdgcn_exp2f(t);
+  e = fmaf(e, r * kLn2, e);
+  return __builtin_amdgcn_rcpf(1.0f + e);
 }
-__device__ __forceinline__ s16x4 lds_read_tr(uint32_t a) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)a);
-}
+
+static __device__ __align__(16) const uint32_t zeros16[4] = {0, 0, 0, 0};
 
 // ---- operand tiles ----
+// Where a lane's share of a tile lies.  Load i of wave w fills bytes
+// (i * kWaves + w) * 1024 .. of the tile, 16 for each lane.
 
-// Row form: ROWS rows of K, loaded by NW waves.
-template <int ROWS, int NW>
-struct RowTile {
-  static constexpr int kBytes = ROWS * kBK * 2;
-  static constexpr int kLoads = kBytes / (NW * 1024);
-  static_assert(kLoads * NW * 1024 == kBytes, "tile must divide over the waves");
-  const char* p[kLoads];  // the lane's chunk of row i in the current slice
-  int k;                  // its first k there
+// Row form: rows of kBK consecutive K; a load covers 8 rows.
+struct RowForm {
   __device__ static int row(int i) {
-    return (i * NW + (int)threadIdx.x / kWave) * 8 + lane_id() / 8;
+    return (i * kWaves + (int)threadIdx.x / kWave) * 8 + lane_id() / 8;
   }
-  __device__ static int chunk() { return (lane_id() & 7) ^ (lane_id() >> 3); }
-  __device__ void start() { k = chunk() * 8; }
-  // `src` is row i's first element, null for a row that is not there.
-  __device__ void set_row(int i, const void* src) {
-    p[i] = src ? (const char*)src + chunk() * 16 : nullptr;
-  }
-  __device__ void load(uint32_t lds, int wave, int K) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const bool ok = p[i] && k < K;
-      load_to_lds(ok ? p[i] : (const char*)zeros16, lds + (i * NW + wave) * 1024);
-      if (p[i]) p[i] += kBK * 2;
-    }
-    k += kBK;
-  }
-  // Fragment addresses: rows row0 + 16 m + lane % 16, K step kk of 32.
-  uint32_t base;
-  uint32_t swz;
+  __device__ static int k() { return ((lane_id() & 7) ^ ((row(0) >> 1) & 7)) * 8; }
+  // Fragments: rows row0 + 32 m + lane % 32, k 16 kb + lane / 32 * 8 .. + 7.
+  uint32_t at[4];  // by kb
   __device__ void frag_init(int row0) {
     const int l = lane_id();
-    base = (row0 + (l & 15)) * (kBK * 2);
-    swz = ((l >> 4) ^ (l & 7)) * 16;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+      at[kb] = (row0 + (l & 31)) * (kBK * 2) + (((kb * 2 + (l >> 5)) ^ ((l >> 1) & 7)) * 16);
   }
-  __device__ s16x8 frag(uint32_t lds, int m, int kk) const {
-    return lds_read8(lds + base + m * 16 * kBK * 2 + (swz ^ (kk * 64)));
+  __device__ s16x8 frag(uint32_t lds, int m, int kb) const {
+    return *(const __attribute__((address_space(3))) s16x8*)((const lds_char*)(lds + at[kb]) +
+                                                             m * 32 * kBK * 2);
   }
 };
 
-// Column form: 64 k-rows of COLS columns.
-template <int COLS, int NW>
-struct ColTile {
-  static constexpr int kBytes = COLS * kBK * 2;
-  static constexpr int kLoads = kBytes / (NW * 1024);
+// Column form: kBK k-rows of COLS columns.
+template <int COLS>
+struct ColForm {
   static constexpr int kRowBytes = COLS * 2;
   static constexpr int kRowsPerLoad = 1024 / kRowBytes;
-  static_assert(kLoads * NW * 1024 == kBytes && kRowsPerLoad >= 1, "tile over the waves");
-  __device__ static int f(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
-  // k-row of load i within the slice.
+  static_assert(kRowsPerLoad >= 1, "a load covers whole rows");
+  __device__ static int f(int k) { return (k & 3) * 2; }
   __device__ static int row(int i) {
-    return (i * NW + (int)threadIdx.x / kWave) * kRowsPerLoad + lane_id() * 16 / kRowBytes;
+    return (i * kWaves + (int)threadIdx.x / kWave) * kRowsPerLoad + lane_id() * 16 / kRowBytes;
   }
-  // First column of the lane's chunk in load i (the same for every slice).
-  __device__ static int col(int i) {
+  // First column of the lane's chunk, the same in every load.
+  __device__ static int col() {
     const int c = lane_id() % (kRowBytes / 16);
     const int seg = c >> 1;
-    return (((seg & ~7) | ((seg ^ f(row(i))) & 7)) * 2 + (c & 1)) * 8;
+    return (((seg & ~7) | ((seg ^ f(row(0))) & 7)) * 2 + (c & 1)) * 8;
   }
-  __device__ static void load(uint32_t lds, int wave, int i, const void* src) {
-    load_to_lds(src ? src : (const void*)zeros16, lds + (i * NW + wave) * 1024);
-  }
-  uint32_t base;
-  int seg0, fk;
+  // Fragments: columns col0 + 32 m + lane % 32, k as in the row form.  A lane
+  // gives the address of 4 columns of one k-row and gets 4 k of one column.
+  uint32_t at[4];  // by m
   __device__ void frag_init(int col0) {
-    const int l = lane_id(), k = (l >> 4) * 8 + ((l & 15) >> 2);
-    fk = f(k);
-    seg0 = col0 / 16;
-    base = k * kRowBytes + (l & 3) * 8;
+    const int l = lane_id(), k = (l >> 5) * 8 + ((l & 15) >> 2);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int seg = col0 / 16 + 2 * m + ((l >> 4) & 1);
+      at[m] = k * kRowBytes + ((seg & ~7) | ((seg ^ f(k)) & 7)) * 32 + (l & 3) * 8;
+    }
   }
-  __device__ s16x8 frag(uint32_t lds, int m, int kk) const {
-    const int s = seg0 + m;
-    const uint32_t a =
-        lds + base + ((s & ~7) | ((s ^ fk) & 7)) * 32 + kk * 32 * kRowBytes;
-    const s16x4 lo = lds_read_tr(a), hi = lds_read_tr(a + 4 * kRowBytes);
+  __device__ s16x8 frag(uint32_t lds, int m, int kb) const {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    lds_char* p = (lds_char*)(lds + at[m]) + kb * 16 * kRowBytes;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * kRowBytes));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 };
@@ -177,9 +208,35 @@ struct ProductArgs {
   float* u;
   void* hw;          // w h
   const float* val;
-  float* dval_part;  // per entry: one partial sum of each 64 columns
+  float* dval_part;  // per entry: one partial sum of each 128 columns
   int parts;
 };
+
+// 8 values to p at once where it is aligned to them (vec) and n >= 8; else the
+// first n one by one.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, int n, const float v[8]) {
+  if (vec && n >= 8) {
+    struct alignas(16) Pack { T v[16 / sizeof(T)]; };
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) {
+      Pack q;
+#pragma unroll
+      for (int j = 0; j < V; ++j) q.v[j] = from_f32<T>(v[i * V + j]);
+      ((Pack*)p)[i] = q;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = from_f32<T>(v[j]);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float v[8]) {
+  const f32x4 a = ((const f32x4*)p)[0], b = ((const f32x4*)p)[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = a[j], v[j + 4] = b[j];
+}
 
 template <typename T>
 __device__ __forceinline__ void store4(T* p, bool vec, int n, const float v[4]) {
@@ -196,291 +253,426 @@ __device__ __forceinline__ void store4(T* p, bool vec, int n, const float v[4]) 
   }
 }
 
-// Work group -> tile.  Work groups go round-robin to the XCDs, so XCD x takes
-// a contiguous share of the tiles; inside it they come as groups of 8 row
-// tiles by all column tiles, which keeps a group's rows and weights in its L2.
-__device__ __forceinline__ bool tile_of(int rows, int cols, int& tr, int& tc) {
-  const int total = rows * cols, share = (total + kXcds - 1) / kXcds;
-  const int b = blockIdx.x, at = b / kXcds;
-  const int lin = (b % kXcds) * share + at;
-  if (at >= share || lin >= total) return false;
+// Tile number `lin` -> row tile and column tile: groups of 8 row tiles by all
+// column tiles, so that the work groups of one XCD, which take consecutive
+// numbers, share rows and weights in its L2.
+__device__ __forceinline__ void tile_at(int lin, int rows, int cols, int& tr, int& tc) {
   const int group = lin / (8 * cols), r = lin % (8 * cols);
   const int gr = min(8, rows - group * 8);
   tr = group * 8 + r % gr;
   tc = r / gr;
-  return true;
 }
 
-template <typename T, int KIND, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * kWave) void k_product(ProductArgs a) {
-  constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
+// What a work group needs to know about its tile.
+struct Tile {
+  int expert;
+  int row0, rows;  // first sorted position and how many (weight gradients: the K)
+  int m0, n0;      // first row (weight gradients) and column of the result
+};
+
+// Positions of the sorted token list that a weight gradient keeps in LDS.
+constexpr int kListLen = 4096;
+
+template <typename F, int... kI>
+__device__ __forceinline__ void for_each_index(F& f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI>{}), ...);
+}
+template <int kN, typename F>
+__device__ __forceinline__ void for_each_index(F& f) {
+  for_each_index(f, std::make_integer_sequence<int, kN>{});
+}
+
+// LDS stages of the operands.  160 KB hold five of 32 KB: the left operand
+// has three, which gives its loads half a slice more.  A weight gradient
+// keeps its token list there instead.
+template <int KIND, int BM>
+struct Stages {
+  static constexpr bool kWGrad = KIND == kGradWOut || KIND == kGradWIn;
+  static constexpr int kA = kWGrad ? 2 : 3, kB = !kWGrad && BM < 256 ? 3 : 2;
+};
+
+template <typename T, int KIND, int BM, int BN>
+__global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product(
+    ProductArgs a) {
+  constexpr int HM = BM / 2, HN = BN / 2, MT = HM / 32, NT = HN / 32;
   constexpr bool kWGrad = KIND == kGradWOut || KIND == kGradWIn;
   constexpr bool kACol = kWGrad, kBCol = kWGrad || KIND == kGradH || KIND == kGradX;
-  constexpr int kStage = (BM + BN) * kBK * 2;
-  extern __shared__ char smem[];
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-  const int wm = wave / WN, wn = wave % WN, l = lane_id();
-
-  // Which tile: expert, its rows, first row and column of the result.
-  int expert, row0, rows, n0;  // row0: first sorted position, rows: how many
-  int m0 = 0;                  // weight gradients: first row of the result
+  constexpr bool kAGather = KIND == kIn || KIND == kGradH || KIND == kGradWOut;
+  constexpr bool kBGather = KIND == kGradWIn;
+  constexpr int kABytes = BM * kBK * 2, kBBytes = BN * kBK * 2;
+  constexpr int AL = BM / 32, BL = BN / 32;  // loads of a wave per slice
+  constexpr int AS = Stages<KIND, BM>::kA, BS = Stages<KIND, BM>::kB;
   constexpr int kNStep = KIND == kIn ? BN / 2 : BN;
+  extern __shared__ char smem[];
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)smem;
+  int32_t* list = (int32_t*)(smem + AS * kABytes + BS * kBBytes);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int wm = wave >> 1, wn = wave & 1, l = lane_id();
+
   const int cols = (a.N + kNStep - 1) / kNStep;
-  int tr, tc;
-  if constexpr (kWGrad) {
-    const int mts = (a.M + BM - 1) / BM;
-    if (!tile_of(a.E * mts, cols, tr, tc)) return;
-    expert = tr / mts;
-    m0 = tr % mts * BM;
-    row0 = a.d.row_ptr[expert];
-    rows = a.d.row_ptr[expert + 1] - row0;
-  } else {
-    if (!tile_of(*a.d.ntiles, cols, tr, tc)) return;
-    expert = a.d.tiles[2 * tr];
-    row0 = a.d.tiles[2 * tr + 1];
-    rows = min(BM, a.d.row_ptr[expert + 1] - row0);
-  }
-  n0 = tc * kNStep;
-  const int K = kWGrad ? rows : a.K;
-  const int slices = (K + kBK - 1) / kBK;
+  const int row_tiles = kWGrad ? a.E * ((a.M + BM - 1) / BM) : *a.d.ntiles;
+  // Work groups go round-robin to the XCDs: XCD x takes a contiguous share.
+  const int total = row_tiles * cols, share = (total + kXcds - 1) / kXcds;
+  const int first = ((int)blockIdx.x % kXcds) * share, last = min(total, first + share);
+  const int lin = first + (int)blockIdx.x / kXcds;
+  if (lin >= last) return;
 
-  const T* A = (const T*)a.a;
-  const T* B = (const T*)a.b + (kWGrad ? 0 : expert * a.b_expert);
-
-  RowTile<BM, NW> ar;
-  RowTile<BN, NW> br;
-  ColTile<BM, NW> ac;
-  ColTile<BN, NW> bc;
-  // Sorted tokens of the next slice's rows (weight gradients).
-  constexpr int AL = ColTile<BM, NW>::kLoads, BL = ColTile<BN, NW>::kLoads;
-  int ai[AL], bi[BL];
-
-  if constexpr (!kACol) {
-    ar.start();
-#pragma unroll
-    for (int i = 0; i < RowTile<BM, NW>::kLoads; ++i) {
-      const int r = ar.row(i);
-      const T* src = nullptr;
-      if (r < rows) {
-        const int64_t at = KIND == kIn || KIND == kGradH ? a.d.tok[row0 + r] : row0 + r;
-        src = A + at * a.lda;
-      }
-      ar.set_row(i, src);
+  Tile t;
+  {
+    int tr, tc;
+    tile_at(lin, row_tiles, cols, tr, tc);
+    if constexpr (kWGrad) {
+      const int mts = (a.M + BM - 1) / BM;
+      t.expert = tr / mts;
+      t.m0 = tr % mts * BM;
+      t.row0 = a.d.row_ptr[t.expert];
+      t.rows = a.d.row_ptr[t.expert + 1] - t.row0;
+    } else {
+      t.expert = a.d.tiles[2 * tr];
+      t.row0 = a.d.tiles[2 * tr + 1];
+      t.rows = min(BM, a.d.row_ptr[t.expert + 1] - t.row0);
+      t.m0 = 0;
     }
-    ar.frag_init(wm * (BM / WM));
+    t.n0 = tc * kNStep;
+  }
+  const int K = kWGrad ? t.rows : a.K;
+  const int steps = (K + kBK - 1) / kBK;
+
+  // Operand addresses: uniform base of the next slice to load, and offsets in
+  // bytes that stay; or, where rows are gathered, pointers.  Rows and columns
+  // outside the result are clamped: what they give is not stored.  K outside
+  // is read from zeros.
+  const T* abase = (const T*)a.a;
+  const T* bbase = (const T*)a.b + (kWGrad ? 0 : t.expert * a.b_expert);
+  if constexpr (kWGrad && !kAGather) abase += (int64_t)t.row0 * a.lda;
+  if constexpr (kWGrad && !kBGather) bbase += (int64_t)t.row0 * a.ldb;
+  if constexpr (!kWGrad && !kAGather) abase += (int64_t)t.row0 * a.lda;
+  RowForm ar, br;
+  ColForm<BM> ac;
+  ColForm<BN> bc;
+  uint32_t aoff[AL], boff[BL];
+  const char* aptr[AL];
+  uint32_t aidx[AL], bidx[BL];  // tokens of the next slice to load (weight gradients)
+  uint32_t acol = 0, bcol = 0;
+  if constexpr (!kACol) {
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int r = min(ar.row(i), t.rows - 1);
+      if constexpr (kAGather)
+        aptr[i] = (const char*)(abase + (int64_t)a.d.tok[t.row0 + r] * a.lda + ar.k());
+      else
+        aoff[i] = ((uint32_t)r * (uint32_t)a.lda + ar.k()) * 2;
+    }
+    ar.frag_init(wm * HM);
   } else {
-    ac.frag_init(wm * (BM / WM));
+    const int c = t.m0 + ac.col();
+    acol = (c < a.Mpad ? c : 0) * 2;
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      aoff[i] = (uint32_t)ac.row(i) * (uint32_t)a.lda * 2 + acol;
+    }
+    ac.frag_init(wm * HM);
   }
   if constexpr (!kBCol) {
-    br.start();
 #pragma unroll
-    for (int i = 0; i < RowTile<BN, NW>::kLoads; ++i) {
+    for (int i = 0; i < BL; ++i) {
       const int r = br.row(i);
-      int64_t n;
+      int n;
       if constexpr (KIND == kIn) {
         // Each wave's columns: half gate rows, then the same rows of up.
-        constexpr int H = BN / WN / 2;
-        const int f = n0 + r / (2 * H) * H + r % H;
-        n = f < a.N ? (r % (2 * H) < H ? f : a.N + f) : -1;
+        constexpr int H = HN / 2;
+        n = min(t.n0 + r / HN * H + r % H, a.N - 1) + (r % HN < H ? 0 : a.N);
       } else {
-        n = n0 + r < a.N ? n0 + r : -1;
+        n = min(t.n0 + r, a.N - 1);
       }
-      br.set_row(i, n >= 0 ? B + n * a.ldb : nullptr);
+      boff[i] = ((uint32_t)n * (uint32_t)a.ldb + br.k()) * 2;
     }
-    br.frag_init(wn * (BN / WN));
+    br.frag_init(wn * HN);
   } else {
-    bc.frag_init(wn * (BN / WN));
+    const int c = t.n0 + bc.col();
+    bcol = (c < a.Npad ? c : 0) * 2;
+#pragma unroll
+    for (int i = 0; i < BL; ++i) {
+      boff[i] = (uint32_t)bc.row(i) * (uint32_t)a.ldb * 2 + bcol;
+    }
+    bc.frag_init(wn * HN);
   }
 
-  // Where the rows of slice s of a column-form operand are: the sorted
-  // position itself, or its token.
-  auto fetch_rows = [&](int s) {
-    if constexpr (kWGrad) {
+  // Address of load i of slice s.
+  auto addr_a = [&](int s, int i) -> const char* {
+    if constexpr (kWGrad && kAGather) return (const char*)abase + (uint64_t)aidx[i] * ((uint32_t)a.lda * 2) + acol;
+    else if constexpr (kAGather) return aptr[i];
+    else return (const char*)abase + aoff[i];
+  };
+  auto addr_b = [&](int s, int i) -> const char* {
+    if constexpr (kBGather) return (const char*)bbase + (uint64_t)bidx[i] * ((uint32_t)a.ldb * 2) + bcol;
+    else return (const char*)bbase + boff[i];
+  };
+  // Whether its K is inside.
+  auto inside_a = [&](int s, int i) {
+    return kACol ? s * kBK + ac.row(i) < K : s * kBK + ar.k() < a.Kpad;
+  };
+  auto inside_b = [&](int s, int i) {
+    return kBCol ? s * kBK + bc.row(i) < K : s * kBK + br.k() < a.Kpad;
+  };
+  auto next_a = [&]() {
+    if constexpr (kACol) {
+      if constexpr (!kAGather) abase += (int64_t)kBK * a.lda;
+    } else if constexpr (kAGather) {
 #pragma unroll
-      for (int i = 0; i < AL; ++i) {
-        const int r = s * kBK + ac.row(i);
-        ai[i] = r < rows ? (KIND == kGradWOut ? a.d.tok[row0 + r] : row0 + r) : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < BL; ++i) {
-        const int r = s * kBK + bc.row(i);
-        bi[i] = r < rows ? (KIND == kGradWIn ? a.d.tok[row0 + r] : row0 + r) : -1;
-      }
+      for (int i = 0; i < AL; ++i) aptr[i] += kBK * 2;
+    } else {
+      abase += kBK;
     }
   };
-  auto load_slice = [&](int s) {
-    const uint32_t lds = lds0 + (s & 1) * kStage;
-    if constexpr (!kACol) {
-      ar.load(lds, wave, a.Kpad);
+  auto next_b = [&]() {
+    if constexpr (kBCol) {
+      if constexpr (!kBGather) bbase += (int64_t)kBK * a.ldb;
     } else {
-#pragma unroll
-      for (int i = 0; i < AL; ++i) {
-        const int c = m0 + ac.col(i);
-        ac.load(lds, wave, i, ai[i] >= 0 && c < a.Mpad ? A + ai[i] * a.lda + c : nullptr);
-      }
+      bbase += kBK;
     }
-    const uint32_t ldsb = lds + BM * kBK * 2;
-    if constexpr (!kBCol) {
-      br.load(ldsb, wave, a.Kpad);
-    } else {
-#pragma unroll
-      for (int i = 0; i < BL; ++i) {
-        const int c = n0 + bc.col(i);
-        int64_t r;
-        if constexpr (kWGrad) {
-          r = bi[i];
-        } else {
-          r = s * kBK + bc.row(i);
-          if (r >= K) r = -1;
-        }
-        bc.load(ldsb, wave, i, r >= 0 && c < a.Npad ? B + r * a.ldb + c : nullptr);
-      }
+  };
+  // The part of the token list that begins at slice s, and the tokens of
+  // slice s from it.
+  auto fill_list = [&](int s) {
+    if constexpr (kWGrad) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kListLen; i += kNT)
+        list[i] = a.d.tok[t.row0 + min(s * kBK + i, K - 1)];
+      __syncthreads();
     }
+  };
+  auto fetch_tokens = [&](int s) {
+    if constexpr (kWGrad && kAGather) {
+#pragma unroll
+      for (int i = 0; i < AL; ++i) aidx[i] = list[(s * kBK + ac.row(i)) % kListLen];
+    }
+    if constexpr (kBGather) {
+#pragma unroll
+      for (int i = 0; i < BL; ++i) bidx[i] = list[(s * kBK + bc.row(i)) % kListLen];
+    }
+  };
+  auto stage_a = [&](int s) { return lds0 + (uint32_t)(s % AS) * kABytes; };
+  auto stage_b = [&](int s) { return lds0 + AS * kABytes + (uint32_t)(s % BS) * kBBytes; };
+  auto frag_a = [&](uint32_t lds, int m, int kb) {
+    if constexpr (kACol) return ac.frag(lds, m, kb);
+    else return ar.frag(lds, m, kb);
+  };
+  auto frag_b = [&](uint32_t lds, int n, int kb) {
+    if constexpr (kBCol) return bc.frag(lds, n, kb);
+    else return br.frag(lds, n, kb);
   };
 
-  f32x4 acc[MT][NT];
+  f32x16 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[m][n][j] = 0.0f;
 
-  if (slices > 0) {
-    fetch_rows(0);
-    load_slice(0);
-    fetch_rows(1);
-    wait_stage();
-  }
-  for (int s = 0; s < slices; ++s) {
-    if (s + 1 < slices) {
-      load_slice(s + 1);
-      fetch_rows(s + 2);
+  if (steps > 0) {
+    fill_list(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      fetch_tokens(s);
+#pragma unroll
+      for (int i = 0; i < AL; ++i)
+        load_to_lds(stage_a(s) + (i * kWaves + wave) * 1024,
+                    inside_a(s, i) ? (const void*)addr_a(s, i) : (const void*)zeros16);
+#pragma unroll
+      for (int i = 0; i < BL; ++i)
+        load_to_lds(stage_b(s) + (i * kWaves + wave) * 1024,
+                    inside_b(s, i) ? (const void*)addr_b(s, i) : (const void*)zeros16);
+      next_a();
+      next_b();
     }
-    const uint32_t lds = lds0 + (s & 1) * kStage, ldsb = lds + BM * kBK * 2;
+    fetch_tokens(2);
+    // A slice has two halves of 32 k.  Half 0 multiplies the fragments of its
+    // own k, read before, and reads those of half 1.  Then the slice is no
+    // longer needed in LDS, and the next one has to be there.  Half 1
+    // multiplies its fragments and reads the next slice's first ones.  The
+    // loads of the slice after that go into half 0 where the operand has a
+    // third stage, into half 1 where it takes the place of this slice.
+    s16x8 fa[2][2][MT], fb[2][2][NT];  // [half][16 k of it][]
+    wait_loads<AL + BL>();
 #pragma unroll
-    for (int kk = 0; kk < kBK / 32; ++kk) {
-      s16x8 fa[MT], fb[NT];
+    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) fb[n] = kBCol ? bc.frag(ldsb, n, kk) : br.frag(ldsb, n, kk);
+      for (int n = 0; n < NT; ++n) fb[0][kb][n] = frag_b(stage_b(0), n, kb);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) fa[m] = kACol ? ac.frag(lds, m, kk) : ar.frag(lds, m, kk);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = mfma(T{}, fb[n], fa[m], acc[m][n]);
+      for (int m = 0; m < MT; ++m) fa[0][kb][m] = frag_a(stage_a(0), m, kb);
     }
-    wait_stage();
-  }
-
-  // acc[m][n][j]: row wm*(BM/WM) + 16 m + l % 16, column 16 n + l / 16 * 4 + j
-  // of the wave's part.
-  if constexpr (KIND == kIn) {
-    T* h = (T*)a.c;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = wm * (BM / WM) + m * 16 + (l & 15);
-      if (r >= rows) continue;
-#pragma unroll
-      for (int n = 0; n < NT / 2; ++n) {
-        const int f = n0 + wn * (BN / WN / 2) + n * 16 + (l >> 4) * 4;
-        if (f >= a.Fpad) continue;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x = acc[m][n][j];
-          v[j] = x / (1.0f + expf(-x)) * acc[m][n + NT / 2][j];
+    // LDS offsets of slices s, s + 1, s + 2.
+    uint32_t la[3] = {stage_a(0), stage_a(1), stage_a(2)};
+    uint32_t lb[3] = {stage_b(0), stage_b(1), stage_b(2)};
+    auto half = [&](int s, auto which, auto checked) {
+      constexpr int P = decltype(which)::value, Q = 1 - P;
+      constexpr bool kCheck = decltype(checked)::value;
+      constexpr bool kLoadA = P == 0 ? AS == 3 : AS == 2, kLoadB = P == 0 ? BS == 3 : BS == 2;
+      constexpr int kLoadsA = kLoadA ? AL : 0, kLoads = kLoadsA + (kLoadB ? BL : 0);
+      const uint32_t ra = la[P], rb = lb[P];
+      const uint32_t wa = la[2] + wave * 1024, wb = lb[2] + wave * 1024;
+      constexpr int kAll = 2 * MT * NT, kReads = 2 * (MT + NT);
+      constexpr int kSpan = kAll * 3 / 4;  // products that reads and loads go between
+      auto step = [&](auto index) {
+        constexpr int i = decltype(index)::value;
+        constexpr int kb = i / (MT * NT), m = i / NT % MT, n = i % NT;
+        constexpr int x = i * kLoads / kSpan;
+        if constexpr (x < kLoads && x != (i + 1) * kLoads / kSpan) {
+          constexpr bool kA = x < kLoadsA;
+          constexpr int y = kA ? x : x - kLoadsA;
+          if constexpr (kCheck) {
+            const char* p = kA ? (inside_a(s + 2, y) ? addr_a(s + 2, y) : (const char*)zeros16)
+                               : (inside_b(s + 2, y) ? addr_b(s + 2, y) : (const char*)zeros16);
+            mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
+                                         p);
+          } else if constexpr (kA ? kAGather : kBGather) {
+            mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
+                                         kA ? addr_a(s + 2, y) : addr_b(s + 2, y));
+          } else {
+            mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
+                                         kA ? abase : bbase, kA ? aoff[y] : boff[y]);
+          }
+        } else {
+          mfma(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n]);
         }
-        const int64_t at = (int64_t)(row0 + r) * a.Fpad + f;
-        store4(h + at, true, 4, v);
+#pragma unroll
+        for (int z = i * kReads / kSpan; z < (i + 1) * kReads / kSpan && z < kReads; ++z) {
+          const int k2 = z / (MT + NT), w = z % (MT + NT);
+          if (w == 0) fa[Q][k2][0] = frag_a(ra, 0, 2 * Q + k2);
+          else if (w <= NT) fb[Q][k2][w - 1] = frag_b(rb, w - 1, 2 * Q + k2);
+          else fa[Q][k2][w - NT] = frag_a(ra, w - NT, 2 * Q + k2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      for_each_index<kAll>(step);
+      if constexpr (kLoadA) next_a();
+      if constexpr (kLoadB) next_b();
+    };
+    const int full = K / kBK;  // slices without an end of K
+    auto slice = [&](int s, auto checked) {
+      half(s, std::integral_constant<int, 0>{}, checked);
+      wait_slice<(AS == 3 ? AL : 0) + (BS == 3 ? BL : 0)>();
+      if constexpr (kWGrad) {
+        if (((s + 3) * kBK) % kListLen == 0) fill_list(s + 3);
+      }
+      half(s, std::integral_constant<int, 1>{}, checked);
+      fetch_tokens(s + 3);
+      const uint32_t fa0 = AS == 3 ? la[0] : la[1], fb0 = BS == 3 ? lb[0] : lb[1];
+      la[0] = la[1], la[1] = la[2], la[2] = fa0;
+      lb[0] = lb[1], lb[1] = lb[2], lb[2] = fb0;
+    };
+    int s = 0;
+    for (; s + 2 < full; ++s) slice(s, std::false_type{});
+    for (; s < steps; ++s) slice(s, std::true_type{});
+    // The loads of zeros beyond K must not outlive the work group's LDS.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    settle(acc);
+  }
+
+  // The result goes through LDS, 32 rows of the wave's part at a time, so that
+  // every store writes whole stretches of a row.  Stored from the products'
+  // layout, 16 bytes of each of 32 rows at once, the weight gradients took
+  // twice the time.
+  // acc[m][n][4 g + j]: row wm*HM + 32 m + l % 32, column wn*HN + 32 n + 8 g +
+  // l / 32 * 4 + j.
+  wait_slice<0>();
+  constexpr int kPitch = HN + 4;
+  float* stg = (float*)smem + wave * 32 * kPitch;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = acc[m][n][4 * q + j];
+        *(f32x4*)(stg + (l & 31) * kPitch + n * 32 + q * 8 + (l >> 5) * 4) = v;
+      }
+    __builtin_amdgcn_wave_barrier();
+    // 8 columns to a lane, R rows at once.
+    constexpr int kCols = KIND == kIn ? HN / 2 : HN, kLanes = kCols / 8, R = kWave / kLanes;
+    const int lr = l / kLanes, lc = l % kLanes * 8;
+    const int x = t.n0 + wn * kCols + lc;
+#pragma unroll(KIND == kGradH ? 4 : 2)
+    for (int p = 0; p < 32 / R; ++p) {
+      const int rr = p * R + lr, r = wm * HM + m * 32 + rr;
+      const float* src = stg + rr * kPitch + lc;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = src[j];
+      if constexpr (KIND == kIn) {
+        if (r >= t.rows || x >= a.Fpad) continue;
+        float u[8], h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          u[j] = src[kCols + j];
+          if (x + j >= a.F) v[j] = u[j] = 0.0f;
+          h[j] = v[j] * fast_sigmoid(v[j]) * u[j];
+        }
+        const int64_t at = (int64_t)(t.row0 + r) * a.Fpad + x;
+        store8((T*)a.c + at, true, 8, h);
         if (a.g) {
-          *(f32x4*)(a.g + at) = acc[m][n];
-          *(f32x4*)(a.u + at) = acc[m][n + NT / 2];
+          store8(a.g + at, true, 8, v);
+          store8(a.u + at, true, 8, u);
         }
-      }
-    }
-  } else if constexpr (KIND == kOut || KIND == kGradX) {
-    float* c = (float*)a.c;
+      } else if constexpr (KIND == kOut || KIND == kGradX) {
+        if (r < t.rows && x < a.ldc)
+          store8((float*)a.c + (int64_t)(t.row0 + r) * a.ldc + x, true, 8, v);
+      } else if constexpr (KIND == kGradH) {
+        float dot = 0.0f;
+        if (r < t.rows && x < a.Fpad) {
+          const int64_t row = t.row0 + r;
+          const float w = a.val[a.d.ent[row]];
+          float g[8], u[8], dg[8], du[8], hv[8];
+          load8(a.g + row * a.Fpad + x, g);
+          load8(a.u + row * a.Fpad + x, u);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = wm * (BM / WM) + m * 16 + (l & 15);
-      if (r >= rows) continue;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int x = n0 + wn * (BN / WN) + n * 16 + (l >> 4) * 4;
-        if (x < a.ldc) *(f32x4*)(c + (int64_t)(row0 + r) * a.ldc + x) = acc[m][n];
-      }
-    }
-  } else if constexpr (KIND == kGradH) {
-    T* dgu = (T*)a.c;
-    T* hw = (T*)a.hw;
-    const bool vec = a.F % 4 == 0;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = wm * (BM / WM) + m * 16 + (l & 15);
-      float dot = 0.0f;
-      if (r < rows) {
-        const int64_t row = row0 + r;
-        const float w = a.val[a.d.ent[row]];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int f = n0 + wn * (BN / WN) + n * 16 + (l >> 4) * 4;
-          if (f >= a.Fpad) continue;
-          const f32x4 g = *(const f32x4*)(a.g + row * a.Fpad + f);
-          const f32x4 u = *(const f32x4*)(a.u + row * a.Fpad + f);
-          float dg[4], du[4], hv[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float q = acc[m][n][j];
-            const float s = 1.0f / (1.0f + expf(-g[j]));
-            const float silu = g[j] * s, h = silu * u[j], dh = w * q;
-            dot += h * q;
+          for (int j = 0; j < 8; ++j) {
+            const float s = fast_sigmoid(g[j]);
+            const float silu = g[j] * s, h = silu * u[j], dh = w * v[j];
+            dot += h * v[j];
             dg[j] = dh * u[j] * s * (1.0f + g[j] * (1.0f - s));
             du[j] = dh * silu;
             hv[j] = w * h;
           }
-          store4(hw + row * a.Fpad + f, true, 4, hv);
-          T* o = dgu + row * a.ldc + f;
-          store4(o, vec, a.F - f, dg);
-          store4(o + a.F, vec, a.F - f, du);
+          const bool vec = a.F % 8 == 0;
+          T* o = (T*)a.c + row * a.ldc + x;
+          store8((T*)a.hw + row * a.Fpad + x, true, 8, hv);
+          store8(o, vec, a.F - x, dg);
+          store8(o + a.F, vec, a.F - x, du);
         }
-      }
-      dot += __shfl_xor(dot, 16);
-      dot += __shfl_xor(dot, 32);
-      const int part = n0 / (BN / WN) + wn;
-      if (l < 16 && r < rows && part < a.parts)
-        a.dval_part[(int64_t)(row0 + r) * a.parts + part] = dot;
-    }
-  } else {
-    T* c = (T*)a.c + expert * a.c_expert;
-    const bool vec = a.ldc % 4 == 0 && (uintptr_t)a.c % 8 == 0;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = m0 + wm * (BM / WM) + m * 16 + (l & 15);
-      if (r >= a.M) continue;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int x = n0 + wn * (BN / WN) + n * 16 + (l >> 4) * 4;
-        if (x >= a.N) continue;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = acc[m][n][j];
-        store4(c + (int64_t)r * a.ldc + x, vec, a.N - x, v);
+        for (int d = 1; d < kLanes; d <<= 1) dot += __shfl_xor(dot, d);
+        const int part = t.n0 / HN + wn;
+        if (lc == 0 && r < t.rows && part < a.parts)
+          a.dval_part[(int64_t)(t.row0 + r) * a.parts + part] = dot;
+      } else {
+        const int row = t.m0 + r;
+        if (row < a.M && x < a.N)
+          store8((T*)a.c + t.expert * a.c_expert + (int64_t)row * a.ldc + x,
+                 a.ldc % 8 == 0 && (uintptr_t)a.c % 16 == 0, a.N - x, v);
       }
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <typename T, int KIND, int BM, int BN, int WM, int WN>
+template <typename T, int KIND, int BM, int BN>
 void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
-  auto kernel = k_product<T, KIND, BM, BN, WM, WN>;
+  auto kernel = k_product<T, KIND, BM, BN>;
   static const bool once = (allow_max_dynamic_lds((const void*)kernel), true);
   (void)once;
   const int64_t step = KIND == kIn ? BN / 2 : BN;
   const int64_t tiles = row_tiles * ((a.N + step - 1) / step);
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid == 0) return;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(WM * WN * kWave),
-                     2 * (BM + BN) * kBK * 2, s, a);
+  typedef Stages<KIND, BM> S;
+  const size_t lds =
+      (S::kA * BM + S::kB * BN) * kBK * 2 + (S::kWGrad ? kListLen * sizeof(int32_t) : 0);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kNT), lds, s, a);
 }
 
 // ---- sums over a token's entries ----
@@ -635,7 +827,7 @@ struct BackwardWork {
   Padded pad;
 };
 
-int dval_parts(const Sizes& z) { return (int)((z.Fp + 63) / 64); }
+int dval_parts(const Sizes& z) { return (int)((z.Fp + 127) / 128); }
 
 BackwardWork take_backward(Carver& c, const Sizes& z, bool padded) {
   BackwardWork w{};
@@ -672,8 +864,8 @@ template <typename T, int KIND>
 void product_by_rows(const ProductArgs& a, const Sizes& z, hipStream_t s) {
   const int bm = tile_rows(z);
   const int64_t tiles = dispatch_max_tiles(z.n, z.E, bm);
-  if (bm == 256) launch_product<T, KIND, 256, 256, 2, 4>(a, tiles, s);
-  else launch_product<T, KIND, 128, 256, 2, 4>(a, tiles, s);
+  if (bm == 256) launch_product<T, KIND, 256, 256>(a, tiles, s);
+  else launch_product<T, KIND, 128, 256>(a, tiles, s);
 }
 
 ProductArgs base_args(const Sizes& z, const Dispatch& d) {
@@ -796,7 +988,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.c = dw_out;
   a.ldc = z.F;
   a.c_expert = z.D * z.F;
-  launch_product<T, kGradWOut, 256, 256, 2, 4>(a, z.E * ((z.D + 255) / 256), s);
+  launch_product<T, kGradWOut, 256, 256>(a, z.E * ((z.D + 255) / 256), s);
   a = base_args(z, kp.d);
   a.a = w.dgu;
   a.lda = z.S2;
@@ -809,7 +1001,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.c = dw_in;
   a.ldc = z.D;
   a.c_expert = 2 * z.F * z.D;
-  launch_product<T, kGradWIn, 256, 256, 2, 4>(a, z.E * ((2 * z.F + 255) / 256), s);
+  launch_product<T, kGradWIn, 256, 256>(a, z.E * ((2 * z.F + 255) / 256), s);
 }
 
 // ---- checks ----
@@ -828,7 +1020,10 @@ spgemm_status check_desc(const spgemm_experts_desc* d) {
                   "experts: tokens < 0, experts outside [1, 1024] or k outside [1, 64]");
   if (d->width < 1 || d->hidden < 1 || d->x_ld < d->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: empty width, or a row stride below it");
-  if (d->width > (1 << 24) || d->hidden > (1 << 24) ||
+  if (d->x_ld >= 1 << 30 || d->grad_ld >= 1 << 30)
+    return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "experts: a row stride of 2^30 elements or more");
+  if (d->width > (1 << 22) || d->hidden > (1 << 22) ||
+      2 * round8(d->hidden) * round8(d->width) >= (int64_t)1 << 31 ||
       d->tokens > INT32_MAX / d->k ||
       d->tokens * d->k / 128 + d->experts > INT32_MAX / ((d->width + d->hidden) / 128 + 1) / 2 ||
       d->experts * ((d->width + 255) / 256 + 1) * ((2 * d->hidden + 255) / 256 + 1) >
