@@ -85,6 +85,7 @@ struct Dispatch {
   int32_t* row_ptr;  // E + 1
   int32_t* ent;      // sorted position -> entry t * k + i
   int32_t* tok;      // sorted position -> token t
+  float* w;          // sorted position -> value, where values are given
   int32_t* pos;      // entry -> sorted position, -1 where there is none
   int32_t* tiles;    // (expert, first sorted position) of every row tile
   int32_t* ntiles;   // row tiles
@@ -92,7 +93,7 @@ struct Dispatch {
 
 int64_t dispatch_tmp_elems(int64_t n, int64_t E);
 int64_t dispatch_max_tiles(int64_t n, int64_t E, int tile_rows);
-void launch_dispatch(const int32_t* col, int64_t n, int k, int64_t E, int tile_rows,
+void launch_dispatch(const int32_t* col, const float* val, int64_t n, int k, int64_t E, int tile_rows,
                      const Dispatch& d, int32_t* tmp, hipStream_t s);
 
 }  // namespace sg

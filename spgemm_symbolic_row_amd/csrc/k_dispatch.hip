@@ -38,7 +38,7 @@ __device__ __forceinline__ void count_waves(const int32_t* col, int64_t n, int E
 
 // Places the work group's entries.  wc holds each wave's first position per
 // expert and is advanced.
-__device__ __forceinline__ void place(const int32_t* col, int64_t n, int k, int E, int bits,
+__device__ __forceinline__ void place(const int32_t* col, const float* val, int64_t n, int k, int E, int bits,
                                       int64_t e0, int32_t* wc, const Dispatch& d) {
   const int w = threadIdx.x / kWave;
   int32_t* my = wc + w * E;
@@ -55,6 +55,7 @@ __device__ __forceinline__ void place(const int32_t* col, int64_t n, int k, int 
       if (lane_id() == last_set64(peers)) my[c] = p + 1;
       d.ent[p] = (int32_t)e;
       d.tok[p] = (int32_t)(e / k);
+      if (val) d.w[p] = val[e];
     }
     if (e < n) d.pos[e] = p;
   }
@@ -87,7 +88,7 @@ __device__ __forceinline__ void scan_experts(int E, int tile_rows, const int32_t
 }
 
 __global__ __launch_bounds__(kDispNT) void k_dispatch_one(const int32_t* __restrict__ col,
-                                                          int64_t n, int k, int E, int bits,
+                                                          const float* __restrict__ val, int64_t n, int k, int E, int bits,
                                                           int tile_rows, Dispatch d) {
   extern __shared__ int32_t lds[];
   int32_t* wc = lds;                  // kDispNW * E
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_one(const int32_t* __restr
     }
   }
   __syncthreads();
-  place(col, n, k, E, bits, 0, wc, d);
+  place(col, val, n, k, E, bits, 0, wc, d);
 }
 
 // hist[b * E + x]: entries of expert x in work group b's range.
@@ -154,6 +155,7 @@ __global__ __launch_bounds__(1024) void k_dispatch_scan(int64_t nb, int E, int t
 }
 
 __global__ __launch_bounds__(kDispNT) void k_dispatch_place(const int32_t* __restrict__ col,
+                                                            const float* __restrict__ val,
                                                             int64_t n, int k, int E, int bits,
                                                             const int32_t* __restrict__ hist,
                                                             Dispatch d) {
@@ -169,7 +171,7 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_place(const int32_t* __res
     }
   }
   __syncthreads();
-  place(col, n, k, E, bits, e0, wc, d);
+  place(col, val, n, k, E, bits, e0, wc, d);
 }
 
 }  // namespace
@@ -182,7 +184,7 @@ int64_t dispatch_max_tiles(int64_t n, int64_t E, int tile_rows) {
   return n / tile_rows + std::min(n, E);
 }
 
-void launch_dispatch(const int32_t* col, int64_t n, int k, int64_t E, int tile_rows,
+void launch_dispatch(const int32_t* col, const float* val, int64_t n, int k, int64_t E, int tile_rows,
                      const Dispatch& d, int32_t* tmp, hipStream_t s) {
   int bits = 0;
   while (((int64_t)1 << bits) < E) ++bits;
@@ -190,13 +192,13 @@ void launch_dispatch(const int32_t* col, int64_t n, int k, int64_t E, int tile_r
   const size_t wcb = (size_t)kDispNW * E * sizeof(int32_t);
   if (nb <= 1) {
     hipLaunchKernelGGL(k_dispatch_one, dim3(1), dim3(kDispNT), wcb + 2 * E * sizeof(int32_t), s,
-                       col, n, k, (int)E, bits, tile_rows, d);
+                       col, val, n, k, (int)E, bits, tile_rows, d);
     return;
   }
   hipLaunchKernelGGL(k_dispatch_count, dim3((unsigned)nb), dim3(kDispNT), wcb, s, col, n, (int)E,
                      tmp);
   hipLaunchKernelGGL(k_dispatch_scan, dim3(1), dim3(1024), 0, s, nb, (int)E, tile_rows, tmp, d);
-  hipLaunchKernelGGL(k_dispatch_place, dim3((unsigned)nb), dim3(kDispNT), wcb, s, col, n, k,
+  hipLaunchKernelGGL(k_dispatch_place, dim3((unsigned)nb), dim3(kDispNT), wcb, s, col, val, n, k,
                      (int)E, bits, (const int32_t*)tmp, d);
 }
 
@@ -253,7 +255,7 @@ extern "C" spgemm_status spgemm_dispatch(int64_t T, int32_t k, int64_t E, const 
   d.pos = w.pos;
   d.tiles = w.tiles;
   d.ntiles = w.ntiles;
-  launch_dispatch(dCol, n, k, E, 256, d, w.tmp, (hipStream_t)stream);
+  launch_dispatch(dCol, nullptr, n, k, E, 256, d, w.tmp, (hipStream_t)stream);
   const hipError_t e = hipGetLastError();
   if (e == hipSuccess) return SPGEMM_OK;
   set_thread_error(hipGetErrorString(e));

@@ -106,16 +106,10 @@ __device__ __forceinline__ void wait_slice() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-// 1 / (1 + exp(-g)) to about 2 ulp: exp by the native base-2 exponential, with
-// the rounding of its argument put back; the clamp keeps the argument finite.
+// 1 / (1 + exp(-g)) by the native base-2 exponential and reciprocal: within
+// (2 + |g|) 2^-24 of its value.  The exponential overflows where the result is 0.
 __device__ __forceinline__ float fast_sigmoid(float g) {
-  constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-  const float x = fminf(fmaxf(-g, -87.0f), 87.0f);
-  const float t = x * kLog2e;
-  const float r = fmaf(x, kLog2e, -t);
-  float e = __builtin_amdgcn_exp2f(t);
-  e = fmaf(e, r * kLn2, e);
-  return __builtin_amdgcn_rcpf(1.0f + e);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g));
 }
 
 static __device__ __align__(16) const uint32_t zeros16[4] = {0, 0, 0, 0};
@@ -207,7 +201,6 @@ struct ProductArgs {
   float* g;          // fp32 pre-activations, Fpad to a row
   float* u;
   void* hw;          // w h
-  const float* val;
   float* dval_part;  // per entry: one partial sum of each 128 columns
   int parts;
 };
@@ -291,7 +284,9 @@ struct Stages {
   static constexpr int kA = kWGrad ? 2 : 3, kB = !kWGrad && BM < 256 ? 3 : 2;
 };
 
-template <typename T, int KIND, int BM, int BN>
+// kFar: the gathered rows span 4 GB or more, so that their offsets are 64-bit
+// pointers; those cost 7% of the main loop.
+template <typename T, int KIND, int BM, int BN, bool kFar>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product(
     ProductArgs a) {
   constexpr int HM = BM / 2, HN = BN / 2, MT = HM / 32, NT = HN / 32;
@@ -358,10 +353,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
       const int r = min(ar.row(i), t.rows - 1);
-      if constexpr (kAGather)
-        aptr[i] = (const char*)(abase + (int64_t)a.d.tok[t.row0 + r] * a.lda + ar.k());
-      else
-        aoff[i] = ((uint32_t)r * (uint32_t)a.lda + ar.k()) * 2;
+      const uint32_t at = kAGather ? a.d.tok[t.row0 + r] : r;
+      if constexpr (kFar) aptr[i] = (const char*)(abase + (int64_t)at * a.lda + ar.k());
+      else aoff[i] = (at * (uint32_t)a.lda + ar.k()) * 2;
     }
     ar.frag_init(wm * HM);
   } else {
@@ -401,7 +395,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   // Address of load i of slice s.
   auto addr_a = [&](int s, int i) -> const char* {
     if constexpr (kWGrad && kAGather) return (const char*)abase + (uint64_t)aidx[i] * ((uint32_t)a.lda * 2) + acol;
-    else if constexpr (kAGather) return aptr[i];
+    else if constexpr (kFar) return aptr[i];
     else return (const char*)abase + aoff[i];
   };
   auto addr_b = [&](int s, int i) -> const char* {
@@ -418,11 +412,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   auto next_a = [&]() {
     if constexpr (kACol) {
       if constexpr (!kAGather) abase += (int64_t)kBK * a.lda;
-    } else if constexpr (kAGather) {
-#pragma unroll
-      for (int i = 0; i < AL; ++i) aptr[i] += kBK * 2;
-    } else {
-      abase += kBK;
+    } else if constexpr (!kFar) {
+      abase += kBK;  // far pointers move as they are used
     }
   };
   auto next_b = [&]() {
@@ -484,6 +475,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       for (int i = 0; i < BL; ++i)
         load_to_lds(stage_b(s) + (i * kWaves + wave) * 1024,
                     inside_b(s, i) ? (const void*)addr_b(s, i) : (const void*)zeros16);
+      if constexpr (kFar) {
+#pragma unroll
+        for (int i = 0; i < AL; ++i) aptr[i] += kBK * 2;
+      }
       next_a();
       next_b();
     }
@@ -527,13 +522,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                                : (inside_b(s + 2, y) ? addr_b(s + 2, y) : (const char*)zeros16);
             mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
                                          p);
-          } else if constexpr (kA ? kAGather : kBGather) {
+          } else if constexpr (kA ? kFar || (kACol && kAGather) : kBGather) {
             mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
                                          kA ? addr_a(s + 2, y) : addr_b(s + 2, y));
           } else {
             mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
                                          kA ? abase : bbase, kA ? aoff[y] : boff[y]);
           }
+          if constexpr (kA && kFar) aptr[y] += kBK * 2;
         } else {
           mfma(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n]);
         }
@@ -577,11 +573,17 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   // twice the time.
   // acc[m][n][4 g + j]: row wm*HM + 32 m + l % 32, column wn*HN + 32 n + 8 g +
   // l / 32 * 4 + j.
-  wait_slice<0>();
   constexpr int kPitch = HN + 4;
+  constexpr int kCols = KIND == kIn ? HN / 2 : HN;      // of the wave's part of the result
+  constexpr int kLanes = kCols / 8, R = kWave / kLanes;  // 8 columns to a lane, R rows at once
+  constexpr int kPass = 32 / R;
   float* stg = (float*)smem + wave * 32 * kPitch;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  const int lr = l / kLanes, lc = l % kLanes * 8;
+  const int x = t.n0 + wn * kCols + lc;
+  auto row_of = [&](int m, int p) { return wm * HM + m * 32 + p * R + lr; };
+  auto stage_block = [&](auto block) {
+    constexpr int m = decltype(block)::value;
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -592,77 +594,110 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         *(f32x4*)(stg + (l & 31) * kPitch + n * 32 + q * 8 + (l >> 5) * 4) = v;
       }
     __builtin_amdgcn_wave_barrier();
-    // 8 columns to a lane, R rows at once.
-    constexpr int kCols = KIND == kIn ? HN / 2 : HN, kLanes = kCols / 8, R = kWave / kLanes;
-    const int lr = l / kLanes, lc = l % kLanes * 8;
-    const int x = t.n0 + wn * kCols + lc;
-#pragma unroll(KIND == kGradH ? 4 : 2)
-    for (int p = 0; p < 32 / R; ++p) {
-      const int rr = p * R + lr, r = wm * HM + m * 32 + rr;
-      const float* src = stg + rr * kPitch + lc;
-      float v[8];
+  };
+  if constexpr (KIND == kGradH) {
+    // g, u and w of the next 4 passes are loaded while these 4 are worked on:
+    // one wave to a SIMD hides no latency otherwise.
+    constexpr int kUnit = 4, kUnits = MT * kPass / kUnit;
+    float g[2][kUnit][8], u[2][kUnit][8], w[2][kUnit];
+    const int xc = min(x, a.Fpad - 8);
+    auto fetch = [&](int unit, int buf) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = src[j];
-      if constexpr (KIND == kIn) {
-        if (r >= t.rows || x >= a.Fpad) continue;
-        float u[8], h[8];
+      for (int i = 0; i < kUnit; ++i) {
+        const int p = unit * kUnit + i;
+        const int64_t row = t.row0 + min(row_of(p / kPass, p % kPass), t.rows - 1);
+        load8(a.g + row * a.Fpad + xc, g[buf][i]);
+        load8(a.u + row * a.Fpad + xc, u[buf][i]);
+        w[buf][i] = a.d.w[row];
+      }
+    };
+    fetch(0, 0);
+    wait_slice<63>();
+    auto unit = [&](auto index) {
+      constexpr int c = decltype(index)::value, buf = c % 2, m = c * kUnit / kPass;
+      if constexpr (c + 1 < kUnits) fetch(c + 1, 1 - buf);
+      if constexpr (c * kUnit % kPass == 0) stage_block(std::integral_constant<int, m>{});
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) {
+        const int p = c * kUnit % kPass + i, r = row_of(m, p);
+        const bool inside = r < t.rows && x < a.Fpad;
+        float v[8], dg[8], du[8], hv[8], dot = 0.0f;
+        load8(stg + (p * R + lr) * kPitch + lc, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          u[j] = src[kCols + j];
-          if (x + j >= a.F) v[j] = u[j] = 0.0f;
-          h[j] = v[j] * fast_sigmoid(v[j]) * u[j];
+          const float gj = g[buf][i][j], uj = u[buf][i][j], ww = w[buf][i];
+          const float s = fast_sigmoid(gj);
+          const float silu = gj * s, h = silu * uj, dh = ww * v[j];
+          dot += h * v[j];
+          dg[j] = dh * uj * s * (1.0f + gj * (1.0f - s));
+          du[j] = dh * silu;
+          hv[j] = ww * h;
         }
-        const int64_t at = (int64_t)(t.row0 + r) * a.Fpad + x;
-        store8((T*)a.c + at, true, 8, h);
-        if (a.g) {
-          store8(a.g + at, true, 8, v);
-          store8(a.u + at, true, 8, u);
-        }
-      } else if constexpr (KIND == kOut || KIND == kGradX) {
-        if (r < t.rows && x < a.ldc)
-          store8((float*)a.c + (int64_t)(t.row0 + r) * a.ldc + x, true, 8, v);
-      } else if constexpr (KIND == kGradH) {
-        float dot = 0.0f;
-        if (r < t.rows && x < a.Fpad) {
+        if (inside) {
           const int64_t row = t.row0 + r;
-          const float w = a.val[a.d.ent[row]];
-          float g[8], u[8], dg[8], du[8], hv[8];
-          load8(a.g + row * a.Fpad + x, g);
-          load8(a.u + row * a.Fpad + x, u);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float s = fast_sigmoid(g[j]);
-            const float silu = g[j] * s, h = silu * u[j], dh = w * v[j];
-            dot += h * v[j];
-            dg[j] = dh * u[j] * s * (1.0f + g[j] * (1.0f - s));
-            du[j] = dh * silu;
-            hv[j] = w * h;
-          }
           const bool vec = a.F % 8 == 0;
           T* o = (T*)a.c + row * a.ldc + x;
           store8((T*)a.hw + row * a.Fpad + x, true, 8, hv);
           store8(o, vec, a.F - x, dg);
           store8(o + a.F, vec, a.F - x, du);
+        } else {
+          dot = 0.0f;
         }
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1) dot += __shfl_xor(dot, d);
         const int part = t.n0 / HN + wn;
         if (lc == 0 && r < t.rows && part < a.parts)
           a.dval_part[(int64_t)(t.row0 + r) * a.parts + part] = dot;
-      } else {
-        const int row = t.m0 + r;
-        if (row < a.M && x < a.N)
-          store8((T*)a.c + t.expert * a.c_expert + (int64_t)row * a.ldc + x,
-                 a.ldc % 8 == 0 && (uintptr_t)a.c % 16 == 0, a.N - x, v);
       }
-    }
-    __builtin_amdgcn_wave_barrier();
+    };
+    for_each_index<kUnits>(unit);
+  } else {
+    wait_slice<0>();
+    auto block = [&](auto index) {
+      constexpr int m = decltype(index)::value;
+      stage_block(index);
+#pragma unroll
+      for (int p = 0; p < kPass; ++p) {
+        const int r = row_of(m, p);
+        const float* src = stg + (p * R + lr) * kPitch + lc;
+        float v[8];
+        load8(src, v);
+        if constexpr (KIND == kIn) {
+          float u[8], h[8];
+          load8(src + kCols, u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[j] = v[j] * fast_sigmoid(v[j]) * u[j];
+          if (x + 8 > a.F) {  // columns that fill a row up hold zeros
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (x + j >= a.F) v[j] = u[j] = h[j] = 0.0f;
+          }
+          if (r < t.rows && x < a.Fpad) {
+            const int64_t at = (int64_t)(t.row0 + r) * a.Fpad + x;
+            store8((T*)a.c + at, true, 8, h);
+            if (a.g) {
+              store8(a.g + at, true, 8, v);
+              store8(a.u + at, true, 8, u);
+            }
+          }
+        } else if constexpr (KIND == kOut || KIND == kGradX) {
+          if (r < t.rows && x < a.ldc)
+            store8((float*)a.c + (int64_t)(t.row0 + r) * a.ldc + x, true, 8, v);
+        } else {
+          const int row = t.m0 + r;
+          if (row < a.M && x < a.N)
+            store8((T*)a.c + t.expert * a.c_expert + (int64_t)row * a.ldc + x,
+                   a.ldc % 8 == 0 && (uintptr_t)a.c % 16 == 0, a.N - x, v);
+        }
+      }
+    };
+    for_each_index<MT>(block);
   }
 }
 
-template <typename T, int KIND, int BM, int BN>
+template <typename T, int KIND, int BM, int BN, bool kFar = false>
 void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
-  auto kernel = k_product<T, KIND, BM, BN>;
+  auto kernel = k_product<T, KIND, BM, BN, kFar>;
   static const bool once = (allow_max_dynamic_lds((const void*)kernel), true);
   (void)once;
   const int64_t step = KIND == kIn ? BN / 2 : BN;
@@ -774,6 +809,7 @@ void take_dispatch(Carver& c, const Sizes& z, Dispatch& d) {
   d.row_ptr = c.take<int32_t>(z.E + 1);
   d.ent = c.take<int32_t>(z.n);
   d.tok = c.take<int32_t>(z.n);
+  d.w = c.take<float>(z.n);
   d.pos = c.take<int32_t>(z.n);
   d.tiles = c.take<int32_t>(2 * dispatch_max_tiles(z.n, z.E, tile_rows(z)));
   d.ntiles = c.take<int32_t>(1);
@@ -864,6 +900,13 @@ template <typename T, int KIND>
 void product_by_rows(const ProductArgs& a, const Sizes& z, hipStream_t s) {
   const int bm = tile_rows(z);
   const int64_t tiles = dispatch_max_tiles(z.n, z.E, bm);
+  if constexpr (KIND == kIn || KIND == kGradH) {
+    if (z.T * a.lda >= (int64_t)1 << 31) {
+      if (bm == 256) launch_product<T, KIND, 256, 256, true>(a, tiles, s);
+      else launch_product<T, KIND, 128, 256, true>(a, tiles, s);
+      return;
+    }
+  }
   if (bm == 256) launch_product<T, KIND, 256, 256>(a, tiles, s);
   else launch_product<T, KIND, 128, 256>(a, tiles, s);
 }
@@ -897,7 +940,7 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   } else {
     kp.d = w.d;
   }
-  launch_dispatch(col, z.n, z.k, z.E, tile_rows(z), kp.d, w.tmp, s);
+  launch_dispatch(col, val, z.n, z.k, z.E, tile_rows(z), kp.d, w.tmp, s);
   const Rows xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
   const Rows w1 = padded_rows(w_in, z.D, z.E * 2 * z.F, z.D, w.pad.w_in, s);
   const Rows w2 = padded_rows(w_out, z.F, z.E * z.D, z.F, w.pad.w_out, s);
@@ -931,7 +974,7 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
 
 template <typename T>
 void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
-              const void* w_out, const float* val, const void* dy, const void* kept, void* dx,
+              const void* w_out, const void* dy, const void* kept, void* dx,
               void* dw_in, void* dw_out, float* dval, const BackwardWork& w, hipStream_t s) {
   const Sizes z = sizes_of(desc);
   Carver kc((void*)kept);
@@ -956,7 +999,6 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.g = kp.g;
   a.u = kp.u;
   a.hw = w.hw;
-  a.val = val;
   a.dval_part = w.part;
   a.parts = dval_parts(z);
   product_by_rows<T, kGradH>(a, z, s);
@@ -1117,10 +1159,10 @@ extern "C" spgemm_status spgemm_experts_backward(
   const BackwardWork w = take_backward(c, z, needs_padding(*desc, dX, dWIn, dWOut, dGradY));
   if (work_bytes < c.used) return refuse(SPGEMM_ERR_INVALID_ARG, "experts: workspace too small");
   if (desc->dtype == SPGEMM_BF16)
-    backward<__bf16>(*desc, dX, dWIn, dWOut, dVal, dGradY, dKept, dGradX, dGradWIn, dGradWOut,
+    backward<__bf16>(*desc, dX, dWIn, dWOut, dGradY, dKept, dGradX, dGradWIn, dGradWOut,
                      dGradVal, w, s);
   else
-    backward<_Float16>(*desc, dX, dWIn, dWOut, dVal, dGradY, dKept, dGradX, dGradWIn, dGradWOut,
+    backward<_Float16>(*desc, dX, dWIn, dWOut, dGradY, dKept, dGradX, dGradWIn, dGradWOut,
                        dGradVal, w, s);
   return launched();
 }
