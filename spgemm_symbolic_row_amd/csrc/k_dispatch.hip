@@ -12,38 +12,48 @@
 namespace sg {
 namespace {
 
-constexpr int kDispNT = 256;
+constexpr int kDispNT = 1024;
 constexpr int kDispNW = kDispNT / kWave;
-constexpr int kDispBlock = 4096;                 // entries of one work group
-constexpr int kDispWave = kDispBlock / kDispNW;  // consecutive entries of one wave
+constexpr int kDispBlock = 4096;  // entries of one work group
 
 __device__ __forceinline__ int expert_of(const int32_t* col, int64_t e, int64_t n, int E) {
   const int c = e < n ? col[e] : -1;
   return (uint32_t)c < (uint32_t)E ? c : -1;
 }
 
-// Entries per expert of each wave's range: wc[w * E + x].
+// Entries per expert of each wave's range of `len` entries: wc[w * E + x].
 __device__ __forceinline__ void count_waves(const int32_t* col, int64_t n, int E, int64_t e0,
-                                            int32_t* wc) {
+                                            int len, int32_t* wc) {
   for (int i = threadIdx.x; i < kDispNW * E; i += kDispNT) wc[i] = 0;
   __syncthreads();
   const int w = threadIdx.x / kWave;
-  const int64_t first = e0 + (int64_t)w * kDispWave;
-  for (int i = lane_id(); i < kDispWave && first + i < n; i += kWave) {
+  const int64_t first = e0 + (int64_t)w * len;
+  for (int i = lane_id(); i < len && first + i < n; i += kWave) {
     const int c = expert_of(col, first + i, n, E);
     if (c >= 0) atomicAdd(&wc[w * E + c], 1);
   }
   __syncthreads();
 }
 
+// Turns each wave's counts of expert x into its first positions, from `at`.
+__device__ __forceinline__ void count_to_start(int E, int x, int at, int32_t* wc) {
+#pragma unroll
+  for (int w = 0; w < kDispNW; ++w) {
+    const int c = wc[w * E + x];
+    wc[w * E + x] = at;
+    at += c;
+  }
+}
+
 // Places the work group's entries.  wc holds each wave's first position per
 // expert and is advanced.
-__device__ __forceinline__ void place(const int32_t* col, const float* val, int64_t n, int k, int E, int bits,
-                                      int64_t e0, int32_t* wc, const Dispatch& d) {
+__device__ __forceinline__ void place(const int32_t* col, const float* val, int64_t n, int k,
+                                      int E, int bits, int64_t e0, int len, int32_t* wc,
+                                      const Dispatch& d) {
   const int w = threadIdx.x / kWave;
   int32_t* my = wc + w * E;
-  const int64_t first = e0 + (int64_t)w * kDispWave;
-  for (int i = 0; i < kDispWave && first + i < n; i += kWave) {
+  const int64_t first = e0 + (int64_t)w * len;
+  for (int i = 0; i < len && first + i < n; i += kWave) {
     const int64_t e = first + i + lane_id();
     const int c = expert_of(col, e, n, E);
     const uint64_t peers = match_key((uint32_t)c, bits, c >= 0);
@@ -54,104 +64,92 @@ __device__ __forceinline__ void place(const int32_t* col, const float* val, int6
       p = my[c] + (int)__popcll(peers & lanemask_lt());
       if (lane_id() == last_set64(peers)) my[c] = p + 1;
       d.ent[p] = (int32_t)e;
-      d.tok[p] = (int32_t)(e / k);
+      d.tok[p] = (int32_t)((uint32_t)e / (uint32_t)k);
       if (val) d.w[p] = val[e];
     }
     if (e < n) d.pos[e] = p;
   }
 }
 
-// Exclusive scan over the experts of their totals and of their row tiles by
-// the first wave; every lane takes consecutive experts.
-__device__ __forceinline__ void scan_experts(int E, int tile_rows, const int32_t* total,
-                                             int32_t* start, const Dispatch& d) {
-  const int per = (E + kWave - 1) / kWave;
-  const int a = min(E, lane_id() * per), b = min(E, a + per);
-  int rows = 0, tiles = 0;
-  for (int x = a; x < b; ++x) {
-    rows += total[x];
-    tiles += (total[x] + tile_rows - 1) / tile_rows;
+// First position of expert x = threadIdx.x (< E) from its total: an exclusive
+// scan over the work group of the totals and of the experts' row tiles.
+// Writes the row pointers and the tiles.
+__device__ __forceinline__ int scan_experts(int E, int tile_rows, int total, const Dispatch& d) {
+  __shared__ int64_t wave_total[kDispNW];
+  const int x = threadIdx.x, w = x / kWave;
+  const int tiles = (total + tile_rows - 1) / tile_rows;
+  const int64_t own = (int64_t)tiles << 32 | (uint32_t)total;  // no total reaches 2^31
+  const int64_t incl = wave_incl_scan(own);
+  if (lane_id() == kWave - 1) wave_total[w] = incl;
+  __syncthreads();
+  int64_t before = incl - own;
+  for (int i = 0; i < w; ++i) before += wave_total[i];
+  const int start = (int)(uint32_t)before;
+  int t = (int)(before >> 32);
+  if (x < E) d.row_ptr[x] = start;
+  for (int i = 0; i < total; i += tile_rows, ++t) {
+    d.tiles[2 * t] = x;
+    d.tiles[2 * t + 1] = start + i;
   }
-  int r = wave_incl_scan(rows) - rows, t = wave_incl_scan(tiles) - tiles;
-  for (int x = a; x < b; ++x) {
-    d.row_ptr[x] = start[x] = r;
-    for (int i = 0; i < total[x]; i += tile_rows, ++t) {
-      d.tiles[2 * t] = x;
-      d.tiles[2 * t + 1] = r + i;
-    }
-    r += total[x];
-  }
-  if (lane_id() == kWave - 1) {
-    d.row_ptr[E] = r;
+  if (x == E - 1) {
+    d.row_ptr[E] = start + total;
     *d.ntiles = t;
   }
+  return start;
 }
 
 __global__ __launch_bounds__(kDispNT) void k_dispatch_one(const int32_t* __restrict__ col,
-                                                          const float* __restrict__ val, int64_t n, int k, int E, int bits,
-                                                          int tile_rows, Dispatch d) {
-  extern __shared__ int32_t lds[];
-  int32_t* wc = lds;                  // kDispNW * E
-  int32_t* total = wc + kDispNW * E;  // E
-  int32_t* start = total + E;         // E
-  count_waves(col, n, E, 0, wc);
-  for (int x = threadIdx.x; x < E; x += kDispNT) {
-    int sum = 0;
-    for (int w = 0; w < kDispNW; ++w) sum += wc[w * E + x];
-    total[x] = sum;
-  }
+                                                          const float* __restrict__ val,
+                                                          int64_t n, int k, int E, int bits,
+                                                          int len, int tile_rows, Dispatch d) {
+  extern __shared__ int32_t wc[];  // kDispNW * E
+  count_waves(col, n, E, 0, len, wc);
+  const int x = threadIdx.x;
+  int total = 0;
+  if (x < E)
+#pragma unroll
+    for (int w = 0; w < kDispNW; ++w) total += wc[w * E + x];
+  const int start = scan_experts(E, tile_rows, total, d);
+  if (x < E) count_to_start(E, x, start, wc);
   __syncthreads();
-  if (threadIdx.x < kWave) scan_experts(E, tile_rows, total, start, d);
-  __syncthreads();
-  for (int x = threadIdx.x; x < E; x += kDispNT) {
-    int at = start[x];
-    for (int w = 0; w < kDispNW; ++w) {
-      const int c = wc[w * E + x];
-      wc[w * E + x] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
-  place(col, val, n, k, E, bits, 0, wc, d);
+  place(col, val, n, k, E, bits, 0, len, wc, d);
 }
 
 // hist[b * E + x]: entries of expert x in work group b's range.
 __global__ __launch_bounds__(kDispNT) void k_dispatch_count(const int32_t* __restrict__ col,
                                                             int64_t n, int E,
                                                             int32_t* __restrict__ hist) {
-  extern __shared__ int32_t lds[];
-  count_waves(col, n, E, (int64_t)blockIdx.x * kDispBlock, lds);
-  for (int x = threadIdx.x; x < E; x += kDispNT) {
-    int sum = 0;
-    for (int w = 0; w < kDispNW; ++w) sum += lds[w * E + x];
-    hist[(int64_t)blockIdx.x * E + x] = sum;
+  extern __shared__ int32_t h[];  // E
+  for (int i = threadIdx.x; i < E; i += kDispNT) h[i] = 0;
+  __syncthreads();
+  const int64_t e0 = (int64_t)blockIdx.x * kDispBlock;
+#pragma unroll
+  for (int i = 0; i < kDispBlock; i += kDispNT) {
+    const int c = expert_of(col, e0 + i + threadIdx.x, n, E);
+    if (c >= 0) atomicAdd(&h[c], 1);
   }
+  __syncthreads();
+  for (int x = threadIdx.x; x < E; x += kDispNT) hist[(int64_t)blockIdx.x * E + x] = h[x];
 }
 
 // Turns hist into every range's first position per expert, and writes the row
 // pointers and the tiles.  One work group; thread x walks expert x's column.
-__global__ __launch_bounds__(1024) void k_dispatch_scan(int64_t nb, int E, int tile_rows,
-                                                        int32_t* __restrict__ hist, Dispatch d) {
-  __shared__ int32_t total[kMaxExperts], start[kMaxExperts];
+__global__ __launch_bounds__(kDispNT) void k_dispatch_scan(int64_t nb, int E, int tile_rows,
+                                                           int32_t* __restrict__ hist,
+                                                           Dispatch d) {
   const int x = threadIdx.x;
-  if (x < E) {
-    int sum = 0;
+  int total = 0;
+  if (x < E)
 #pragma unroll 8
-    for (int64_t b = 0; b < nb; ++b) sum += hist[b * E + x];
-    total[x] = sum;
-  }
-  __syncthreads();
-  if (threadIdx.x < kWave) scan_experts(E, tile_rows, total, start, d);
-  __syncthreads();
-  if (x < E) {
-    int at = start[x];
+    for (int64_t b = 0; b < nb; ++b) total += hist[b * E + x];
+  int at = scan_experts(E, tile_rows, total, d);
+  if (x < E)
 #pragma unroll 8
     for (int64_t b = 0; b < nb; ++b) {
       const int c = hist[b * E + x];
       hist[b * E + x] = at;
       at += c;
     }
-  }
 }
 
 __global__ __launch_bounds__(kDispNT) void k_dispatch_place(const int32_t* __restrict__ col,
@@ -160,18 +158,13 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_place(const int32_t* __res
                                                             const int32_t* __restrict__ hist,
                                                             Dispatch d) {
   extern __shared__ int32_t wc[];
+  constexpr int kLen = kDispBlock / kDispNW;
   const int64_t e0 = (int64_t)blockIdx.x * kDispBlock;
-  count_waves(col, n, E, e0, wc);
-  for (int x = threadIdx.x; x < E; x += kDispNT) {
-    int at = hist[(int64_t)blockIdx.x * E + x];
-    for (int w = 0; w < kDispNW; ++w) {
-      const int c = wc[w * E + x];
-      wc[w * E + x] = at;
-      at += c;
-    }
-  }
+  count_waves(col, n, E, e0, kLen, wc);
+  for (int x = threadIdx.x; x < E; x += kDispNT)
+    count_to_start(E, x, hist[(int64_t)blockIdx.x * E + x], wc);
   __syncthreads();
-  place(col, val, n, k, E, bits, e0, wc, d);
+  place(col, val, n, k, E, bits, e0, kLen, wc, d);
 }
 
 }  // namespace
@@ -191,13 +184,14 @@ void launch_dispatch(const int32_t* col, const float* val, int64_t n, int k, int
   const int64_t nb = (n + kDispBlock - 1) / kDispBlock;
   const size_t wcb = (size_t)kDispNW * E * sizeof(int32_t);
   if (nb <= 1) {
-    hipLaunchKernelGGL(k_dispatch_one, dim3(1), dim3(kDispNT), wcb + 2 * E * sizeof(int32_t), s,
-                       col, val, n, k, (int)E, bits, tile_rows, d);
+    const int len = (int)((n + kDispNT - 1) / kDispNT) * kWave;  // whole rounds of a wave
+    hipLaunchKernelGGL(k_dispatch_one, dim3(1), dim3(kDispNT), wcb, s, col, val, n, k, (int)E,
+                       bits, len, tile_rows, d);
     return;
   }
-  hipLaunchKernelGGL(k_dispatch_count, dim3((unsigned)nb), dim3(kDispNT), wcb, s, col, n, (int)E,
-                     tmp);
-  hipLaunchKernelGGL(k_dispatch_scan, dim3(1), dim3(1024), 0, s, nb, (int)E, tile_rows, tmp, d);
+  hipLaunchKernelGGL(k_dispatch_count, dim3((unsigned)nb), dim3(kDispNT), E * sizeof(int32_t), s,
+                     col, n, (int)E, tmp);
+  hipLaunchKernelGGL(k_dispatch_scan, dim3(1), dim3(kDispNT), 0, s, nb, (int)E, tile_rows, tmp, d);
   hipLaunchKernelGGL(k_dispatch_place, dim3((unsigned)nb), dim3(kDispNT), wcb, s, col, val, n, k,
                      (int)E, bits, (const int32_t*)tmp, d);
 }

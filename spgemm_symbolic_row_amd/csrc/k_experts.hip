@@ -203,7 +203,12 @@ struct ProductArgs {
   void* hw;          // w h
   float* dval_part;  // per entry: one partial sum of each 128 columns
   int parts;
+  int k;               // slots of a row of the routing matrix
+  const int32_t* col;  // and its entries, where they are taken unsorted
+  const float* val;
 };
+
+constexpr int kFewRows = 16;  // rows of a tile of the few-rows products
 
 // 8 values to p at once where it is aligned to them (vec) and n >= 8; else the
 // first n one by one.
@@ -710,6 +715,200 @@ void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kNT), lds, s, a);
 }
 
+// ---- few rows: products that stream the weights ----
+// With a few rows to an expert every weight is used once and its bytes bound
+// the product.  A wave takes 16 weight rows straight from memory to registers
+// (16x16x32 MFMA, the weights as the left operand, up to 16 rows of x as the
+// right one), 8 loads in flight, and the waves of a work group share K, so that
+// many small work groups keep the memory busy.
+
+__device__ __forceinline__ f32x4 mfma16(__bf16, s16x8 a, s16x8 b, f32x4 c) {
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a),
+                                                 __builtin_bit_cast(v8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma16(_Float16, s16x8 a, s16x8 b, f32x4 c) {
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a),
+                                                __builtin_bit_cast(v8, b), c, 0, 0, 0);
+}
+
+// Rows of a few-rows tile: of its own entry where entries are not sorted (a
+// tile is an entry, in their order), else of the sorted list.
+struct FewTile {
+  int expert, row0, rows;
+};
+template <bool kDirect>
+__device__ __forceinline__ bool few_tile(const ProductArgs& a, int tile, FewTile& t) {
+  if constexpr (kDirect) {
+    t.expert = a.col[tile];
+    t.row0 = tile;
+    t.rows = 1;
+    return (uint32_t)t.expert < (uint32_t)a.E;
+  } else {
+    if (tile >= *a.d.ntiles) return false;
+    t.expert = a.d.tiles[2 * tile];
+    t.row0 = a.d.tiles[2 * tile + 1];
+    t.rows = min(kFewRows, a.d.row_ptr[t.expert + 1] - t.row0);
+    return true;
+  }
+}
+
+// The lane's share of K step s: 8 values of its row from k = 32 s + l / 16 * 8,
+// zeros beyond K.
+__device__ __forceinline__ s16x8 few_load(const void* row, int s, int K) {
+  const int k = s * 32 + (lane_id() >> 4) * 8;
+  s16x8 v = *(const s16x8*)((const char*)row + (k < K ? k : 0) * 2);
+  if (k >= K) v = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+  return v;
+}
+
+constexpr int kFewBatch = 8;
+
+// acc[o] += W rows of operand o times x rows, K steps first, first + step, ..
+template <typename T, int kOps>
+__device__ __forceinline__ void few_products(const void* const (&w)[kOps], const void* x,
+                                             int first, int step, int steps, int K,
+                                             f32x4 (&acc)[kOps]) {
+  for (int s = first; s < steps; s += step * kFewBatch) {
+    s16x8 wf[kFewBatch][kOps], xf[kFewBatch];
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      const int at = s + i * step;
+      if (at >= steps) break;
+#pragma unroll
+      for (int o = 0; o < kOps; ++o) wf[i][o] = few_load(w[o], at, K);
+      xf[i] = few_load(x, at, K);
+    }
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      if (s + i * step >= steps) break;
+#pragma unroll
+      for (int o = 0; o < kOps; ++o) acc[o] = mfma16(T{}, wf[i][o], xf[i], acc[o]);
+    }
+  }
+}
+
+// h of one tile's rows, 16 columns to a work group.
+template <typename T, bool kDirect>
+__global__ __launch_bounds__(kNT) void k_few_in(ProductArgs a) {
+  const int cols = (a.Fpad + 15) / 16;
+  FewTile t;
+  if (!few_tile<kDirect>(a, blockIdx.x / cols, t)) return;
+  const int f0 = blockIdx.x % cols * 16, l = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const T* W = (const T*)a.b + t.expert * a.b_expert;
+  const int f = min(f0 + (l & 15), a.F - 1);
+  const void* w[2] = {W + (int64_t)f * a.ldb, W + (int64_t)(a.F + f) * a.ldb};
+  const int at = t.row0 + min(l & 15, t.rows - 1);
+  const void* x = (const T*)a.a + (int64_t)(kDirect ? at / a.k : a.d.tok[at]) * a.lda;
+  f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  few_products<T, 2>(w, x, wave, kWaves, (a.Kpad + 31) / 32, a.Kpad, acc);
+  __shared__ float part[kWaves][2][16][17];
+#pragma unroll
+  for (int o = 0; o < 2; ++o)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[wave][o][(l >> 4) * 4 + j][l & 15] = acc[o][j];
+  __syncthreads();
+  const int r = threadIdx.x / 16, c = threadIdx.x % 16;  // row, column
+  if (r >= t.rows || f0 + c >= a.Fpad) return;
+  float g = 0.0f, u = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kWaves; ++v) {
+    g += part[v][0][c][r];
+    u += part[v][1][c][r];
+  }
+  const float h = f0 + c < a.F ? g * fast_sigmoid(g) * u : 0.0f;
+  ((T*)a.c)[(int64_t)(t.row0 + r) * a.Fpad + f0 + c] = from_f32<T>(h);
+}
+
+// Rows of y before their sum, 32 columns to a work group.
+template <typename T>
+__global__ __launch_bounds__(kNT) void k_few_out(ProductArgs a) {
+  const int cols = (a.N + 31) / 32;
+  FewTile t;
+  if (!few_tile<false>(a, blockIdx.x / cols, t)) return;
+  const int n0 = blockIdx.x % cols * 32, l = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const T* W = (const T*)a.b + t.expert * a.b_expert;
+  const void* w[2] = {W + (int64_t)min(n0 + (l & 15), a.N - 1) * a.ldb,
+                      W + (int64_t)min(n0 + 16 + (l & 15), a.N - 1) * a.ldb};
+  const void* x = (const T*)a.a + (int64_t)(t.row0 + min(l & 15, t.rows - 1)) * a.lda;
+  f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  few_products<T, 2>(w, x, wave, kWaves, (a.Kpad + 31) / 32, a.Kpad, acc);
+  __shared__ float part[kWaves][32][17];
+#pragma unroll
+  for (int o = 0; o < 2; ++o)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[wave][o * 16 + (l >> 4) * 4 + j][l & 15] = acc[o][j];
+  __syncthreads();
+  const int c = threadIdx.x % 32;
+  for (int r = threadIdx.x / 32; r < t.rows; r += kNT / 32) {
+    if (n0 + c >= a.ldc) break;
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += part[i][c][r];
+    ((float*)a.c)[(int64_t)(t.row0 + r) * a.ldc + n0 + c] = v;
+  }
+}
+
+// y of one token straight from its entries' h (entry order), 16 columns to a
+// work group of 8 waves that share each entry's K.
+constexpr int kFewTokenWaves = 8;
+template <typename T>
+__global__ __launch_bounds__(kFewTokenWaves * kWave) void k_few_token(ProductArgs a) {
+  const int cols = (a.N + 15) / 16;
+  const int64_t t = blockIdx.x / cols;
+  const int n0 = blockIdx.x % cols * 16, l = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  const int n = min(n0 + (l & 15), a.N - 1);
+  // K steps of all entries in one row: step q is step q % per of entry q / per.
+  const int per = (a.Kpad + 31) / 32, all = per * a.k;
+  f32x4 sum = {0, 0, 0, 0}, acc = {0, 0, 0, 0};
+  float weight = 0.0f;
+  int entry = -1;
+  for (int q0 = wave; q0 < all; q0 += kFewTokenWaves * kFewBatch) {
+    s16x8 wf[kFewBatch], xf[kFewBatch];
+    int from[kFewBatch];
+    float wt[kFewBatch];
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      const int q = min(q0 + i * kFewTokenWaves, all - 1);
+      const int e = q / per, s = q0 + i * kFewTokenWaves < all ? q - e * per : per;
+      const int64_t at = t * a.k + e;
+      const int c = a.col[at];
+      const bool there = (uint32_t)c < (uint32_t)a.E;
+      from[i] = e;
+      wt[i] = there ? a.val[at] : 0.0f;
+      const int K = there ? a.Kpad : 0;
+      wf[i] = few_load((const T*)a.b + (there ? c : 0) * a.b_expert + (int64_t)n * a.ldb, s, K);
+      xf[i] = few_load((const T*)a.a + at * a.lda, s, K);
+    }
+#pragma unroll
+    for (int i = 0; i < kFewBatch; ++i) {
+      if (from[i] != entry) {
+        sum += weight * acc;
+        acc = f32x4{0, 0, 0, 0};
+        entry = from[i];
+        weight = wt[i];
+      }
+      acc = mfma16(T{}, wf[i], xf[i], acc);
+    }
+  }
+  sum += weight * acc;
+  __shared__ float part[kFewTokenWaves][16];
+  if ((l & 15) == 0)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[wave][(l >> 4) * 4 + j] = sum[j];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c >= 16 || n0 + c >= a.N) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kFewTokenWaves; ++i) v += part[i][c];
+  ((T*)a.c)[t * a.N + n0 + c] = from_f32<T>(v);
+}
+
 // ---- sums over a token's entries ----
 
 // out[t] = sum over its entries of w * rows[pos] (w = 1 without val), in the
@@ -794,6 +993,17 @@ Sizes sizes_of(const spgemm_experts_desc& d) {
   return z;
 }
 
+// How a forward pass goes: by entries in their own order, by tiles of a few
+// rows, or by large tiles.
+enum Path { kPathDirect, kPathFew, kPathTiles };
+
+Path path_of(const Sizes& z, bool keep) {
+  if (keep) return kPathTiles;
+  if (z.T == 1 || z.n <= z.E / 4) return kPathDirect;
+  if (z.n <= 6 * z.E) return kPathFew;
+  return kPathTiles;
+}
+
 // Rows of a tile: 256 when the experts' rows fill such tiles to more than
 // about half on average, else 128.
 int tile_rows(const Sizes& z) { return z.n > 256 * z.E ? 256 : 128; }
@@ -811,7 +1021,7 @@ void take_dispatch(Carver& c, const Sizes& z, Dispatch& d) {
   d.tok = c.take<int32_t>(z.n);
   d.w = c.take<float>(z.n);
   d.pos = c.take<int32_t>(z.n);
-  d.tiles = c.take<int32_t>(2 * dispatch_max_tiles(z.n, z.E, tile_rows(z)));
+  d.tiles = c.take<int32_t>(2 * dispatch_max_tiles(z.n, z.E, kFewRows));
   d.ntiles = c.take<int32_t>(1);
 }
 
@@ -940,7 +1150,10 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   } else {
     kp.d = w.d;
   }
-  launch_dispatch(col, val, z.n, z.k, z.E, tile_rows(z), kp.d, w.tmp, s);
+  const Path path = path_of(z, kept != nullptr);
+  if (path != kPathDirect)
+    launch_dispatch(col, val, z.n, z.k, z.E, path == kPathFew ? kFewRows : tile_rows(z), kp.d,
+                    w.tmp, s);
   const Rows xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
   const Rows w1 = padded_rows(w_in, z.D, z.E * 2 * z.F, z.D, w.pad.w_in, s);
   const Rows w2 = padded_rows(w_out, z.F, z.E * z.D, z.F, w.pad.w_out, s);
@@ -956,7 +1169,16 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   a.c = w.h;
   a.g = kp.g;
   a.u = kp.u;
-  product_by_rows<T, kIn>(a, z, s);
+  a.k = z.k;
+  a.col = col;
+  const int64_t few = path == kPathDirect ? z.n : dispatch_max_tiles(z.n, z.E, kFewRows);
+  const dim3 in_grid((unsigned)(few * ((z.Fp + 15) / 16)));
+  if (path == kPathDirect)
+    hipLaunchKernelGGL((k_few_in<T, true>), in_grid, dim3(kNT), 0, s, a);
+  else if (path == kPathFew)
+    hipLaunchKernelGGL((k_few_in<T, false>), in_grid, dim3(kNT), 0, s, a);
+  else
+    product_by_rows<T, kIn>(a, z, s);
   a = base_args(z, kp.d);
   a.a = w.h;
   a.lda = z.Fp;
@@ -968,7 +1190,20 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   a.Kpad = (int)z.Fp;
   a.c = w.rows;
   a.ldc = z.Dp;
-  product_by_rows<T, kOut>(a, z, s);
+  if (path == kPathDirect) {
+    a.c = y;
+    a.k = z.k;
+    a.col = col;
+    a.val = val;
+    hipLaunchKernelGGL((k_few_token<T>), dim3((unsigned)(z.T * ((z.D + 15) / 16))),
+                       dim3(kFewTokenWaves * kWave), 0, s, a);
+    return;
+  }
+  if (path == kPathFew)
+    hipLaunchKernelGGL((k_few_out<T>), dim3((unsigned)(few * ((z.D + 31) / 32))), dim3(kNT), 0, s,
+                       a);
+  else
+    product_by_rows<T, kOut>(a, z, s);
   combine<T>(z, w.rows, kp.d.pos, val, y, s);
 }
 

@@ -49,6 +49,11 @@ CASES = [
     (50, 6, 2, 1, 1, BF, {}),
     (200, 1024, 3, 16, 24, BF, {}),
     (33, 4, 2, 127, 65, HF, dict(gaps=True)),
+    (4, 64, 6, 264, 136, BF, {}),                 # few entries: each on its own
+    (7, 80, 5, 71, 50, HF, dict(gaps=True)),
+    (1, 3, 2, 2056, 520, BF, {}),
+    (60, 40, 2, 520, 104, BF, dict(hot=0.9)),     # few rows to most experts, several tiles of one
+    (31, 32, 4, 40, 2064, HF, dict(idle=0.2)),
 ]
 
 
