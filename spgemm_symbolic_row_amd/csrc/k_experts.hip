@@ -201,7 +201,7 @@ struct ProductArgs {
   float* g;          // fp32 pre-activations, Fpad to a row
   float* u;
   void* hw;          // w h
-  float* dval_part;  // per entry: one partial sum of each 128 columns
+  float* dval_part;  // per entry: one partial sum of each wave's columns
   int parts;
   int k;               // slots of a row of the routing matrix
   const int32_t* col;  // and its entries, where they are taken unsorted
@@ -283,10 +283,10 @@ __device__ __forceinline__ void for_each_index(F& f) {
 // LDS stages of the operands.  160 KB hold five of 32 KB: the left operand
 // has three, which gives its loads half a slice more.  A weight gradient
 // keeps its token list there instead.
-template <int KIND, int BM>
+template <int KIND, int BM, int BN>
 struct Stages {
   static constexpr bool kWGrad = KIND == kGradWOut || KIND == kGradWIn;
-  static constexpr int kA = kWGrad ? 2 : 3, kB = !kWGrad && BM < 256 ? 3 : 2;
+  static constexpr int kA = kWGrad ? 2 : 3, kB = !kWGrad && BM < BN ? 3 : 2;
 };
 
 // kFar: the gathered rows span 4 GB or more, so that their offsets are 64-bit
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   constexpr bool kBGather = KIND == kGradWIn;
   constexpr int kABytes = BM * kBK * 2, kBBytes = BN * kBK * 2;
   constexpr int AL = BM / 32, BL = BN / 32;  // loads of a wave per slice
-  constexpr int AS = Stages<KIND, BM>::kA, BS = Stages<KIND, BM>::kB;
+  constexpr int AS = Stages<KIND, BM, BN>::kA, BS = Stages<KIND, BM, BN>::kB;
   constexpr int kNStep = KIND == kIn ? BN / 2 : BN;
   extern __shared__ char smem[];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)smem;
@@ -514,7 +514,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       const uint32_t ra = la[P], rb = lb[P];
       const uint32_t wa = la[2] + wave * 1024, wb = lb[2] + wave * 1024;
       constexpr int kAll = 2 * MT * NT, kReads = 2 * (MT + NT);
-      constexpr int kSpan = kAll * 3 / 4;  // products that reads and loads go between
+      // Products that reads and loads go between; a product takes one load at most.
+      constexpr int kSpan = kAll * 3 / 4 > kLoads ? kAll * 3 / 4 : kLoads;
+      static_assert(kSpan <= kAll, "a half has products for all its loads");
       auto step = [&](auto index) {
         constexpr int i = decltype(index)::value;
         constexpr int kb = i / (MT * NT), m = i / NT % MT, n = i % NT;
@@ -709,7 +711,7 @@ void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   const int64_t tiles = row_tiles * ((a.N + step - 1) / step);
   const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
   if (grid == 0) return;
-  typedef Stages<KIND, BM> S;
+  typedef Stages<KIND, BM, BN> S;
   const size_t lds =
       (S::kA * BM + S::kB * BN) * kBK * 2 + (S::kWGrad ? kListLen * sizeof(int32_t) : 0);
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(kNT), lds, s, a);
@@ -999,7 +1001,12 @@ enum Path { kPathDirect, kPathFew, kPathTiles };
 
 Path path_of(const Sizes& z, bool keep) {
   if (keep) return kPathTiles;
+  // Unsorted entries read the weights of a shared expert once each, but save
+  // the dispatch and the sum: 2 tokens of 8 picks among 128 experts 43 against
+  // 46 us, 8 tokens 118 against 105 us.
   if (z.T == 1 || z.n <= z.E / 4) return kPathDirect;
+  // 16 rows to a tile against 128: 3 entries to an expert 209 against 237 us, 4.5
+  // 180 against 194, 6 186 against 228, 9 217 against 209.
   if (z.n <= 6 * z.E) return kPathFew;
   return kPathTiles;
 }
@@ -1073,14 +1080,15 @@ struct BackwardWork {
   Padded pad;
 };
 
-int dval_parts(const Sizes& z) { return (int)((z.Fp + 127) / 128); }
+// Partial sums of a value's gradient: one for each wave's columns.
+int dval_parts(const Sizes& z, int cols) { return (int)((z.Fp + cols - 1) / cols); }
 
 BackwardWork take_backward(Carver& c, const Sizes& z, bool padded) {
   BackwardWork w{};
   w.dgu = c.take<uint16_t>(z.n * z.S2);
   w.hw = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
-  w.part = c.take<float>(z.n * dval_parts(z));
+  w.part = c.take<float>(z.n * dval_parts(z, 64));
   if (padded) w.pad = take_padded(c, z, true);
   return w;
 }
@@ -1106,19 +1114,42 @@ bool needs_padding(const spgemm_experts_desc& d, const void* x, const void* w_in
          ((uintptr_t)x | (uintptr_t)w_in | (uintptr_t)w_out | (uintptr_t)dy) % 16;
 }
 
-template <typename T, int KIND>
-void product_by_rows(const ProductArgs& a, const Sizes& z, hipStream_t s) {
+// Up to this many tiles a product takes smaller ones, so that more of the 256
+// compute units have one.  Measured, forward pass: 76 tiles 36 -> 29 us, 120
+// tiles 46 -> 38 us, but 195 tiles 59 -> 66 us and 256 tiles 81 -> 106 us, where
+// the smaller ones take two rounds.
+constexpr int64_t kFewTiles = 128;
+
+// Whether a product of N columns (of pairs: gate and up) by row tiles of 128
+// takes them.
+bool narrow_tiles(const Sizes& z, int64_t N, bool pairs) {
+  const int64_t step = pairs ? 128 : 256;
+  return dispatch_max_tiles(z.n, z.E, 128) * ((N + step - 1) / step) <= kFewTiles;
+}
+
+template <typename T, int KIND, bool kFar>
+void product_by_size(const ProductArgs& a, const Sizes& z, hipStream_t s) {
   const int bm = tile_rows(z);
   const int64_t tiles = dispatch_max_tiles(z.n, z.E, bm);
-  if constexpr (KIND == kIn || KIND == kGradH) {
-    if (z.T * a.lda >= (int64_t)1 << 31) {
-      if (bm == 256) launch_product<T, KIND, 256, 256, true>(a, tiles, s);
-      else launch_product<T, KIND, 128, 256, true>(a, tiles, s);
-      return;
-    }
-  }
-  if (bm == 256) launch_product<T, KIND, 256, 256>(a, tiles, s);
-  else launch_product<T, KIND, 128, 256>(a, tiles, s);
+  if (bm == 256) launch_product<T, KIND, 256, 256, kFar>(a, tiles, s);
+  else if (narrow_tiles(z, a.N, KIND == kIn)) launch_product<T, KIND, 128, 128, kFar>(a, tiles, s);
+  else launch_product<T, KIND, 128, 256, kFar>(a, tiles, s);
+}
+
+template <typename T, int KIND>
+void product_by_rows(const ProductArgs& a, const Sizes& z, hipStream_t s) {
+  if constexpr (KIND == kIn || KIND == kGradH)
+    if (z.T * a.lda >= (int64_t)1 << 31) return product_by_size<T, KIND, true>(a, z, s);
+  product_by_size<T, KIND, false>(a, z, s);
+}
+
+template <typename T, int KIND>
+void weight_gradient(const ProductArgs& a, const Sizes& z, hipStream_t s) {
+  auto up = [](int64_t x, int64_t t) { return (x + t - 1) / t; };
+  if (z.E * up(a.M, 256) * up(a.N, 256) <= kFewTiles)
+    launch_product<T, KIND, 128, 128>(a, z.E * up(a.M, 128), s);
+  else
+    launch_product<T, KIND, 256, 256>(a, z.E * up(a.M, 256), s);
 }
 
 ProductArgs base_args(const Sizes& z, const Dispatch& d) {
@@ -1235,7 +1266,8 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.u = kp.u;
   a.hw = w.hw;
   a.dval_part = w.part;
-  a.parts = dval_parts(z);
+  a.parts = dval_parts(z, tile_rows(z) == 128 && narrow_tiles(z, z.Fp, false) ? 64 : 128);
+  const int parts = a.parts;
   product_by_rows<T, kGradH>(a, z, s);
   a = base_args(z, kp.d);
   a.a = w.dgu;
@@ -1252,7 +1284,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   product_by_rows<T, kGradX>(a, z, s);
   combine<T>(z, w.rows, kp.d.pos, nullptr, dx, s);
   hipLaunchKernelGGL(k_dval, dim3((unsigned)((z.n + 255) / 256)), dim3(256), 0, s, z.n,
-                     dval_parts(z), kp.d.pos, w.part, dval);
+                     parts, kp.d.pos, w.part, dval);
   a = base_args(z, kp.d);
   a.a = gr.p;
   a.lda = gr.ld;
@@ -1265,7 +1297,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.c = dw_out;
   a.ldc = z.F;
   a.c_expert = z.D * z.F;
-  launch_product<T, kGradWOut, 256, 256>(a, z.E * ((z.D + 255) / 256), s);
+  weight_gradient<T, kGradWOut>(a, z, s);
   a = base_args(z, kp.d);
   a.a = w.dgu;
   a.lda = z.S2;
@@ -1278,7 +1310,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.c = dw_in;
   a.ldc = z.D;
   a.c_expert = 2 * z.F * z.D;
-  launch_product<T, kGradWIn, 256, 256>(a, z.E * ((2 * z.F + 255) / 256), s);
+  weight_gradient<T, kGradWIn>(a, z, s);
 }
 
 // ---- checks ----
