@@ -3,8 +3,11 @@
 // Squares are summed in fp64, which no finite value overflows, in an order
 // that only the sizes fix.  The first kernel leaves one partial sum per work
 // group; each work group of the second adds them up again (at most 16 KB from
-// L2, which costs less than a launch between) and scales its share.  Every
-// element is read twice and written once; the bytes bound it.
+// L2, which costs less than a launch between) and scales its share.  Tables
+// that do not fit one launch's arguments take several of each, and one work
+// group between that adds all partial sums up.  Every element is read twice and
+// written once; the bytes bound it.  The scaling goes backwards, so that it
+// begins with what the memory-side cache still holds.
 #include <algorithm>
 
 #include "expert_common.hpp"
@@ -14,7 +17,7 @@ namespace {
 
 constexpr int kGnNT = 256;
 constexpr int kGnTable = 96;       // tensors of one launch (2.3 KB of kernel arguments)
-constexpr int kGnParts = 2048;     // partial sums of one call
+constexpr int kGnParts = 2048;     // partial sums, and work groups, of one launch
 constexpr int64_t kGnChunk = 16384;  // elements of one work item
 
 struct GradTable {
@@ -118,6 +121,16 @@ __device__ __forceinline__ void scale_from(const T* p, void* o, int out, int64_t
   else scale_into(p, (_Float16*)o + off, n, c);
 }
 
+// total = the sum of all partial sums.
+__global__ __launch_bounds__(kGnNT) void k_grad_total(const double* __restrict__ parts, int nparts,
+                                                      double* __restrict__ total) {
+  double s = 0.0;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < nparts; i += kGnNT) s += parts[i];
+  s = group_sum(s);
+  if (threadIdx.x == 0) *total = s;
+}
+
 __global__ __launch_bounds__(kGnNT) void k_grad_scale(GradTable t,
                                                       const double* __restrict__ parts,
                                                       int nparts, double max_norm,
@@ -143,11 +156,9 @@ bool is_grad_type(int32_t t) { return t == SPGEMM_F32 || t == SPGEMM_BF16 || t =
 
 int64_t items_of(int64_t n) { return (n + kGnChunk - 1) / kGnChunk; }
 
-// Work groups of one launch with `items` work items out of `all`.
-int grid_of(int64_t items, int64_t all) {
-  if (all <= kGnParts) return (int)std::max<int64_t>(items, 1);
-  return (int)std::max<int64_t>(1, items * (kGnParts - 64) / all);
-}
+int grid_of(int64_t items) { return (int)std::min<int64_t>(std::max<int64_t>(items, 1), kGnParts); }
+
+int64_t launches_of(int64_t count) { return std::max<int64_t>(count, 0) / kGnTable + 1; }
 
 }  // namespace
 }  // namespace sg
@@ -155,7 +166,7 @@ int grid_of(int64_t items, int64_t all) {
 using namespace sg;
 
 extern "C" int64_t spgemm_clip_grad_norm_workspace(int64_t count) {
-  return (kGnParts + std::max<int64_t>(count, 0) / kGnTable + 1) * (int64_t)sizeof(double);
+  return (launches_of(count) * kGnParts + 1) * (int64_t)sizeof(double);
 }
 
 extern "C" spgemm_status spgemm_clip_grad_norm(int64_t count, const void* const* dGrads,
@@ -186,32 +197,38 @@ extern "C" spgemm_status spgemm_clip_grad_norm(int64_t count, const void* const*
     return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "clip_grad_norm: too many elements");
   const hipStream_t s = (hipStream_t)stream;
   double* parts = (double*)dWork;
-  int nparts = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t i = 0;
-    bool first = true;
-    do {
-      GradTable t{};
-      for (; i < count && t.count < kGnTable; ++i) {
-        if (!sizes[i]) continue;
-        t.in[t.count] = dGrads[i];
-        t.out[t.count] = dOut[i];
-        t.n[t.count] = sizes[i];
-        t.type[t.count] = (uint8_t)(grad_types[i] | out_types[i] << 4);
-        t.first[t.count + 1] = t.first[t.count] + (int32_t)items_of(sizes[i]);
-        ++t.count;
-      }
-      const int grid = grid_of(t.first[t.count], all);
-      if (pass == 0) {
-        hipLaunchKernelGGL(k_grad_squares, dim3(grid), dim3(kGnNT), 0, s, t, parts + nparts);
-        nparts += grid;
-      } else {
-        hipLaunchKernelGGL(k_grad_scale, dim3(grid), dim3(kGnNT), 0, s, t, (const double*)parts,
-                           nparts, max_norm, first ? dNorm : nullptr);
-        first = false;
-      }
-    } while (i < count);
+  auto add = [&](GradTable& t, int64_t i) {
+    if (!sizes[i]) return;
+    t.in[t.count] = dGrads[i];
+    t.out[t.count] = dOut[i];
+    t.n[t.count] = sizes[i];
+    t.type[t.count] = (uint8_t)(grad_types[i] | out_types[i] << 4);
+    t.first[t.count + 1] = t.first[t.count] + (int32_t)items_of(sizes[i]);
+    ++t.count;
+  };
+  int nparts = 0, launches = 0;
+  int64_t i = 0;
+  do {
+    GradTable t{};
+    for (; i < count && t.count < kGnTable; ++i) add(t, i);
+    const int grid = grid_of(t.first[t.count]);
+    hipLaunchKernelGGL(k_grad_squares, dim3(grid), dim3(kGnNT), 0, s, t, parts + nparts);
+    nparts += grid;
+    ++launches;
+  } while (i < count);
+  const double* sums = parts;
+  if (launches > 1) {
+    double* total = parts + launches * kGnParts;
+    hipLaunchKernelGGL(k_grad_total, dim3(1), dim3(kGnNT), 0, s, sums, nparts, total);
+    sums = total;
+    nparts = 1;
   }
+  do {
+    GradTable t{};
+    for (; i > 0 && t.count < kGnTable; --i) add(t, i - 1);
+    hipLaunchKernelGGL(k_grad_scale, dim3(grid_of(t.first[t.count])), dim3(kGnNT), 0, s, t, sums,
+                       nparts, max_norm, dNorm);
+  } while (i > 0);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SPGEMM_OK : refuse(SPGEMM_ERR_HIP, hipGetErrorString(e));
 }

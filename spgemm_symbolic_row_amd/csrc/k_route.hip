@@ -2,13 +2,14 @@
 // row t of the sparse routing matrix: the k experts with the largest keys,
 // columns rising, and their weights.
 //
-// One wave takes one row; lane l holds experts l*V .. l*V+V-1, so the lowest
-// lane of a tie holds the lowest expert.  Keys are compared as ordered 32-bit
-// integers; each of the k picks is one DPP maximum over the wave and one
-// ballot.  All sums are in 32 bits.  A row is read once (4 to 2 bytes per
-// logit) and 8 bytes per entry are written; what bounds it is the chain of
-// picks (about 8 dependent steps each) at few rows, and their instructions at
-// many.
+// Up to 256 experts 16 lanes take a row, four rows to a wave; above, a wave
+// does.  Lane l of a row holds experts l*V .. l*V+V-1, so the lowest lane of a
+// tie holds the lowest expert.  Keys are compared as ordered 32-bit integers;
+// each of the k picks is a maximum over the lane's keys, one over the row by
+// DPP and one ballot.  The picks are then packed through LDS, so that the
+// weights cost one exponential each.  All sums are in 32 bits.  A row is read
+// once (4 or 2 bytes per logit) and 8 bytes per entry are written; what bounds
+// it is the chain of picks at few rows and the instructions at many.
 #include <algorithm>
 
 #include "expert_common.hpp"
@@ -17,20 +18,59 @@ namespace sg {
 namespace {
 
 constexpr int kRouteNT = 256;
-constexpr int kRouteRows = kRouteNT / kWave;
+constexpr int kRouteRows = kRouteNT / kWave;  // of the gradient: a wave takes a row
 
 template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* row, int E, bool vec, float z[V]) {
-  const int e0 = lane_id() * V;
+__device__ __forceinline__ void load_logits(const T* row, int e0, int E, bool vec, float z[V]) {
   if (vec && e0 + V <= E) {
-    struct alignas(sizeof(T) * V) Pack { T v[V]; };
-    const Pack p = *(const Pack*)(row + e0);
+    constexpr int kOnce = V * sizeof(T) > 16 ? 16 / sizeof(T) : V;  // values of one load
+    struct alignas(sizeof(T) * kOnce) Pack { T v[kOnce]; };
 #pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = to_f32(p.v[j]);
+    for (int i = 0; i < V / kOnce; ++i) {
+      const Pack p = ((const Pack*)(row + e0))[i];
+#pragma unroll
+      for (int j = 0; j < kOnce; ++j) z[i * kOnce + j] = to_f32(p.v[j]);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) z[j] = e0 + j < E ? to_f32(row[e0 + j]) : -INFINITY;
   }
+}
+
+// Maximum and sum over the L lanes of a row, in all of them.
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t x) {
+  if constexpr (L == 64) return wave_max_u32(x);
+  x = max(x, dpp_or_zero<0x128, 0xf>(x));  // row_ror:8
+  x = max(x, dpp_or_zero<0x124, 0xf>(x));
+  x = max(x, dpp_or_zero<0x122, 0xf>(x));
+  return max(x, dpp_or_zero<0x121, 0xf>(x));
+}
+template <int L>
+__device__ __forceinline__ float row_sum(float x) {
+  if constexpr (L == 64) return wave_sum_f32(x);
+  x = dpp_add<0x128, 0xf>(x);
+  x = dpp_add<0x124, 0xf>(x);
+  x = dpp_add<0x122, 0xf>(x);
+  return dpp_add<0x121, 0xf>(x);
+}
+// First lane of the row, counted from its start, for which `is` holds.
+template <int L>
+__device__ __forceinline__ int row_first(bool is) {
+  const uint64_t m = __ballot(is);
+  if constexpr (L == 64) return ffs64(m);
+  return __ffs((int)(uint32_t)(m >> (lane_id() & 48)) & 0xffff) - 1;
+}
+// Sum over the row's lower lanes.
+template <int L>
+__device__ __forceinline__ int row_excl_scan(int x) {
+  if constexpr (L == 64) return wave_incl_scan(x) - x;
+  uint32_t s = x;
+  s += dpp_or_zero<0x111, 0xf>(s);  // row_shr:1
+  s += dpp_or_zero<0x112, 0xf>(s);
+  s += dpp_or_zero<0x114, 0xf>(s);
+  s += dpp_or_zero<0x118, 0xf>(s);
+  return (int)s - x;
 }
 
 // As the keys are defined: 0 below z = -88, where exp(-z) is beyond fp32.
@@ -52,41 +92,73 @@ __device__ __forceinline__ uint32_t key_of(float z, float b, bool biased) {
 }
 
 // The groups that may be chosen from, as a bit mask: group g's score is its
-// largest key (softmax) or the sum of its two largest (sigmoid).
-template <int V, bool kSig>
-__device__ __forceinline__ uint64_t pick_groups(const uint32_t key[V], int per, int G, int top) {
-  const int e0 = lane_id() * V;
-  uint32_t score = 0;  // of group lane_id()
-  for (int g = 0; g < G; ++g) {
-    uint32_t m = 0;
+// largest key (softmax) or the sum of its two largest (sigmoid).  Where a group
+// is `span` = a power of two whole lanes, all groups are reduced at once by
+// exchanges inside them; else one after the other.
+template <int L, int V, bool kSig>
+__device__ __forceinline__ uint64_t pick_groups(const uint32_t key[V], int per, int G, int top,
+                                                int span) {
+  const int lane = lane_id() % L, e0 = lane * V;
+  constexpr int kSlots = 64 / L;  // lane l holds the scores of groups l, l + L, ..
+  uint32_t score[kSlots];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if ((e0 + j) / per == g) m = max(m, key[j]);
-    const uint32_t M = wave_max_u32(m);
-    uint32_t s = M;
-    if (kSig && M) {
-      const int first = ffs64(__ballot(m == M));
-      uint32_t m2 = 0;
-      bool seen = false;  // the largest key counts once, at its lowest expert
+  for (int i = 0; i < kSlots; ++i) score[i] = 0;
+  auto score_of = [](uint32_t m, uint32_t m2) {
+    return kSig && m2 ? ordered_bits(from_ordered(m) + from_ordered(m2)) : m;
+  };
+  if (span) {
+    uint32_t m = 0, m2 = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      m2 = max(m2, min(m, key[j]));
+      m = max(m, key[j]);
+    }
+    for (int d = 1; d < span; d <<= 1) {
+      const uint32_t o = __shfl_xor(m, d), o2 = __shfl_xor(m2, d);
+      m2 = max(max(m2, o2), min(m, o));
+      m = max(m, o);
+    }
+    const uint32_t s = score_of(m, m2);
+    // At most L groups here.
+    const uint32_t mine = __shfl(s, (lane_id() & ~(L - 1)) + lane * span % L);
+    score[0] = lane < G ? mine : 0;
+  } else {
+    for (int g = 0; g < G; ++g) {
+      uint32_t m = 0, m2 = 0;
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if ((e0 + j) / per == g) {
-          const bool skip = lane_id() == first && key[j] == M && !seen;
-          if (skip) seen = true;
-          else m2 = max(m2, key[j]);
+          m2 = max(m2, min(m, key[j]));
+          m = max(m, key[j]);
         }
-      const uint32_t M2 = wave_max_u32(m2);
-      if (M2) s = ordered_bits(from_ordered(M) + from_ordered(M2));
+      const uint32_t M = row_max<L>(m);
+      uint32_t s = M;
+      if constexpr (kSig) {
+        // The row's second key: the first holder of the largest gives its own second.
+        const int first = row_first<L>(m == M);
+        s = score_of(M, row_max<L>(lane == first ? m2 : m));
+      }
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i)
+        if (lane + i * L == g) score[i] = s;
     }
-    if (lane_id() == g) score = s;
   }
   uint64_t chosen = 0;
-  for (int i = 0; i < top; ++i) {
-    const uint32_t M = wave_max_u32(score);
-    if (!M) break;
-    const int g = ffs64(__ballot(score == M));
-    chosen |= 1ull << g;
-    if (lane_id() == g) score = 0;
+  for (int n = 0; n < top; ++n) {
+    uint32_t m = score[0];
+#pragma unroll
+    for (int i = 1; i < kSlots; ++i) m = max(m, score[i]);
+    const uint32_t M = row_max<L>(m);
+    bool done = false;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const int l = row_first<L>(score[i] == M && M);
+      if (!done && l >= 0) {
+        done = true;
+        chosen |= 1ull << (l + i * L);
+        if (lane == l) score[i] = 0;
+      }
+    }
   }
   return chosen;
 }
@@ -99,21 +171,23 @@ struct RouteArgs {
   int32_t* col;
   float* val;
   int64_t T;
-  int E, k, groups, top_groups;
+  int E, k, groups, top_groups, span;
   bool renorm, vec;
   float scale;
 };
 
-template <typename T, int V, bool kSig>
+template <typename T, int L, int V, bool kSig>
 __global__ __launch_bounds__(kRouteNT) void k_route(RouteArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * kRouteRows + threadIdx.x / kWave;
-  if (t >= a.T) return;
-  const int lane = lane_id(), e0 = lane * V;
+  extern __shared__ uint32_t packed[];  // per row: k columns, k logits
+  const int row = threadIdx.x / L, lane = threadIdx.x % L, e0 = lane * V;
+  const int64_t t = (int64_t)blockIdx.x * (kRouteNT / L) + row;
+  if ((int64_t)blockIdx.x * (kRouteNT / L) + threadIdx.x / kWave * (kWave / L) >= a.T)
+    return;  // the whole wave
+  const bool inside = t < a.T;
   float z[V];
   uint32_t key[V];
-  const bool active = !a.active || a.active[t];
-  if (active) {
-    load_logits<T, V>((const T*)a.logits + t * a.ld, a.E, a.vec, z);
+  if (inside && (!a.active || a.active[t])) {
+    load_logits<T, V>((const T*)a.logits + t * a.ld, e0, a.E, a.vec, z);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) z[j] = -INFINITY;
@@ -131,76 +205,91 @@ __global__ __launch_bounds__(kRouteNT) void k_route(RouteArgs a) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (key[j]) m = max(m, ordered_bits(z[j]));
-    const uint32_t M = wave_max_u32(m);
+    const uint32_t M = row_max<L>(m);
     top = M ? from_ordered(M) : 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (key[j]) total += expf(z[j] - top);
-    total = wave_sum_f32(total);
+    total = row_sum<L>(total);
   }
   if (a.groups > 1) {
     const int per = a.E / a.groups;
-    const uint64_t chosen = pick_groups<V, kSig>(key, per, a.groups, a.top_groups);
+    const uint64_t chosen = pick_groups<L, V, kSig>(key, per, a.groups, a.top_groups, a.span);
+    if (a.span) {  // a lane's experts are of one group
+      const bool keep = e0 < a.E && (chosen >> (e0 / per)) & 1;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (e0 + j < a.E && !((chosen >> ((e0 + j) / per)) & 1)) key[j] = 0;
+      for (int j = 0; j < V; ++j) key[j] = keep ? key[j] : 0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (e0 + j < a.E && !((chosen >> ((e0 + j) / per)) & 1)) key[j] = 0;
+    }
   }
   uint32_t taken = 0;  // bit j: expert e0 + j is picked
-  int count = 0;
-  for (; count < a.k; ++count) {
+  for (int n = 0; n < a.k; ++n) {
     uint32_t m = key[0];
 #pragma unroll
     for (int j = 1; j < V; ++j) m = max(m, key[j]);
-    const uint32_t M = wave_max_u32(m);
-    if (!M) break;
-    if (lane == ffs64(__ballot(m == M))) {
-      bool done = false;
+    const uint32_t M = row_max<L>(m);
+    if (L == 64 && !M) break;
+    if (M && lane == row_first<L>(m == M)) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) bits |= (key[j] == M ? 1u : 0u) << j;
+      bits &= -bits;
+      taken |= bits;
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (!done && key[j] == M) {
-          done = true;
-          key[j] = 0;
-          taken |= 1u << j;
-        }
+        if ((bits >> j) & 1) key[j] = 0;
     }
   }
-  // Weights of the picked experts.
-  float w[V];
+  // Pack the picks: those of lower lanes first, then of lower experts.
+  uint32_t* cols = packed + row * 2 * a.k;
+  float* zs = (float*)(cols + a.k);
+  const int mine = __popc(taken), before = row_excl_scan<L>(mine);
+  int at = before;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((taken >> j) & 1) {
+      cols[at] = e0 + j;
+      zs[at] = z[j];
+      ++at;
+    }
+  const int count = __shfl(before + mine, (lane_id() & ~(L - 1)) + L - 1);
+  __builtin_amdgcn_wave_barrier();  // one wave's LDS accesses are performed in order
+  // Weights: entry i of the row in lane i % L.
+  constexpr int kMost = 64 / L;
+  float w[kMost], sum = 0.0f;
   if (!kSig && a.renorm) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if ((taken >> j) & 1) m = max(m, ordered_bits(z[j]));
-    const uint32_t M = wave_max_u32(m);
+    for (int n = 0; n < kMost; ++n)
+      if (lane + n * L < count) m = max(m, ordered_bits(zs[lane + n * L]));
+    const uint32_t M = row_max<L>(m);
     top = M ? from_ordered(M) : 0.0f;
   }
-  float sum = 0.0f;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    w[j] = (taken >> j) & 1 ? (kSig ? sigmoid(z[j]) : expf(z[j] - top)) : 0.0f;
-    sum += w[j];
+  for (int n = 0; n < kMost; ++n) {
+    w[n] = 0.0f;
+    if (lane + n * L < count) {
+      const float x = zs[lane + n * L];
+      w[n] = kSig ? sigmoid(x) : expf(x - top);
+      sum += w[n];
+    }
   }
   if (a.renorm) {
-    total = wave_sum_f32(sum);
+    total = row_sum<L>(sum);
     if (kSig) total += 1e-20f;
   } else if (kSig) {
     total = 1.0f;
   }
-  // Positions: picks of lower lanes, then of lower experts in the lane.
-  int at = 0;
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    at += (int)__popcll(__ballot((taken >> j) & 1) & lanemask_lt());
-#pragma unroll
-  for (int j = 0; j < V; ++j)
-    if ((taken >> j) & 1) {
-      a.col[t * a.k + at] = e0 + j;
-      a.val[t * a.k + at] = w[j] / total * a.scale;
-      ++at;
+  for (int n = 0; n < kMost; ++n) {
+    const int i = lane + n * L;
+    if (inside && i < a.k) {
+      a.col[t * a.k + i] = i < count ? (int)cols[i] : -1;
+      a.val[t * a.k + i] = i < count ? w[n] / total * a.scale : 0.0f;
     }
-  if (lane >= count && lane < a.k) {
-    a.col[t * a.k + lane] = -1;
-    a.val[t * a.k + lane] = 0.0f;
   }
 }
 
@@ -248,7 +337,7 @@ __global__ __launch_bounds__(kRouteNT) void k_route_grad(RouteGradArgs a) {
     }
     __builtin_amdgcn_wave_barrier();
     float z[V], p[V], dw[V];
-    load_logits<T, V>((const T*)a.logits + t * a.ld, a.E, a.vec, z);
+    load_logits<T, V>((const T*)a.logits + t * a.ld, e0, a.E, a.vec, z);
     bool in[V], pick[V];
     uint32_t m = 0;
 #pragma unroll
@@ -289,14 +378,27 @@ __global__ __launch_bounds__(kRouteNT) void k_route_grad(RouteGradArgs a) {
     if (e0 + j < a.E) out[e0 + j] = from_f32<T>(d[j]);
 }
 
+// Experts of a lane, and lanes of a row.
+int width_of(int64_t E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
+int lanes_of(int64_t E) { return E <= 256 ? 16 : 64; }
+
+template <typename T, int L, int V, bool kSig>
+void launch_route(const RouteArgs& a, hipStream_t s) {
+  constexpr int kRows = kRouteNT / L;
+  hipLaunchKernelGGL((k_route<T, L, V, kSig>), dim3((unsigned)((a.T + kRows - 1) / kRows)),
+                     dim3(kRouteNT), (size_t)kRows * 2 * a.k * sizeof(uint32_t), s, a);
+}
+
 template <typename T, bool kSig>
 void route_by_width(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + kRouteRows - 1) / kRouteRows)), nt(kRouteNT);
-  if (a.E <= 64) hipLaunchKernelGGL((k_route<T, 1, kSig>), grid, nt, 0, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((k_route<T, 2, kSig>), grid, nt, 0, s, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((k_route<T, 4, kSig>), grid, nt, 0, s, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((k_route<T, 8, kSig>), grid, nt, 0, s, a);
-  else hipLaunchKernelGGL((k_route<T, 16, kSig>), grid, nt, 0, s, a);
+  if (lanes_of(a.E) == 64) return launch_route<T, 64, 16, kSig>(a, s);
+  switch (width_of(a.E)) {
+    case 1: return launch_route<T, 16, 1, kSig>(a, s);
+    case 2: return launch_route<T, 16, 2, kSig>(a, s);
+    case 4: return launch_route<T, 16, 4, kSig>(a, s);
+    case 8: return launch_route<T, 16, 8, kSig>(a, s);
+    default: return launch_route<T, 16, 16, kSig>(a, s);
+  }
 }
 
 template <typename T, bool kSig>
@@ -310,14 +412,12 @@ void route_grad_by_width(const RouteGradArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_route_grad<T, 16, kSig>), grid, nt, lds, s, a);
 }
 
-int width_of(int64_t E) { return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16; }
-
 int64_t type_bytes(spgemm_dtype t) { return t == SPGEMM_F32 ? 4 : 2; }
 
-// Whether a lane's experts can be loaded at once.
-bool can_vec(const void* p, int64_t ld, int64_t E, spgemm_dtype t) {
-  const int64_t b = type_bytes(t) * width_of(E);
-  return (uintptr_t)p % b == 0 && ld % width_of(E) == 0 && b <= 16;
+// Whether a lane's `width` experts can be loaded at once, 16 bytes at most.
+bool can_vec(const void* p, int64_t ld, int64_t width, spgemm_dtype t) {
+  const int64_t b = std::min<int64_t>(type_bytes(t) * width, 16);
+  return (uintptr_t)p % b == 0 && ld * type_bytes(t) % b == 0;
 }
 
 spgemm_status refuse(spgemm_status st, const char* msg) {
@@ -381,7 +481,9 @@ extern "C" spgemm_status spgemm_route(int64_t T, int64_t E, int32_t k, const voi
   a.top_groups = opts->top_groups ? opts->top_groups : a.groups;
   if (a.top_groups == a.groups) a.groups = 1;  // every group is chosen
   a.renorm = !opts->no_renormalise;
-  a.vec = can_vec(dLogits, ld, E, dtype);
+  a.vec = can_vec(dLogits, ld, width_of(E), dtype);
+  const int64_t per = E / a.groups, lanes = per / width_of(E);
+  if (per % width_of(E) == 0 && (lanes & (lanes - 1)) == 0) a.span = (int)lanes;
   a.scale = opts->scale != 0.0f ? opts->scale : 1.0f;
   const hipStream_t s = (hipStream_t)stream;
   if (dtype == SPGEMM_F32)
@@ -413,7 +515,8 @@ extern "C" spgemm_status spgemm_route_backward(int64_t T, int64_t E, int32_t k,
   a.E = (int)E;
   a.k = k;
   a.renorm = !opts->no_renormalise;
-  a.vec = can_vec(dLogits, ld, E, dtype);
+  const int64_t width = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16;
+  a.vec = can_vec(dLogits, ld, width, dtype);
   a.scale = opts->scale != 0.0f ? opts->scale : 1.0f;
   const hipStream_t s = (hipStream_t)stream;
   if (dtype == SPGEMM_F32)

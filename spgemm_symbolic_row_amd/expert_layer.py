@@ -17,6 +17,7 @@ stream of the tensors' device, asynchronously.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
@@ -38,11 +39,15 @@ def _check(status):
         check(status)
 
 
+_HERE = nullcontext()
+
+
 def _on(x):
     """Makes x's device current, so that the call runs on its stream there."""
-    if not x.is_cuda:
+    i = x.get_device()
+    if i < 0:
         raise TypeError("tensors must be device tensors")
-    return torch.cuda.device(x.device)
+    return _HERE if i == torch.cuda.current_device() else torch.cuda.device(i)
 
 
 def _stream(x):
@@ -63,9 +68,9 @@ def _rows(x, what):
 
 
 def _dense(x, shape, dtype, device, what):
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
     if x.device != device:
         raise TypeError(f"{what} must be on {device}")
@@ -265,25 +270,27 @@ def clip_grad_norm(grads, max_norm, out=None):
     if not grads:
         raise ValueError("no gradients")
     dev, n = grads[0].device, len(grads)
-    for g, o in zip(grads, outs):
-        if g.device != dev or o.device != dev:
-            raise TypeError("tensors must be on one device")
-        if g.shape != o.shape:
-            raise ValueError("out must have the shapes of grads")
-        if not (g.is_contiguous() and o.is_contiguous()):
-            raise TypeError("tensors must be contiguous")
+    T = torch.Tensor
+    if len(set(map(T.get_device, grads)) | set(map(T.get_device, outs))) != 1:
+        raise TypeError("tensors must be on one device")
+    if outs is not grads and [g.shape for g in grads] != [o.shape for o in outs]:
+        raise ValueError("out must have the shapes of grads")
+    if not (all(map(T.is_contiguous, grads)) and all(map(T.is_contiguous, outs))):
+        raise TypeError("tensors must be contiguous")
     try:
-        types = [(_TYPES[g.dtype], _TYPES[o.dtype]) for g, o in zip(grads, outs)]
+        types = (c_i32 * n)(*[_TYPES[g.dtype] for g in grads])
+        out_types = types if outs is grads else (c_i32 * n)(*[_TYPES[o.dtype] for o in outs])
     except KeyError:
         raise TypeError("tensors must be float32, bfloat16 or float16") from None
+    pointers = (c_vp * n)(*map(T.data_ptr, grads))
+    out_pointers = pointers if outs is grads else (c_vp * n)(*map(T.data_ptr, outs))
+    sizes = (c_i64 * n)(*map(T.numel, grads))
     L = _lib()
     with _on(grads[0]):
         need = L.spgemm_clip_grad_norm_workspace(n)
         work = torch.empty(need, dtype=torch.uint8, device=dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(L.spgemm_clip_grad_norm(
-            n, (c_vp * n)(*[g.data_ptr() for g in grads]), (c_vp * n)(*[o.data_ptr() for o in outs]),
-            (c_i64 * n)(*[g.numel() for g in grads]), (c_i32 * n)(*[t[0] for t in types]),
-            (c_i32 * n)(*[t[1] for t in types]), float(max_norm), norm.data_ptr(),
-            work.data_ptr(), need, _stream(norm)))
+        _check(L.spgemm_clip_grad_norm(n, pointers, out_pointers, sizes, types, out_types,
+                                       float(max_norm), norm.data_ptr(), work.data_ptr(), need,
+                                       _stream(norm)))
     return norm
