@@ -17,26 +17,27 @@ stream of the tensors' device, asynchronously.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
 import torch
 
-from ._expert_abi import ExpertsDesc, RouteOptions, c_i32, c_i64, c_vp
+import spgemm_symbolic_row_amd as _package
+
+from ._expert_abi import ExpertsDesc, RouteOptions, c_i64
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 2, torch.float16: 3}
 
 
 def _lib():
-    from . import lib
-    return lib()
+    return _package._lib or _package.lib()
 
 
 def _check(status):
     if status:
-        from . import _check as check
-        check(status)
+        _package._check(status)
 
 
 _HERE = nullcontext()
@@ -50,7 +51,14 @@ def _on(x):
     return _HERE if i == torch.cuda.current_device() else torch.cuda.device(i)
 
 
+# The current stream's handle by device index, without a Stream object around
+# it (2 us of a call's 10) where torch has that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(x):
+    if _raw_stream is not None:
+        return _raw_stream(x.get_device())
     return torch.cuda.current_stream(x.device).cuda_stream
 
 
@@ -261,7 +269,7 @@ def experts_backward(grad_y, kept):
 def clip_grad_norm(grads, max_norm, out=None):
     """The 2-norm over all the tensors (a float32 scalar on the device), and
     the tensors scaled by min(1, max_norm / (norm + 1e-6)): in place, or into
-    the tensors of `out`.  Contiguous float32, bfloat16 or float16 tensors of
+    the tensors of `out`, of as many elements each.  Contiguous float32, bfloat16 or float16 tensors of
     one device, mixed at will."""
     grads = list(grads)
     outs = grads if out is None else list(out)
@@ -273,24 +281,24 @@ def clip_grad_norm(grads, max_norm, out=None):
     T = torch.Tensor
     if len(set(map(T.get_device, grads)) | set(map(T.get_device, outs))) != 1:
         raise TypeError("tensors must be on one device")
-    if outs is not grads and [g.shape for g in grads] != [o.shape for o in outs]:
-        raise ValueError("out must have the shapes of grads")
+    sizes = array("q", map(T.numel, grads))
+    if outs is not grads and sizes != array("q", map(T.numel, outs)):
+        raise ValueError("out must have as many elements as grads, each")
     if not (all(map(T.is_contiguous, grads)) and all(map(T.is_contiguous, outs))):
         raise TypeError("tensors must be contiguous")
     try:
-        types = (c_i32 * n)(*[_TYPES[g.dtype] for g in grads])
-        out_types = types if outs is grads else (c_i32 * n)(*[_TYPES[o.dtype] for o in outs])
+        types = array("i", [_TYPES[g.dtype] for g in grads])
+        out_types = types if outs is grads else array("i", [_TYPES[o.dtype] for o in outs])
     except KeyError:
         raise TypeError("tensors must be float32, bfloat16 or float16") from None
-    pointers = (c_vp * n)(*map(T.data_ptr, grads))
-    out_pointers = pointers if outs is grads else (c_vp * n)(*map(T.data_ptr, outs))
-    sizes = (c_i64 * n)(*map(T.numel, grads))
+    pointers = array("Q", map(T.data_ptr, grads))
+    out_pointers = pointers if outs is grads else array("Q", map(T.data_ptr, outs))
+    tables = [t.buffer_info()[0] for t in (pointers, out_pointers, sizes, types, out_types)]
     L = _lib()
     with _on(grads[0]):
         need = L.spgemm_clip_grad_norm_workspace(n)
         work = torch.empty(need, dtype=torch.uint8, device=dev)
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(L.spgemm_clip_grad_norm(n, pointers, out_pointers, sizes, types, out_types,
-                                       float(max_norm), norm.data_ptr(), work.data_ptr(), need,
-                                       _stream(norm)))
+        _check(L.spgemm_clip_grad_norm(n, *tables, float(max_norm), norm.data_ptr(),
+                                       work.data_ptr(), need, _stream(norm)))
     return norm
