@@ -197,6 +197,7 @@ struct ProductArgs {
   int Kpad;
   int F, Fpad;
   void* c;           // 16-bit or fp32 result
+  float* scales;     // of rows held as scaled fp16
   int64_t ldc, c_expert;
   float* g;          // fp32 pre-activations, Fpad to a row
   float* u;
@@ -270,6 +271,61 @@ struct Tile {
 
 // Positions of the sorted token list that a weight gradient keeps in LDS.
 constexpr int kListLen = 4096;
+
+// Rows that are summed per token (of y and of dx) are written by one kernel and
+// read by another.  For bfloat16 tensors they are held as fp16, each 64 columns
+// with a power of two that brings their largest finite value to [2^14, 2^15):
+// 11 bits where the sum is rounded to 8 in the end, which adds 1/64 of that
+// rounding's variance, for half the bytes (the sum 236 -> 120 us, W_out's
+// product 730 -> 660 us at 131,072 rows of 2048).  float16 tensors have 11 bits
+// themselves: their rows stay in fp32.
+template <typename T>
+constexpr bool kRows16 = std::is_same<T, __bf16>::value;
+constexpr int kScaleCols = 64;
+__host__ __device__ inline int64_t scale_blocks(int64_t cols) {
+  return (cols + kScaleCols - 1) / kScaleCols;
+}
+
+// Maximum over 8 consecutive lanes, in all of them.
+__device__ __forceinline__ uint32_t max_of_8(uint32_t x) {
+  x = max(x, dpp_or_zero<0xb1, 0xf>(x));   // quad_perm: 1 0 3 2
+  x = max(x, dpp_or_zero<0x4e, 0xf>(x));   // quad_perm: 2 3 0 1
+  return max(x, dpp_or_zero<0x141, 0xf>(x));  // row_half_mirror
+}
+
+// Sum over kLanes = 8 or 16 consecutive lanes, in all of them.
+template <int kLanes>
+__device__ __forceinline__ float sum_of_lanes(float x) {
+  x = dpp_add<0xb1, 0xf>(x);
+  x = dpp_add<0x4e, 0xf>(x);
+  x = dpp_add<0x141, 0xf>(x);
+  if constexpr (kLanes == 16) x = dpp_add<0x140, 0xf>(x);  // row_mirror
+  return x;
+}
+
+// 8 of a row's 64 columns, in 8 consecutive lanes, to fp16 with their scale;
+// returns what the stored values are to be multiplied by.
+__device__ __forceinline__ float scale_to_f16(const float v[8], s16x8& out) {
+  float most = fabsf(v[0]);  // NaN is passed over
+#pragma unroll
+  for (int j = 1; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
+  uint32_t m = max_of_8(__float_as_uint(most));
+  if (__ballot(m >= 0x7f800000u)) {  // infinities: the largest finite value counts
+    m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
+      m = max(m, b < 0x7f800000u ? b : 0u);
+    }
+    m = max_of_8(m);
+  }
+  // The exponent is kept where both powers of two are normal.
+  const uint32_t e = min(max(m >> 23, 15u), 254u);
+  const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = __builtin_bit_cast(short, (_Float16)(v[j] * up));
+  return down;
+}
 
 template <typename F, int... kI>
 __device__ __forceinline__ void for_each_index(F& f, std::integer_sequence<int, kI...>) {
@@ -586,8 +642,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   constexpr int kPass = 32 / R;
   float* stg = (float*)smem + wave * 32 * kPitch;
   const int lr = l / kLanes, lc = l % kLanes * 8;
-  const int x = t.n0 + wn * kCols + lc;
-  auto row_of = [&](int m, int p) { return wm * HM + m * 32 + p * R + lr; };
+  const float* src = stg + lr * kPitch + lc;
   auto stage_block = [&](auto block) {
     constexpr int m = decltype(block)::value;
     __builtin_amdgcn_wave_barrier();
@@ -602,103 +657,139 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       }
     __builtin_amdgcn_wave_barrier();
   };
+  // Rows and columns of the result that this tile may write, from the wave's
+  // first; all the wave's columns and rows in a full tile, whose code has no
+  // branches, so that its LDS reads and stores overlap (one wave to a SIMD
+  // hides nothing otherwise).
+  const int xw = t.n0 + wn * kCols;  // the wave's first column
+  const int rows_left = (kWGrad ? a.M - t.m0 : t.rows) - wm * HM;
+  const int cols_all = KIND == kIn || KIND == kGradH ? a.Fpad
+                       : KIND == kOut || KIND == kGradX ? (int)a.ldc : a.N;
+  const int cols_left = cols_all - xw;
+  const bool vec = kWGrad ? a.ldc % 8 == 0 && (uintptr_t)a.c % 16 == 0
+                   : KIND == kGradH || KIND == kIn ? a.F % 8 == 0 : true;
+  const bool full = rows_left >= HM && cols_left >= kCols && vec;
+  // First row of the wave in the result.
+  const int64_t row_w = (kWGrad ? t.m0 : t.row0) + wm * HM;
   if constexpr (KIND == kGradH) {
-    // g, u and w of the next 4 passes are loaded while these 4 are worked on:
-    // one wave to a SIMD hides no latency otherwise.
+    // g, u and w of the next 4 passes are loaded while these 4 are worked on.
     constexpr int kUnit = 4, kUnits = MT * kPass / kUnit;
-    float g[2][kUnit][8], u[2][kUnit][8], w[2][kUnit];
-    const int xc = min(x, a.Fpad - 8);
-    auto fetch = [&](int unit, int buf) {
+    auto epilogue = [&](auto is_full) {
+      constexpr bool kFull = decltype(is_full)::value;
+      float g[2][kUnit][8], u[2][kUnit][8], w[2][kUnit];
+      // A wave all of whose rows are outside reads the tile's last one.
+      const int rmax = rows_left - 1;
+      const uint32_t lane_at = (uint32_t)(lr * a.Fpad + lc);
+      auto fetch = [&](int unit, int buf) {
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        const int p = unit * kUnit + i;
-        const int64_t row = t.row0 + min(row_of(p / kPass, p % kPass), t.rows - 1);
-        load8(a.g + row * a.Fpad + xc, g[buf][i]);
-        load8(a.u + row * a.Fpad + xc, u[buf][i]);
-        w[buf][i] = a.d.w[row];
-      }
-    };
-    fetch(0, 0);
-    wait_slice<63>();
-    auto unit = [&](auto index) {
-      constexpr int c = decltype(index)::value, buf = c % 2, m = c * kUnit / kPass;
-      if constexpr (c + 1 < kUnits) fetch(c + 1, 1 - buf);
-      if constexpr (c * kUnit % kPass == 0) stage_block(std::integral_constant<int, m>{});
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        const int p = c * kUnit % kPass + i, r = row_of(m, p);
-        const bool inside = r < t.rows && x < a.Fpad;
-        float v[8], dg[8], du[8], hv[8], dot = 0.0f;
-        load8(stg + (p * R + lr) * kPitch + lc, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float gj = g[buf][i][j], uj = u[buf][i][j], ww = w[buf][i];
-          const float s = fast_sigmoid(gj);
-          const float silu = gj * s, h = silu * uj, dh = ww * v[j];
-          dot += h * v[j];
-          dg[j] = dh * uj * s * (1.0f + gj * (1.0f - s));
-          du[j] = dh * silu;
-          hv[j] = ww * h;
+        for (int i = 0; i < kUnit; ++i) {
+          const int r0 = (unit * kUnit + i) * R;
+          if constexpr (kFull) {
+            const int64_t base = (row_w + r0) * a.Fpad + xw;
+            load8(a.g + base + lane_at, g[buf][i]);
+            load8(a.u + base + lane_at, u[buf][i]);
+            w[buf][i] = a.d.w[row_w + r0 + lr];
+          } else {
+            const int64_t row = row_w + min(r0 + lr, rmax);
+            const int64_t at = row * a.Fpad + min(xw + lc, a.Fpad - 8);
+            load8(a.g + at, g[buf][i]);
+            load8(a.u + at, u[buf][i]);
+            w[buf][i] = a.d.w[row];
+          }
         }
-        if (inside) {
-          const int64_t row = t.row0 + r;
-          const bool vec = a.F % 8 == 0;
-          T* o = (T*)a.c + row * a.ldc + x;
-          store8((T*)a.hw + row * a.Fpad + x, true, 8, hv);
-          store8(o, vec, a.F - x, dg);
-          store8(o + a.F, vec, a.F - x, du);
-        } else {
-          dot = 0.0f;
-        }
+      };
+      fetch(0, 0);
+      wait_slice<63>();
+      auto unit = [&](auto index) {
+        constexpr int c = decltype(index)::value, buf = c % 2, m = c * kUnit / kPass;
+        if constexpr (c + 1 < kUnits) fetch(c + 1, 1 - buf);
+        if constexpr (c * kUnit % kPass == 0) stage_block(std::integral_constant<int, m>{});
 #pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) dot += __shfl_xor(dot, d);
-        const int part = t.n0 / HN + wn;
-        if (lc == 0 && r < t.rows && part < a.parts)
-          a.dval_part[(int64_t)(t.row0 + r) * a.parts + part] = dot;
-      }
+        for (int i = 0; i < kUnit; ++i) {
+          const int p = c * kUnit % kPass + i, r = (c * kUnit + i) * R;
+          const bool inside = kFull || (r + lr < rows_left && lc < cols_left);
+          float v[8], dg[8], du[8], hv[8], dot = 0.0f;
+          load8(src + p * R * kPitch, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float gj = g[buf][i][j], uj = u[buf][i][j], ww = w[buf][i];
+            const float s = fast_sigmoid(gj);
+            const float silu = gj * s, h = silu * uj, dh = ww * v[j];
+            dot += h * v[j];
+            dg[j] = dh * uj * s * (1.0f + gj * (1.0f - s));
+            du[j] = dh * silu;
+            hv[j] = ww * h;
+          }
+          if (inside) {
+            const int64_t row = row_w + r + lr;
+            T* o = (T*)a.c + row * a.ldc + xw + lc;
+            store8((T*)a.hw + row * a.Fpad + xw + lc, true, 8, hv);
+            store8(o, vec, a.F - xw - lc, dg);
+            store8(o + a.F, vec, a.F - xw - lc, du);
+          } else {
+            dot = 0.0f;
+          }
+          dot = sum_of_lanes<kLanes>(dot);
+          const int part = t.n0 / HN + wn;
+          if (lc == 0 && r + lr < rows_left && part < a.parts)
+            a.dval_part[(row_w + r + lr) * a.parts + part] = dot;
+        }
+      };
+      for_each_index<kUnits>(unit);
     };
-    for_each_index<kUnits>(unit);
+    if (full) epilogue(std::true_type{});
+    else epilogue(std::false_type{});
   } else {
     wait_slice<0>();
-    auto block = [&](auto index) {
-      constexpr int m = decltype(index)::value;
-      stage_block(index);
+    auto epilogue = [&](auto is_full) {
+      constexpr bool kFull = decltype(is_full)::value;
+      const int64_t ld = KIND == kIn ? a.Fpad : a.ldc;
+      const uint32_t lane_at = (uint32_t)lr * (uint32_t)ld + lc;
+      auto block = [&](auto index) {
+        constexpr int m = decltype(index)::value;
+        stage_block(index);
 #pragma unroll
-      for (int p = 0; p < kPass; ++p) {
-        const int r = row_of(m, p);
-        const float* src = stg + (p * R + lr) * kPitch + lc;
-        float v[8];
-        load8(src, v);
-        if constexpr (KIND == kIn) {
-          float u[8], h[8];
-          load8(src + kCols, u);
+        for (int p = 0; p < kPass; ++p) {
+          const int r = m * 32 + p * R;
+          const bool inside = kFull || (r + lr < rows_left && lc < cols_left);
+          const int64_t base = (row_w + r) * ld + xw + (kWGrad ? t.expert * a.c_expert : 0);
+          float v[8];
+          load8(src + p * R * kPitch, v);
+          if constexpr (KIND == kIn) {
+            float u[8], h[8];
+            load8(src + p * R * kPitch + kCols, u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = v[j] * fast_sigmoid(v[j]) * u[j];
-          if (x + 8 > a.F) {  // columns that fill a row up hold zeros
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (x + j >= a.F) v[j] = u[j] = h[j] = 0.0f;
-          }
-          if (r < t.rows && x < a.Fpad) {
-            const int64_t at = (int64_t)(t.row0 + r) * a.Fpad + x;
-            store8((T*)a.c + at, true, 8, h);
-            if (a.g) {
-              store8(a.g + at, true, 8, v);
-              store8(a.u + at, true, 8, u);
+            for (int j = 0; j < 8; ++j) {
+              // Columns that fill a row up hold zeros.
+              if (!kFull && xw + lc + j >= a.F) v[j] = u[j] = 0.0f;
+              h[j] = v[j] * fast_sigmoid(v[j]) * u[j];
             }
+            if (inside) {
+              store8((T*)a.c + base + lane_at, true, 8, h);
+              if (a.g) {
+                store8(a.g + base + lane_at, true, 8, v);
+                store8(a.u + base + lane_at, true, 8, u);
+              }
+            }
+          } else if constexpr ((KIND == kOut || KIND == kGradX) && kRows16<T>) {
+            s16x8 h;
+            const float down = scale_to_f16(v, h);
+            if (inside) {
+              *(s16x8*)((_Float16*)a.c + base + lane_at) = h;
+              if (lc % kScaleCols == 0)
+                a.scales[(row_w + r + lr) * scale_blocks(a.ldc) + (xw + lc) / kScaleCols] = down;
+            }
+          } else if constexpr (KIND == kOut || KIND == kGradX) {
+            if (inside) store8((float*)a.c + base + lane_at, true, 8, v);
+          } else {
+            if (inside) store8((T*)a.c + base + lane_at, vec, cols_left - lc, v);
           }
-        } else if constexpr (KIND == kOut || KIND == kGradX) {
-          if (r < t.rows && x < a.ldc)
-            store8((float*)a.c + (int64_t)(t.row0 + r) * a.ldc + x, true, 8, v);
-        } else {
-          const int row = t.m0 + r;
-          if (row < a.M && x < a.N)
-            store8((T*)a.c + t.expert * a.c_expert + (int64_t)row * a.ldc + x,
-                   a.ldc % 8 == 0 && (uintptr_t)a.c % 16 == 0, a.N - x, v);
         }
-      }
+      };
+      for_each_index<MT>(block);
     };
-    for_each_index<MT>(block);
+    if (full) epilogue(std::true_type{});
+    else epilogue(std::false_type{});
   }
 }
 
@@ -914,28 +1005,37 @@ __global__ __launch_bounds__(kFewTokenWaves * kWave) void k_few_token(ProductArg
 // ---- sums over a token's entries ----
 
 // out[t] = sum over its entries of w * rows[pos] (w = 1 without val), in the
-// entries' order, in fp32, rounded once.  One work group per token and 1024
-// columns, 4 columns to a thread.
-template <typename T>
+// entries' order, in fp32, rounded once.  8 columns to a thread.
+template <typename T, bool k16>
 __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int Dpad,
-                                                 const float* __restrict__ rows,
+                                                 const void* __restrict__ rows,
+                                                 const float* __restrict__ scales,
                                                  const int32_t* __restrict__ pos,
                                                  const float* __restrict__ val,
                                                  T* __restrict__ out) {
-  const int blocks = (Dpad + 1023) / 1024;
-  const int64_t t = blockIdx.x / blocks;
-  const int x = (blockIdx.x % blocks) * 1024 + (int)threadIdx.x * 4;
-  if (x >= D) return;
-  float s[4] = {0, 0, 0, 0};
-  for (int i = 0; i < k; ++i) {
-    const int p = pos[t * k + i];
-    if (p < 0) continue;
-    const float w = val ? val[t * k + i] : 1.0f;
-    const f32x4 v = *(const f32x4*)(rows + (int64_t)p * Dpad + x);
+  const int per = Dpad / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / per;
+  if (t >= Tn) return;
+  const int x = (int)(i - t * per) * 8;
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+  for (int e = 0; e < k; ++e) {
+    const int p = pos[t * k + e];
+    const int64_t row = max(p, 0);  // read in any case, so that the loads do not wait
+    float w = val ? val[t * k + e] : 1.0f, v[8];
+    if constexpr (k16) {
+      const s16x8 h = *(const s16x8*)((const _Float16*)rows + row * Dpad + x);
+      w *= scales[row * scale_blocks(Dpad) + x / kScaleCols];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j] += w * v[j];
+      for (int j = 0; j < 8; ++j) v[j] = (float)__builtin_bit_cast(_Float16, (short)h[j]);
+    } else {
+      load8((const float*)rows + row * Dpad + x, v);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += p < 0 ? 0.0f : w * v[j];
   }
-  store4(out + t * D + x, D % 4 == 0 && (uintptr_t)out % 8 == 0, D - x, s);
+  store8(out + t * D + x, D % 8 == 0 && (uintptr_t)out % 16 == 0, D - x, s);
 }
 
 // dval[entry] = the sum of its partial sums, in order; 0 where there is none.
@@ -1059,6 +1159,7 @@ struct ForwardWork {
   int32_t* tmp;
   uint16_t* h;
   float* rows;
+  float* scales;
   Padded pad;
 };
 
@@ -1068,6 +1169,7 @@ ForwardWork take_forward(Carver& c, const Sizes& z, bool keep, bool padded) {
   w.tmp = c.take<int32_t>(dispatch_tmp_elems(z.n, z.E));
   w.h = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
+  w.scales = c.take<float>(z.n * scale_blocks(z.Dp));
   if (padded) w.pad = take_padded(c, z, false);
   return w;
 }
@@ -1076,6 +1178,7 @@ struct BackwardWork {
   uint16_t* dgu;
   uint16_t* hw;
   float* rows;
+  float* scales;
   float* part;
   Padded pad;
 };
@@ -1088,6 +1191,7 @@ BackwardWork take_backward(Carver& c, const Sizes& z, bool padded) {
   w.dgu = c.take<uint16_t>(z.n * z.S2);
   w.hw = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
+  w.scales = c.take<float>(z.n * scale_blocks(z.Dp));
   w.part = c.take<float>(z.n * dval_parts(z, 64));
   if (padded) w.pad = take_padded(c, z, true);
   return w;
@@ -1161,12 +1265,12 @@ ProductArgs base_args(const Sizes& z, const Dispatch& d) {
   return a;
 }
 
-template <typename T>
-void combine(const Sizes& z, const float* rows, const int32_t* pos, const float* val, void* out,
-             hipStream_t s) {
-  const int64_t blocks = (z.Dp + 1023) / 1024;
-  hipLaunchKernelGGL((k_combine<T>), dim3((unsigned)(z.T * blocks)), dim3(256), 0, s, z.T, z.k,
-                     (int)z.D, (int)z.Dp, rows, pos, val, (T*)out);
+template <typename T, bool k16>
+void combine(const Sizes& z, const void* rows, const float* scales, const int32_t* pos,
+             const float* val, void* out, hipStream_t s) {
+  hipLaunchKernelGGL((k_combine<T, k16>), dim3((unsigned)((z.T * (z.Dp / 8) + 255) / 256)),
+                     dim3(256), 0, s, z.T, z.k, (int)z.D, (int)z.Dp, rows, scales, pos, val,
+                     (T*)out);
 }
 
 template <typename T>
@@ -1230,12 +1334,14 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
                        dim3(kFewTokenWaves * kWave), 0, s, a);
     return;
   }
+  a.scales = w.scales;
   if (path == kPathFew)
     hipLaunchKernelGGL((k_few_out<T>), dim3((unsigned)(few * ((z.D + 31) / 32))), dim3(kNT), 0, s,
                        a);
   else
     product_by_rows<T, kOut>(a, z, s);
-  combine<T>(z, w.rows, kp.d.pos, val, y, s);
+  if (path == kPathFew) combine<T, false>(z, w.rows, nullptr, kp.d.pos, val, y, s);
+  else combine<T, kRows16<T>>(z, w.rows, w.scales, kp.d.pos, val, y, s);
 }
 
 template <typename T>
@@ -1281,8 +1387,9 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.Kpad = (int)z.S2;
   a.c = w.rows;
   a.ldc = z.Dp;
+  a.scales = w.scales;
   product_by_rows<T, kGradX>(a, z, s);
-  combine<T>(z, w.rows, kp.d.pos, nullptr, dx, s);
+  combine<T, kRows16<T>>(z, w.rows, w.scales, kp.d.pos, nullptr, dx, s);
   hipLaunchKernelGGL(k_dval, dim3((unsigned)((z.n + 255) / 256)), dim3(256), 0, s, z.n,
                      parts, kp.d.pos, w.part, dval);
   a = base_args(z, kp.d);
