@@ -276,8 +276,8 @@ constexpr int kListLen = 4096;
 // read by another.  For bfloat16 tensors they are held as fp16, each 64 columns
 // with a power of two that brings their largest finite value to [2^14, 2^15):
 // 11 bits where the sum is rounded to 8 in the end, which adds 1/64 of that
-// rounding's variance, for half the bytes (the sum 236 -> 120 us, W_out's
-// product 730 -> 660 us at 131,072 rows of 2048).  float16 tensors have 11 bits
+// rounding's variance, for half the bytes (the sum of 131,072 rows of 2048: 236
+// -> 130 us).  float16 tensors have 11 bits
 // themselves: their rows stay in fp32.
 template <typename T>
 constexpr bool kRows16 = std::is_same<T, __bf16>::value;
@@ -303,28 +303,42 @@ __device__ __forceinline__ float sum_of_lanes(float x) {
   return x;
 }
 
-// 8 of a row's 64 columns, in 8 consecutive lanes, to fp16 with their scale;
-// returns what the stored values are to be multiplied by.
-__device__ __forceinline__ float scale_to_f16(const float v[8], s16x8& out) {
-  float most = fabsf(v[0]);  // NaN is passed over
+// P rows, 8 of a row's 64 columns in each of 8 consecutive lanes, to fp16 with
+// their scale; `down` is what the stored values are to be multiplied by.
+template <int P>
+__device__ __forceinline__ void scale_to_f16(const float (&v)[P][8], s16x8 (&out)[P],
+                                             float (&down)[P]) {
+  uint32_t m[P];
+  bool infinite = false;
 #pragma unroll
-  for (int j = 1; j < 8; ++j) most = fmaxf(most, fabsf(v[j]));
-  uint32_t m = max_of_8(__float_as_uint(most));
-  if (__ballot(m >= 0x7f800000u)) {  // infinities: the largest finite value counts
-    m = 0;
+  for (int p = 0; p < P; ++p) {
+    float most = fabsf(v[p][0]);  // NaN is passed over
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-      m = max(m, b < 0x7f800000u ? b : 0u);
-    }
-    m = max_of_8(m);
+    for (int j = 1; j < 8; ++j) most = fmaxf(most, fabsf(v[p][j]));
+    m[p] = max_of_8(__float_as_uint(most));
+    infinite |= m[p] >= 0x7f800000u;
   }
-  // The exponent is kept where both powers of two are normal.
-  const uint32_t e = min(max(m >> 23, 15u), 254u);
-  const float up = __uint_as_float((268u - e) << 23), down = __uint_as_float((e - 14u) << 23);
+  if (__ballot(infinite)) {  // the largest finite value counts
 #pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = __builtin_bit_cast(short, (_Float16)(v[j] * up));
-  return down;
+    for (int p = 0; p < P; ++p) {
+      m[p] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(v[p][j]) & 0x7fffffffu;
+        m[p] = max(m[p], b < 0x7f800000u ? b : 0u);
+      }
+      m[p] = max_of_8(m[p]);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    // The exponent is kept where both powers of two are normal.
+    const uint32_t e = min(max(m[p] >> 23, 15u), 254u);
+    const float up = __uint_as_float((268u - e) << 23);
+    down[p] = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[p][j] = __builtin_bit_cast(short, (_Float16)(v[p][j] * up));
+  }
 }
 
 template <typename F, int... kI>
@@ -748,6 +762,29 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       auto block = [&](auto index) {
         constexpr int m = decltype(index)::value;
         stage_block(index);
+        if constexpr ((KIND == kOut || KIND == kGradX) && kRows16<T>) {
+          float v[kPass][8], down[kPass];
+          s16x8 h[kPass];
+#pragma unroll
+          for (int p = 0; p < kPass; ++p) load8(src + p * R * kPitch, v[p]);
+          scale_to_f16<kPass>(v, h, down);
+#pragma unroll
+          for (int p = 0; p < kPass; ++p) {
+            const int r = m * 32 + p * R;
+            if (kFull || (r + lr < rows_left && lc < cols_left))
+              *(s16x8*)((_Float16*)a.c + (row_w + r) * ld + xw + lane_at) = h[p];
+          }
+          if (lc % kScaleCols == 0) {
+            const int64_t blocks = scale_blocks(ld);
+#pragma unroll
+            for (int p = 0; p < kPass; ++p) {
+              const int r = m * 32 + p * R + lr;
+              if (kFull || (r < rows_left && lc < cols_left))
+                a.scales[(row_w + r) * blocks + (xw + lc) / kScaleCols] = down[p];
+            }
+          }
+          return;
+        }
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
           const int r = m * 32 + p * R;
@@ -770,14 +807,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
                 store8(a.g + base + lane_at, true, 8, v);
                 store8(a.u + base + lane_at, true, 8, u);
               }
-            }
-          } else if constexpr ((KIND == kOut || KIND == kGradX) && kRows16<T>) {
-            s16x8 h;
-            const float down = scale_to_f16(v, h);
-            if (inside) {
-              *(s16x8*)((_Float16*)a.c + base + lane_at) = h;
-              if (lc % kScaleCols == 0)
-                a.scales[(row_w + r + lr) * scale_blocks(a.ldc) + (xw + lc) / kScaleCols] = down;
             }
           } else if constexpr (KIND == kOut || KIND == kGradX) {
             if (inside) store8((float*)a.c + base + lane_at, true, 8, v);
