@@ -519,13 +519,13 @@ spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
                                      void *stream);
 
 /* Gradients of x (T x D), w_in, w_out (in the tensors' type) and of the
- * values (T x k, fp32, 0 in empty slots).  Every element is written: 0 for
+ * values (T x k, fp32, 0 in empty slots), for the routing that the forward pass
+ * was given (the kept block holds it).  Every element is written: 0 for
  * experts without tokens.  Sums in fp32, in an order that only the routing
  * fixes: the same call gives the same bits. */
 spgemm_status spgemm_experts_backward(
     const spgemm_experts_desc *desc, const void *dX, const void *dWIn,
-    const void *dWOut, const float *dVal, const void *dGradY,
-    const void *dKept, void *dGradX, void *dGradWIn, void *dGradWOut,
+    const void *dWOut, const void *dGradY, const void *dKept, void *dGradX, void *dGradWIn, void *dGradWOut,
     float *dGradVal, void *dWork, int64_t work_bytes, void *stream);
 
 /* The global norm of `count` tensors (fp32, bf16 or fp16, mixed at will) and

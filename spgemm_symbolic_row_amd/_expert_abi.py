@@ -35,7 +35,7 @@ def declare(L):
     L.spgemm_experts_forward.restype = st
     L.spgemm_experts_forward.argtypes = [ctypes.POINTER(ExpertsDesc)] + [c_vp] * 8 + [c_i64, c_vp]
     L.spgemm_experts_backward.restype = st
-    L.spgemm_experts_backward.argtypes = [ctypes.POINTER(ExpertsDesc)] + [c_vp] * 11 + [c_i64, c_vp]
+    L.spgemm_experts_backward.argtypes = [ctypes.POINTER(ExpertsDesc)] + [c_vp] * 10 + [c_i64, c_vp]
     L.spgemm_clip_grad_norm_workspace.restype = c_i64
     L.spgemm_clip_grad_norm_workspace.argtypes = [c_i64]
     L.spgemm_clip_grad_norm.restype = st

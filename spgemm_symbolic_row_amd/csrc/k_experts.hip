@@ -359,6 +359,14 @@ struct Stages {
   static constexpr int kA = kWGrad ? 2 : 3, kB = !kWGrad && BM < BN ? 3 : 2;
 };
 
+// Whether a work group takes tiles in turn, or there is one for every tile.  In
+// turn: the weight gradients 741 -> 638 us and 355 -> 328 us (their experts'
+// unequal rows are shared out), the first product 1108 -> 970-990 us; not where
+// the loop leaves too few registers: dx's product 514 -> 560 us, the hidden
+// gradient 417 -> 470 us.
+template <int KIND>
+constexpr bool kTurns = KIND == kIn || KIND == kGradWOut || KIND == kGradWIn;
+
 // kFar: the gathered rows span 4 GB or more, so that their offsets are 64-bit
 // pointers; those cost 7% of the main loop.
 template <typename T, int KIND, int BM, int BN, bool kFar>
@@ -381,11 +389,27 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
   const int cols = (a.N + kNStep - 1) / kNStep;
   const int row_tiles = kWGrad ? a.E * ((a.M + BM - 1) / BM) : *a.d.ntiles;
-  // Work groups go round-robin to the XCDs: XCD x takes a contiguous share.
-  const int total = row_tiles * cols, share = (total + kXcds - 1) / kXcds;
-  const int first = ((int)blockIdx.x % kXcds) * share, last = min(total, first + share);
-  const int lin = first + (int)blockIdx.x / kXcds;
-  if (lin >= last) return;
+  // Work groups go round-robin to the XCDs: XCD x takes a contiguous share of
+  // the tiles, and its work groups take them in turn.  The tiles of a weight
+  // gradient cost their expert's rows, so there the shares are of rows, where
+  // more tiles than work groups repay the look-ups (about 5 us).
+  const int total = row_tiles * cols, xcd = (int)blockIdx.x % kXcds;
+  auto share_start = [&](int x) {
+    if (!kWGrad || total <= (int)gridDim.x)
+      return min(total, x * ((total + kXcds - 1) / kXcds));
+    if (x == 0) return 0;
+    if (x == kXcds) return total;
+    const int32_t* rp = a.d.row_ptr;
+    const int64_t at = (int64_t)rp[a.E] * x / kXcds;
+    const int64_t e = wave_last_le(rp, (int64_t)0, (int64_t)a.E, at);
+    const int64_t rows = rp[e + 1] - rp[e], per = total / a.E;
+    return (int)(e * per + (rows ? (at - rp[e]) * per / rows : 0));
+  };
+  const int last = __builtin_amdgcn_readfirstlane(share_start(xcd + 1));
+  int lin = __builtin_amdgcn_readfirstlane(share_start(xcd)) + (int)blockIdx.x / kXcds;
+#pragma unroll 1
+  for (; lin < last; lin += (int)gridDim.x / kXcds) {
+  if constexpr (kTurns<KIND>) __syncthreads();  // the last tile's rows have left LDS
 
   Tile t;
   {
@@ -543,13 +567,16 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     for (int s = 0; s < 2; ++s) {
       fetch_tokens(s);
 #pragma unroll
-      for (int i = 0; i < AL; ++i)
-        load_to_lds(stage_a(s) + (i * kWaves + wave) * 1024,
-                    inside_a(s, i) ? (const void*)addr_a(s, i) : (const void*)zeros16);
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < BL; ++i)
-        load_to_lds(stage_b(s) + (i * kWaves + wave) * 1024,
-                    inside_b(s, i) ? (const void*)addr_b(s, i) : (const void*)zeros16);
+        for (int i = h * AL / 2; i < (h + 1) * AL / 2; ++i)
+          load_to_lds(stage_a(s) + (i * kWaves + wave) * 1024,
+                      inside_a(s, i) ? (const void*)addr_a(s, i) : (const void*)zeros16);
+#pragma unroll
+        for (int i = h * BL / 2; i < (h + 1) * BL / 2; ++i)
+          load_to_lds(stage_b(s) + (i * kWaves + wave) * 1024,
+                      inside_b(s, i) ? (const void*)addr_b(s, i) : (const void*)zeros16);
+      }
       if constexpr (kFar) {
 #pragma unroll
         for (int i = 0; i < AL; ++i) aptr[i] += kBK * 2;
@@ -563,7 +590,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // longer needed in LDS, and the next one has to be there.  Half 1
     // multiplies its fragments and reads the next slice's first ones.  The
     // loads of the slice after that go into half 0 where the operand has a
-    // third stage, into half 1 where it takes the place of this slice.
+    // third stage, into half 1 where it takes the place of this slice.  In a
+    // weight gradient the halves of a slice are k-rows of their own, so each
+    // takes the place of its like as soon as that has been read: four stages of
+    // half a slice, with a barrier after either half (1,200 cycles more than
+    // with all loads in half 1 for one to arrive).
     s16x8 fa[2][2][MT], fb[2][2][NT];  // [half][16 k of it][]
     wait_loads<AL + BL>();
 #pragma unroll
@@ -579,8 +610,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     auto half = [&](int s, auto which, auto checked) {
       constexpr int P = decltype(which)::value, Q = 1 - P;
       constexpr bool kCheck = decltype(checked)::value;
-      constexpr bool kLoadA = P == 0 ? AS == 3 : AS == 2, kLoadB = P == 0 ? BS == 3 : BS == 2;
-      constexpr int kLoadsA = kLoadA ? AL : 0, kLoads = kLoadsA + (kLoadB ? BL : 0);
+      constexpr bool kLoadA = kWGrad || (P == 0 ? AS == 3 : AS == 2);
+      constexpr bool kLoadB = kWGrad || (P == 0 ? BS == 3 : BS == 2);
+      constexpr int kShare = kWGrad ? 2 : 1;
+      constexpr int kLoadsA = kLoadA ? AL / kShare : 0;
+      constexpr int kLoads = kLoadsA + (kLoadB ? BL / kShare : 0);
       const uint32_t ra = la[P], rb = lb[P];
       const uint32_t wa = la[2] + wave * 1024, wb = lb[2] + wave * 1024;
       constexpr int kAll = 2 * MT * NT, kReads = 2 * (MT + NT);
@@ -593,10 +627,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         constexpr int x = i * kLoads / kSpan;
         if constexpr (x < kLoads && x != (i + 1) * kLoads / kSpan) {
           constexpr bool kA = x < kLoadsA;
-          constexpr int y = kA ? x : x - kLoadsA;
+          constexpr int y = (kA ? x : x - kLoadsA) + (kWGrad ? P * (kA ? AL : BL) / 2 : 0);
           if constexpr (kCheck) {
-            const char* p = kA ? (inside_a(s + 2, y) ? addr_a(s + 2, y) : (const char*)zeros16)
-                               : (inside_b(s + 2, y) ? addr_b(s + 2, y) : (const char*)zeros16);
+            const char* p = kA ? addr_a(s + 2, y) : addr_b(s + 2, y);
+            asm volatile("" : "+v"(p));  // both sides at hand: a select, no branch
+            if (!(kA ? inside_a(s + 2, y) : inside_b(s + 2, y))) p = (const char*)zeros16;
             mfma_load<y * kWaves * 1024>(T{}, fb[P][kb][n], fa[P][kb][m], acc[m][n], kA ? wa : wb,
                                          p);
           } else if constexpr (kA ? kFar || (kACol && kAGather) : kBGather) {
@@ -620,17 +655,18 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         __builtin_amdgcn_sched_barrier(0);
       };
       for_each_index<kAll>(step);
-      if constexpr (kLoadA) next_a();
-      if constexpr (kLoadB) next_b();
+      if constexpr (kLoadA && (P == 1 || !kWGrad)) next_a();
+      if constexpr (kLoadB && (P == 1 || !kWGrad)) next_b();
     };
     const int full = K / kBK;  // slices without an end of K
     auto slice = [&](int s, auto checked) {
       half(s, std::integral_constant<int, 0>{}, checked);
-      wait_slice<(AS == 3 ? AL : 0) + (BS == 3 ? BL : 0)>();
+      wait_slice<kWGrad ? AL + BL : (AS == 3 ? AL : 0) + (BS == 3 ? BL : 0)>();
       if constexpr (kWGrad) {
         if (((s + 3) * kBK) % kListLen == 0) fill_list(s + 3);
       }
       half(s, std::integral_constant<int, 1>{}, checked);
+      if constexpr (kWGrad) wait_slice<AL + BL>();
       fetch_tokens(s + 3);
       const uint32_t fa0 = AS == 3 ? la[0] : la[1], fb0 = BS == 3 ? lb[0] : lb[1];
       la[0] = la[1], la[1] = la[2], la[2] = fa0;
@@ -820,6 +856,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     if (full) epilogue(std::true_type{});
     else epilogue(std::false_type{});
   }
+  if constexpr (!kTurns<KIND>) break;
+  }  // tiles
 }
 
 template <typename T, int KIND, int BM, int BN, bool kFar = false>
@@ -829,8 +867,10 @@ void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   (void)once;
   const int64_t step = KIND == kIn ? BN / 2 : BN;
   const int64_t tiles = row_tiles * ((a.N + step - 1) / step);
-  const int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid == 0) return;
+  if (tiles == 0) return;
+  int64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
+  // In turn: a work group for every compute unit, or the two that fit one.
+  if (kTurns<KIND>) grid = std::min<int64_t>(grid, BN == 256 ? 256 : 512);
   typedef Stages<KIND, BM, BN> S;
   const size_t lds =
       (S::kA * BM + S::kB * BN) * kBK * 2 + (S::kWGrad ? kListLen * sizeof(int32_t) : 0);
@@ -1471,6 +1511,7 @@ spgemm_status check_desc(const spgemm_experts_desc* d) {
       2 * round8(d->hidden) * round8(d->width) >= (int64_t)1 << 31 ||
       d->tokens > INT32_MAX / d->k ||
       d->tokens * d->k / 128 + d->experts > INT32_MAX / ((d->width + d->hidden) / 128 + 1) / 2 ||
+      d->tokens > INT32_MAX / (d->width / 2048 + 1) ||
       d->experts * ((d->width + 255) / 256 + 1) * ((2 * d->hidden + 255) / 256 + 1) >
           INT32_MAX / 2)
     return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "experts: too many entries or tiles");
@@ -1540,13 +1581,13 @@ extern "C" spgemm_status spgemm_experts_forward(const spgemm_experts_desc* desc,
 
 extern "C" spgemm_status spgemm_experts_backward(
     const spgemm_experts_desc* desc, const void* dX, const void* dWIn, const void* dWOut,
-    const float* dVal, const void* dGradY, const void* dKept, void* dGradX, void* dGradWIn,
+    const void* dGradY, const void* dKept, void* dGradX, void* dGradWIn,
     void* dGradWOut, float* dGradVal, void* dWork, int64_t work_bytes, void* stream) {
   const spgemm_status st = check_desc(desc);
   if (st != SPGEMM_OK) return st;
   if (!dGradWIn || !dGradWOut || !dWork ||
       (desc->tokens > 0 &&
-       (!dX || !dWIn || !dWOut || !dVal || !dGradY || !dKept || !dGradX || !dGradVal)))
+       (!dX || !dWIn || !dWOut || !dGradY || !dKept || !dGradX || !dGradVal)))
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: null array");
   if (desc->grad_ld < desc->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: a row stride below the width");

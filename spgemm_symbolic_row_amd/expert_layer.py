@@ -260,8 +260,8 @@ def experts_backward(grad_y, kept):
         gval = torch.empty_like(val)
         work = torch.empty(max(work_bytes, 1), dtype=torch.uint8, device=dev)
         _check(_lib().spgemm_experts_backward(
-            d, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), val.data_ptr(),
-            grad_y.data_ptr(), kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
+            d, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), grad_y.data_ptr(),
+            kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
             gw_out.data_ptr(), gval.data_ptr(), work.data_ptr(), work_bytes, _stream(x)))
     return gx, gw_in, gw_out, gval
 

@@ -55,9 +55,9 @@ def test_experts_refuse():
     assert f(desc(), P, P, P, P, P, P, None, P, 16, None) == -1
     assert f(desc(T=0), None, None, None, None, None, None, None, None, 0, None) == 0
     b = L.spgemm_experts_backward
-    assert b(desc(), P, P, P, P, P, None, P, P, P, P, P, 1 << 40, None) == -1
-    assert b(desc(grad_ld=8), P, P, P, P, P, P, P, P, P, P, P, 1 << 40, None) == -1
-    assert b(desc(), P, P, P, P, P, P, P, P, P, P, P, 16, None) == -1
+    assert b(desc(), P, P, P, P, None, P, P, P, P, P, 1 << 40, None) == -1
+    assert b(desc(grad_ld=8), P, P, P, P, P, P, P, P, P, P, 1 << 40, None) == -1
+    assert b(desc(), P, P, P, P, P, P, P, P, P, P, 16, None) == -1
 
 
 def test_clip_refuses():
