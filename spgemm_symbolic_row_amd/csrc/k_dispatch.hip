@@ -2,9 +2,10 @@
 // (column -1 where there is none).  The entries are counted per expert,
 // scanned, and placed stably, so that an expert's tokens rise and every sum
 // over them has one order.  Moves 4 bytes in and 16 bytes out per entry; at
-// the sizes it meets (up to some 10^5 entries) it is bound by its launches,
-// so up to kDispBlock entries take one launch of one work group, and more
-// take three.
+// the sizes it meets (up to some 10^5 entries) it is bound by its launches and
+// their chains of dependent reads, so up to 8192 entries take one launch of one
+// work group (384 entries 4.7 us, 5331 entries 10 us, where three launches took
+// 13), and more take three (131,072 entries 27 us).
 #include <algorithm>
 
 #include "expert_common.hpp"
@@ -14,24 +15,31 @@ namespace {
 
 constexpr int kDispNT = 1024;
 constexpr int kDispNW = kDispNT / kWave;
-constexpr int kDispBlock = 4096;  // entries of one work group
+constexpr int kDispBlock = 4096;  // entries of one work group of several
+constexpr int kDispOne = 8192;    // entries that one launch of one work group takes
 
-__device__ __forceinline__ int expert_of(const int32_t* col, int64_t e, int64_t n, int E) {
-  const int c = e < n ? col[e] : -1;
-  return (uint32_t)c < (uint32_t)E ? c : -1;
+// A wave's range is kIt rounds of 64 entries, held in registers: each lane's
+// expert, -1 where there is none.
+template <int kIt>
+__device__ __forceinline__ void load_experts(const int32_t* col, int64_t n, int E, int64_t first,
+                                             int (&c)[kIt]) {
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int64_t e = first + i * kWave + lane_id();
+    const int x = e < n ? col[e] : -1;
+    c[i] = (uint32_t)x < (uint32_t)E ? x : -1;
+  }
 }
 
-// Entries per expert of each wave's range of `len` entries: wc[w * E + x].
-__device__ __forceinline__ void count_waves(const int32_t* col, int64_t n, int E, int64_t e0,
-                                            int len, int32_t* wc) {
+// Entries per expert of each wave's range: wc[w * E + x].
+template <int kIt>
+__device__ __forceinline__ void count_waves(const int (&c)[kIt], int E, int32_t* wc) {
   for (int i = threadIdx.x; i < kDispNW * E; i += kDispNT) wc[i] = 0;
   __syncthreads();
-  const int w = threadIdx.x / kWave;
-  const int64_t first = e0 + (int64_t)w * len;
-  for (int i = lane_id(); i < len && first + i < n; i += kWave) {
-    const int c = expert_of(col, first + i, n, E);
-    if (c >= 0) atomicAdd(&wc[w * E + c], 1);
-  }
+  int32_t* my = wc + threadIdx.x / kWave * E;
+#pragma unroll
+  for (int i = 0; i < kIt; ++i)
+    if (c[i] >= 0) atomicAdd(&my[c[i]], 1);
   __syncthreads();
 }
 
@@ -47,22 +55,21 @@ __device__ __forceinline__ void count_to_start(int E, int x, int at, int32_t* wc
 
 // Places the work group's entries.  wc holds each wave's first position per
 // expert and is advanced.
-__device__ __forceinline__ void place(const int32_t* col, const float* val, int64_t n, int k,
-                                      int E, int bits, int64_t e0, int len, int32_t* wc,
+template <int kIt>
+__device__ __forceinline__ void place(const int (&c)[kIt], const float* val, int64_t n, int k,
+                                      int E, int bits, int64_t first, int32_t* wc,
                                       const Dispatch& d) {
-  const int w = threadIdx.x / kWave;
-  int32_t* my = wc + w * E;
-  const int64_t first = e0 + (int64_t)w * len;
-  for (int i = 0; i < len && first + i < n; i += kWave) {
-    const int64_t e = first + i + lane_id();
-    const int c = expert_of(col, e, n, E);
-    const uint64_t peers = match_key((uint32_t)c, bits, c >= 0);
+  int32_t* my = wc + threadIdx.x / kWave * E;
+#pragma unroll
+  for (int i = 0; i < kIt; ++i) {
+    const int64_t e = first + i * kWave + lane_id();
+    const uint64_t peers = match_key((uint32_t)c[i], bits, c[i] >= 0);
     int p = -1;
-    if (c >= 0) {
+    if (c[i] >= 0) {
       // The lanes of one expert read its position before the last of them
       // advances it; one wave's LDS accesses are performed in order.
-      p = my[c] + (int)__popcll(peers & lanemask_lt());
-      if (lane_id() == last_set64(peers)) my[c] = p + 1;
+      p = my[c[i]] + (int)__popcll(peers & lanemask_lt());
+      if (lane_id() == last_set64(peers)) my[c[i]] = p + 1;
       d.ent[p] = (int32_t)e;
       d.tok[p] = (int32_t)((uint32_t)e / (uint32_t)k);
       if (val) d.w[p] = val[e];
@@ -98,12 +105,16 @@ __device__ __forceinline__ int scan_experts(int E, int tile_rows, int total, con
   return start;
 }
 
+template <int kIt>
 __global__ __launch_bounds__(kDispNT) void k_dispatch_one(const int32_t* __restrict__ col,
                                                           const float* __restrict__ val,
                                                           int64_t n, int k, int E, int bits,
-                                                          int len, int tile_rows, Dispatch d) {
+                                                          int tile_rows, Dispatch d) {
   extern __shared__ int32_t wc[];  // kDispNW * E
-  count_waves(col, n, E, 0, len, wc);
+  const int64_t first = (int64_t)(threadIdx.x / kWave) * kIt * kWave;
+  int c[kIt];
+  load_experts(col, n, E, first, c);
+  count_waves(c, E, wc);
   const int x = threadIdx.x;
   int total = 0;
   if (x < E)
@@ -112,7 +123,7 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_one(const int32_t* __restr
   const int start = scan_experts(E, tile_rows, total, d);
   if (x < E) count_to_start(E, x, start, wc);
   __syncthreads();
-  place(col, val, n, k, E, bits, 0, len, wc, d);
+  place(c, val, n, k, E, bits, first, wc, d);
 }
 
 // hist[b * E + x]: entries of expert x in work group b's range.
@@ -125,8 +136,9 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_count(const int32_t* __res
   const int64_t e0 = (int64_t)blockIdx.x * kDispBlock;
 #pragma unroll
   for (int i = 0; i < kDispBlock; i += kDispNT) {
-    const int c = expert_of(col, e0 + i + threadIdx.x, n, E);
-    if (c >= 0) atomicAdd(&h[c], 1);
+    const int64_t e = e0 + i + threadIdx.x;
+    const int c = e < n ? col[e] : -1;
+    if ((uint32_t)c < (uint32_t)E) atomicAdd(&h[c], 1);
   }
   __syncthreads();
   for (int x = threadIdx.x; x < E; x += kDispNT) hist[(int64_t)blockIdx.x * E + x] = h[x];
@@ -158,13 +170,16 @@ __global__ __launch_bounds__(kDispNT) void k_dispatch_place(const int32_t* __res
                                                             const int32_t* __restrict__ hist,
                                                             Dispatch d) {
   extern __shared__ int32_t wc[];
-  constexpr int kLen = kDispBlock / kDispNW;
-  const int64_t e0 = (int64_t)blockIdx.x * kDispBlock;
-  count_waves(col, n, E, e0, kLen, wc);
+  constexpr int kIt = kDispBlock / kDispNT;
+  const int64_t first =
+      (int64_t)blockIdx.x * kDispBlock + (int64_t)(threadIdx.x / kWave) * kIt * kWave;
+  int c[kIt];
+  load_experts(col, n, E, first, c);
+  count_waves(c, E, wc);
   for (int x = threadIdx.x; x < E; x += kDispNT)
     count_to_start(E, x, hist[(int64_t)blockIdx.x * E + x], wc);
   __syncthreads();
-  place(col, val, n, k, E, bits, e0, kLen, wc, d);
+  place(c, val, n, k, E, bits, first, wc, d);
 }
 
 }  // namespace
@@ -183,10 +198,13 @@ void launch_dispatch(const int32_t* col, const float* val, int64_t n, int k, int
   while (((int64_t)1 << bits) < E) ++bits;
   const int64_t nb = (n + kDispBlock - 1) / kDispBlock;
   const size_t wcb = (size_t)kDispNW * E * sizeof(int32_t);
-  if (nb <= 1) {
-    const int len = (int)((n + kDispNT - 1) / kDispNT) * kWave;  // whole rounds of a wave
-    hipLaunchKernelGGL(k_dispatch_one, dim3(1), dim3(kDispNT), wcb, s, col, val, n, k, (int)E,
-                       bits, len, tile_rows, d);
+  if (n <= kDispOne) {
+    auto one = n <= kDispNT       ? k_dispatch_one<1>
+               : n <= 2 * kDispNT ? k_dispatch_one<2>
+               : n <= 4 * kDispNT ? k_dispatch_one<4>
+                                  : k_dispatch_one<8>;
+    hipLaunchKernelGGL(one, dim3(1), dim3(kDispNT), wcb, s, col, val, n, k, (int)E, bits,
+                       tile_rows, d);
     return;
   }
   hipLaunchKernelGGL(k_dispatch_count, dim3((unsigned)nb), dim3(kDispNT), E * sizeof(int32_t), s,
