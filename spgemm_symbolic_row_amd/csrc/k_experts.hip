@@ -527,8 +527,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
   auto fill_list = [&](int s) {
     if constexpr (kWGrad) {
       __syncthreads();
-      for (int i = threadIdx.x; i < kListLen; i += kNT)
-        list[i] = a.d.tok[t.row0 + min(s * kBK + i, K - 1)];
+      for (int i = threadIdx.x; i < min(kListLen, K - s * kBK); i += kNT)
+        list[i] = a.d.tok[t.row0 + s * kBK + i];
       __syncthreads();
     }
   };
