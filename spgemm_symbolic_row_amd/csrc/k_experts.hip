@@ -14,10 +14,10 @@
 // destination is permuted by choosing the source address:
 //   row form (K contiguous in memory): [row][64 k], 16-byte chunk c of row r
 //     at slot c ^ (r >> 1 & 7); fragments are ds_read_b128.  With r & 7 the
-//     reads ran at 54% of the rate, without the xor at 14%.
+//     reads run at 54% of the rate, without the xor at 14%.
 //   column form (K strided): [k][column], the 32-byte segment s of row k at
 //     segment s ^ 2 (k & 3); fragments are two transposing 8-byte reads.  With
-//     (k & 3) | (k >> 3 & 1) << 2 they ran at 74%, without the xor at 39%.
+//     (k & 3) | (k >> 3 & 1) << 2 they run at 50%, without the xor at 26%.
 // Rows that a tile has not, and K beyond its end, are read from a block of
 // zeros, so no tile ever multiplies foreign data.
 #include <algorithm>
@@ -491,14 +491,16 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     bc.frag_init(wn * HN);
   }
 
+  const char* acols = (const char*)abase + acol;  // gathered rows: the lane's columns
+  const char* bcols = (const char*)bbase + bcol;
   // Address of load i of slice s.
   auto addr_a = [&](int s, int i) -> const char* {
-    if constexpr (kWGrad && kAGather) return (const char*)abase + (uint64_t)aidx[i] * ((uint32_t)a.lda * 2) + acol;
+    if constexpr (kWGrad && kAGather) return acols + (uint64_t)aidx[i] * ((uint32_t)a.lda * 2);
     else if constexpr (kFar) return aptr[i];
     else return (const char*)abase + aoff[i];
   };
   auto addr_b = [&](int s, int i) -> const char* {
-    if constexpr (kBGather) return (const char*)bbase + (uint64_t)bidx[i] * ((uint32_t)a.ldb * 2) + bcol;
+    if constexpr (kBGather) return bcols + (uint64_t)bidx[i] * ((uint32_t)a.ldb * 2);
     else return (const char*)bbase + boff[i];
   };
   // Whether its K is inside.
@@ -532,14 +534,16 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       __syncthreads();
     }
   };
-  auto fetch_tokens = [&](int s) {
+  // Tokens of half h of slice s.
+  auto fetch_tokens = [&](int s, int h) {
+    const int32_t* from = list + s * kBK % kListLen;
     if constexpr (kWGrad && kAGather) {
 #pragma unroll
-      for (int i = 0; i < AL; ++i) aidx[i] = list[(s * kBK + ac.row(i)) % kListLen];
+      for (int i = h * AL / 2; i < (h + 1) * AL / 2; ++i) aidx[i] = from[ac.row(i)];
     }
     if constexpr (kBGather) {
 #pragma unroll
-      for (int i = 0; i < BL; ++i) bidx[i] = list[(s * kBK + bc.row(i)) % kListLen];
+      for (int i = h * BL / 2; i < (h + 1) * BL / 2; ++i) bidx[i] = from[bc.row(i)];
     }
   };
   auto stage_a = [&](int s) { return lds0 + (uint32_t)(s % AS) * kABytes; };
@@ -565,7 +569,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     fill_list(0);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      fetch_tokens(s);
+      fetch_tokens(s, 0);
+      fetch_tokens(s, 1);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -584,7 +589,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       next_a();
       next_b();
     }
-    fetch_tokens(2);
+    fetch_tokens(2, 0);
     // A slice has two halves of 32 k.  Half 0 multiplies the fragments of its
     // own k, read before, and reads those of half 1.  Then the slice is no
     // longer needed in LDS, and the next one has to be there.  Half 1
@@ -615,6 +620,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       constexpr int kShare = kWGrad ? 2 : 1;
       constexpr int kLoadsA = kLoadA ? AL / kShare : 0;
       constexpr int kLoads = kLoadsA + (kLoadB ? BL / kShare : 0);
+      // Tokens that the next half's loads need.
+      if constexpr (P == 0) fetch_tokens(s + 2, 1);
+      else fetch_tokens(s + 3, 0);
       const uint32_t ra = la[P], rb = lb[P];
       const uint32_t wa = la[2] + wave * 1024, wb = lb[2] + wave * 1024;
       constexpr int kAll = 2 * MT * NT, kReads = 2 * (MT + NT);
@@ -667,7 +675,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       }
       half(s, std::integral_constant<int, 1>{}, checked);
       if constexpr (kWGrad) wait_slice<AL + BL>();
-      fetch_tokens(s + 3);
       const uint32_t fa0 = AS == 3 ? la[0] : la[1], fb0 = BS == 3 ? lb[0] : lb[1];
       la[0] = la[1], la[1] = la[2], la[2] = fa0;
       lb[0] = lb[1], lb[1] = lb[2], lb[2] = fb0;
