@@ -612,17 +612,23 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // LDS offsets of slices s, s + 1, s + 2.
     uint32_t la[3] = {stage_a(0), stage_a(1), stage_a(2)};
     uint32_t lb[3] = {stage_b(0), stage_b(1), stage_b(2)};
-    auto half = [&](int s, auto which, auto checked) {
+    // Loads of slice s + 2: all of it is there, its end has to be looked for,
+    // or there is no such slice.
+    enum { kInside, kChecked, kNone };
+    auto half = [&](int s, auto which, auto loads) {
       constexpr int P = decltype(which)::value, Q = 1 - P;
-      constexpr bool kCheck = decltype(checked)::value;
-      constexpr bool kLoadA = kWGrad || (P == 0 ? AS == 3 : AS == 2);
-      constexpr bool kLoadB = kWGrad || (P == 0 ? BS == 3 : BS == 2);
+      constexpr bool kCheck = decltype(loads)::value == kChecked;
+      constexpr bool kAny = decltype(loads)::value != kNone;
+      constexpr bool kLoadA = kAny && (kWGrad || (P == 0 ? AS == 3 : AS == 2));
+      constexpr bool kLoadB = kAny && (kWGrad || (P == 0 ? BS == 3 : BS == 2));
       constexpr int kShare = kWGrad ? 2 : 1;
       constexpr int kLoadsA = kLoadA ? AL / kShare : 0;
       constexpr int kLoads = kLoadsA + (kLoadB ? BL / kShare : 0);
       // Tokens that the next half's loads need.
-      if constexpr (P == 0) fetch_tokens(s + 2, 1);
-      else fetch_tokens(s + 3, 0);
+      if constexpr (kAny) {
+        if constexpr (P == 0) fetch_tokens(s + 2, 1);
+        else fetch_tokens(s + 3, 0);
+      }
       const uint32_t ra = la[P], rb = lb[P];
       const uint32_t wa = la[2] + wave * 1024, wb = lb[2] + wave * 1024;
       constexpr int kAll = 2 * MT * NT, kReads = 2 * (MT + NT);
@@ -667,23 +673,25 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       if constexpr (kLoadB && (P == 1 || !kWGrad)) next_b();
     };
     const int full = K / kBK;  // slices without an end of K
-    auto slice = [&](int s, auto checked) {
-      half(s, std::integral_constant<int, 0>{}, checked);
-      wait_slice<kWGrad ? AL + BL : (AS == 3 ? AL : 0) + (BS == 3 ? BL : 0)>();
-      if constexpr (kWGrad) {
+    auto slice = [&](int s, auto loads) {
+      constexpr bool kAny = decltype(loads)::value != kNone;
+      constexpr int kLeft =
+          !kAny ? 0 : kWGrad ? AL + BL : (AS == 3 ? AL : 0) + (BS == 3 ? BL : 0);
+      half(s, std::integral_constant<int, 0>{}, loads);
+      wait_slice<kLeft>();
+      if constexpr (kWGrad && kAny) {
         if (((s + 3) * kBK) % kListLen == 0) fill_list(s + 3);
       }
-      half(s, std::integral_constant<int, 1>{}, checked);
-      if constexpr (kWGrad) wait_slice<AL + BL>();
+      half(s, std::integral_constant<int, 1>{}, loads);
+      if constexpr (kWGrad) wait_slice<kLeft>();
       const uint32_t fa0 = AS == 3 ? la[0] : la[1], fb0 = BS == 3 ? lb[0] : lb[1];
       la[0] = la[1], la[1] = la[2], la[2] = fa0;
       lb[0] = lb[1], lb[1] = lb[2], lb[2] = fb0;
     };
     int s = 0;
-    for (; s + 2 < full; ++s) slice(s, std::false_type{});
-    for (; s < steps; ++s) slice(s, std::true_type{});
-    // The loads of zeros beyond K must not outlive the work group's LDS.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (; s + 2 < full; ++s) slice(s, std::integral_constant<int, kInside>{});
+    for (; s + 2 < steps; ++s) slice(s, std::integral_constant<int, kChecked>{});
+    for (; s < steps; ++s) slice(s, std::integral_constant<int, kNone>{});
     settle(acc);
   }
 
