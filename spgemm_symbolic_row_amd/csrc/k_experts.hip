@@ -598,8 +598,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // third stage, into half 1 where it takes the place of this slice.  In a
     // weight gradient the halves of a slice are k-rows of their own, so each
     // takes the place of its like as soon as that has been read: four stages of
-    // half a slice, with a barrier after either half (1,200 cycles more than
-    // with all loads in half 1 for one to arrive).
+    // half a slice, with a barrier after either half.
     s16x8 fa[2][2][MT], fb[2][2][NT];  // [half][16 k of it][]
     wait_loads<AL + BL>();
 #pragma unroll
@@ -609,6 +608,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #pragma unroll
       for (int m = 0; m < MT; ++m) fa[0][kb][m] = frag_a(stage_a(0), m, kb);
     }
+    // Half 0 of a weight gradient loads over what all waves have just read.
+    if constexpr (kWGrad) wait_slice<AL + BL>();
     // LDS offsets of slices s, s + 1, s + 2.
     uint32_t la[3] = {stage_a(0), stage_a(1), stage_a(2)};
     uint32_t lb[3] = {stage_b(0), stage_b(1), stage_b(2)};

@@ -85,6 +85,21 @@ def test_many_tokens_of_few_experts():
     test_experts_and_gradients(1500, 4, 2, 136, 72, BF, dict(idle=0.02, hot=0.3))
 
 
+@pytest.mark.parametrize("T,E,D,F", [(4500, 1, 40, 24), (4600, 9, 1032, 264)])
+def test_more_rows_of_one_expert_than_a_token_list(T, E, D, F):
+    """The weight gradients list 4096 tokens at a time: an expert with more of them."""
+    col, val = routing(T, E, 1, 13, hot=0.97)
+    assert int((col == 0).sum()) > 4096
+    x, w_in, w_out, dy = tensors(T, E, D, F, BF, 14)
+    print(f"T={T} E={E} D={D} F={F}", flush=True)
+    want = ref.experts(x, w_in, w_out, col, val, dy)
+    _, kept = sg.experts(*(t.cuda() for t in (x, w_in, w_out, col, val)), keep=True)
+    got = sg.experts_backward(dy.cuda(), kept)
+    torch.cuda.synchronize()
+    for name, g in zip(("grad_x", "grad_w_in", "grad_w_out", "grad_val"), got):
+        ref.assert_within(g, *want[name], name)
+
+
 def test_strided_and_unaligned_operands():
     T, E, k, D, F = 37, 5, 2, 64, 48
     col, val = routing(T, E, k, 1)
@@ -109,6 +124,29 @@ def test_strided_and_unaligned_operands():
         ref.assert_within(y, *want["y"], "y")
         for name, g in zip(("grad_x", "grad_w_in", "grad_w_out", "grad_val"), got):
             ref.assert_within(g, *want[name], name)
+
+
+@pytest.mark.parametrize("T,E,k", [(600, 2, 2), (560, 8, 1)])
+def test_rows_spread_over_more_than_4_gb(T, E, k):
+    """Row strides whose byte offsets pass 32 bits, for x and for the gradient of y."""
+    D, F, ld = 40, 24, 1 << 22
+    print(f"far rows T={T} E={E}: {T * ld * 2 / 2 ** 30:.1f} GiB between the first and the last", flush=True)
+    col, val = routing(T, E, k, 11)
+    x, w_in, w_out, dy = tensors(T, E, D, F, BF, 12)
+    want = ref.experts(x, w_in, w_out, col, val, dy)
+    buf = torch.empty(T * ld, dtype=BF, device="cuda").view(T, ld)
+    x_far, dy_far = buf[:, :D], buf[:, 64:64 + D]
+    x_far.copy_(x.cuda())
+    dy_far.copy_(dy.cuda())
+    args = w_in.cuda(), w_out.cuda(), col.cuda(), val.cuda()
+    y, kept = sg.experts(x_far, *args, keep=True)
+    got = sg.experts_backward(dy_far, kept)
+    few = sg.experts(x_far[-2:], *args[:2], args[2][-2:].contiguous(), args[3][-2:].contiguous())
+    torch.cuda.synchronize()
+    ref.assert_within(y, *want["y"], "y")
+    ref.assert_within(few, want["y"][0][-2:], want["y"][1][-2:], "y of the last two")
+    for name, g in zip(("grad_x", "grad_w_in", "grad_w_out", "grad_val"), got):
+        ref.assert_within(g, *want[name], name)
 
 
 def test_gradients_against_differences():
