@@ -8,18 +8,26 @@
 //   dW_out[e] = sum_t dy_t (w h)^T.
 //
 // One kernel makes all six products.  A work group computes a BM x BN tile
-// from K-slices of 64 staged in LDS, its waves multiply 32x32x16 MFMA blocks
-// with fp32 accumulators.  An operand tile lies in LDS in one of
-// two forms, both filled by 16-byte global-to-LDS loads whose lane-linear
-// destination is permuted by choosing the source address:
+// from K-slices of 64 staged in LDS; its four waves, one to a SIMD, multiply
+// 32x32x16 MFMA blocks with fp32 accumulators.  At 256 x 256 a wave's part is
+// 128 x 128: of a slice's 2048 cycles of products LDS reads and writes take
+// 770, where eight waves of 128 x 64 would read half as much again; one wave to
+// a SIMD issues at most an instruction in 4 cycles, so the loop is kept to 4
+// instructions per 32-cycle product.  A slice takes about 2300 cycles (2800 in
+// the weight gradients), the rest of a tile 15,000-20,000.  At 131,072 rows of
+// 64 experts, 2048 x 1024, W_in's product runs at 1.1 PFLOP/s and 1.76 GHz with
+// the matrix cores busy 67%; the clock falls under the load, and further as
+// they are kept busier.  An operand tile lies in LDS in one of two forms, both
+// filled by 16-byte global-to-LDS loads whose lane-linear destination is
+// permuted by choosing the source address:
 //   row form (K contiguous in memory): [row][64 k], 16-byte chunk c of row r
 //     at slot c ^ (r >> 1 & 7); fragments are ds_read_b128.  With r & 7 the
 //     reads run at 54% of the rate, without the xor at 14%.
 //   column form (K strided): [k][column], the 32-byte segment s of row k at
 //     segment s ^ 2 (k & 3); fragments are two transposing 8-byte reads.  With
 //     (k & 3) | (k >> 3 & 1) << 2 they run at 50%, without the xor at 26%.
-// Rows that a tile has not, and K beyond its end, are read from a block of
-// zeros, so no tile ever multiplies foreign data.
+// K beyond its end is read from a block of zeros.  Rows that a tile has not are
+// its last row again; what they give is not stored.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -360,10 +368,10 @@ struct Stages {
 };
 
 // Whether a work group takes tiles in turn, or there is one for every tile.  In
-// turn: the weight gradients 741 -> 638 us and 355 -> 328 us (their experts'
-// unequal rows are shared out), the first product 1108 -> 970-990 us; not where
-// the loop leaves too few registers: dx's product 514 -> 560 us, the hidden
-// gradient 417 -> 470 us.
+// turn, at 64 experts of 2048 x 1024: the weight gradients 741 -> 638 us and 355
+// -> 328 us (1024 rows to an expert, whose unequal shares are evened out), W_in's
+// product 1108 -> 970-990 us (2048 rows); not where the loop leaves too few
+// registers: dx's product 514 -> 560 us, the hidden gradient 417 -> 470 us.
 template <int KIND>
 constexpr bool kTurns = KIND == kIn || KIND == kGradWOut || KIND == kGradWIn;
 
@@ -898,7 +906,10 @@ void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
 // the product.  A wave takes 16 weight rows straight from memory to registers
 // (16x16x32 MFMA, the weights as the left operand, up to 16 rows of x as the
 // right one), 8 loads in flight, and the waves of a work group share K, so that
-// many small work groups keep the memory busy.
+// many small work groups keep the memory busy: 48 tokens with 8 of 128 experts of
+// 2048 x 768 read W_in at 5.9 and W_out at 6.4 TB/s (some of it from the
+// memory-side cache), one token with 6 of 64 of 2048 x 1024 takes 14.5 + 9.3 us,
+// bound by the latency of its two launches.  16 loads in flight gained nothing.
 
 __device__ __forceinline__ f32x4 mfma16(__bf16, s16x8 a, s16x8 b, f32x4 c) {
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));

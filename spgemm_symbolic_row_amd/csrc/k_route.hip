@@ -9,7 +9,9 @@
 // DPP and one ballot.  The picks are then packed through LDS, so that the
 // weights cost one exponential each.  All sums are in 32 bits.  A row is read
 // once (4 or 2 bytes per logit) and 8 bytes per entry are written; what bounds
-// it is the chain of picks at few rows and the instructions at many.
+// it is the chain of picks at few rows (1 x 64, 6 picks: 3.3 us) and the
+// instructions at many (16384 x 256 fp32, sigmoid, 8 groups, 8 picks: 20 us, 0.9
+// TB/s; a wave to a row took 33).
 #include <algorithm>
 
 #include "expert_common.hpp"
