@@ -29,6 +29,7 @@
 // K beyond its end is read from a block of zeros.  Rows that a tile has not are
 // its last row again; what they give is not stored.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -887,8 +888,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 template <typename T, int KIND, int BM, int BN, bool kFar = false>
 void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   auto kernel = k_product<T, KIND, BM, BN, kFar>;
-  static const bool once = (allow_max_dynamic_lds((const void*)kernel), true);
-  (void)once;
+  static std::atomic<uint64_t> allowed{0};  // devices whose LDS limit is set
+  int device = 0;
+  if (hipGetDevice(&device) != hipSuccess) return;  // reported by the caller's last look
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(allowed.load() & bit)) {
+    allow_max_dynamic_lds((const void*)kernel);
+    allowed.fetch_or(bit);
+  }
   const int64_t step = KIND == kIn ? BN / 2 : BN;
   const int64_t tiles = row_tiles * ((a.N + step - 1) / step);
   if (tiles == 0) return;
