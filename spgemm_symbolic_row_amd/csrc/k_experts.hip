@@ -206,7 +206,6 @@ struct ProductArgs {
   int Kpad;
   int F, Fpad;
   void* c;           // 16-bit or fp32 result
-  float* scales;     // of rows held as scaled fp16
   int64_t ldc, c_expert;
   float* g;          // fp32 pre-activations, Fpad to a row
   float* u;
@@ -281,27 +280,6 @@ struct Tile {
 // Positions of the sorted token list that a weight gradient keeps in LDS.
 constexpr int kListLen = 4096;
 
-// Rows that are summed per token (of y and of dx) are written by one kernel and
-// read by another.  For bfloat16 tensors they are held as fp16, each 64 columns
-// with a power of two that brings their largest finite value to [2^14, 2^15):
-// 11 bits where the sum is rounded to 8 in the end, which adds 1/64 of that
-// rounding's variance, for half the bytes (the sum of 131,072 rows of 2048: 236
-// -> 130 us).  float16 tensors have 11 bits
-// themselves: their rows stay in fp32.
-template <typename T>
-constexpr bool kRows16 = std::is_same<T, __bf16>::value;
-constexpr int kScaleCols = 64;
-__host__ __device__ inline int64_t scale_blocks(int64_t cols) {
-  return (cols + kScaleCols - 1) / kScaleCols;
-}
-
-// Maximum over 8 consecutive lanes, in all of them.
-__device__ __forceinline__ uint32_t max_of_8(uint32_t x) {
-  x = max(x, dpp_or_zero<0xb1, 0xf>(x));   // quad_perm: 1 0 3 2
-  x = max(x, dpp_or_zero<0x4e, 0xf>(x));   // quad_perm: 2 3 0 1
-  return max(x, dpp_or_zero<0x141, 0xf>(x));  // row_half_mirror
-}
-
 // Sum over kLanes = 8 or 16 consecutive lanes, in all of them.
 template <int kLanes>
 __device__ __forceinline__ float sum_of_lanes(float x) {
@@ -310,44 +288,6 @@ __device__ __forceinline__ float sum_of_lanes(float x) {
   x = dpp_add<0x141, 0xf>(x);
   if constexpr (kLanes == 16) x = dpp_add<0x140, 0xf>(x);  // row_mirror
   return x;
-}
-
-// P rows, 8 of a row's 64 columns in each of 8 consecutive lanes, to fp16 with
-// their scale; `down` is what the stored values are to be multiplied by.
-template <int P>
-__device__ __forceinline__ void scale_to_f16(const float (&v)[P][8], s16x8 (&out)[P],
-                                             float (&down)[P]) {
-  uint32_t m[P];
-  bool infinite = false;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    float most = fabsf(v[p][0]);  // NaN is passed over
-#pragma unroll
-    for (int j = 1; j < 8; ++j) most = fmaxf(most, fabsf(v[p][j]));
-    m[p] = max_of_8(__float_as_uint(most));
-    infinite |= m[p] >= 0x7f800000u;
-  }
-  if (__ballot(infinite)) {  // the largest finite value counts
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      m[p] = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(v[p][j]) & 0x7fffffffu;
-        m[p] = max(m[p], b < 0x7f800000u ? b : 0u);
-      }
-      m[p] = max_of_8(m[p]);
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    // The exponent is kept where both powers of two are normal.
-    const uint32_t e = min(max(m[p] >> 23, 15u), 254u);
-    const float up = __uint_as_float((268u - e) << 23);
-    down[p] = __uint_as_float((e - 14u) << 23);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[p][j] = __builtin_bit_cast(short, (_Float16)(v[p][j] * up));
-  }
 }
 
 template <typename F, int... kI>
@@ -823,29 +763,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       auto block = [&](auto index) {
         constexpr int m = decltype(index)::value;
         stage_block(index);
-        if constexpr ((KIND == kOut || KIND == kGradX) && kRows16<T>) {
-          float v[kPass][8], down[kPass];
-          s16x8 h[kPass];
-#pragma unroll
-          for (int p = 0; p < kPass; ++p) load8(src + p * R * kPitch, v[p]);
-          scale_to_f16<kPass>(v, h, down);
-#pragma unroll
-          for (int p = 0; p < kPass; ++p) {
-            const int r = m * 32 + p * R;
-            if (kFull || (r + lr < rows_left && lc < cols_left))
-              *(s16x8*)((_Float16*)a.c + (row_w + r) * ld + xw + lane_at) = h[p];
-          }
-          if (lc % kScaleCols == 0) {
-            const int64_t blocks = scale_blocks(ld);
-#pragma unroll
-            for (int p = 0; p < kPass; ++p) {
-              const int r = m * 32 + p * R + lr;
-              if (kFull || (r < rows_left && lc < cols_left))
-                a.scales[(row_w + r) * blocks + (xw + lc) / kScaleCols] = down[p];
-            }
-          }
-          return;
-        }
 #pragma unroll
         for (int p = 0; p < kPass; ++p) {
           const int r = m * 32 + p * R;
@@ -1109,10 +1026,9 @@ __global__ __launch_bounds__(kFewTokenWaves * kWave) void k_few_token(ProductArg
 
 // out[t] = sum over its entries of w * rows[pos] (w = 1 without val), in the
 // entries' order, in fp32, rounded once.  8 columns to a thread.
-template <typename T, bool k16>
+template <typename T>
 __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int Dpad,
-                                                 const void* __restrict__ rows,
-                                                 const float* __restrict__ scales,
+                                                 const float* __restrict__ rows,
                                                  const int32_t* __restrict__ pos,
                                                  const float* __restrict__ val,
                                                  T* __restrict__ out) {
@@ -1126,15 +1042,9 @@ __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int D
   for (int e = 0; e < k; ++e) {
     const int p = pos[t * k + e];
     const int64_t row = max(p, 0);  // read in any case, so that the loads do not wait
-    float w = val ? val[t * k + e] : 1.0f, v[8];
-    if constexpr (k16) {
-      const s16x8 h = *(const s16x8*)((const _Float16*)rows + row * Dpad + x);
-      w *= scales[row * scale_blocks(Dpad) + x / kScaleCols];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (float)__builtin_bit_cast(_Float16, (short)h[j]);
-    } else {
-      load8((const float*)rows + row * Dpad + x, v);
-    }
+    float v[8];
+    const float w = val ? val[t * k + e] : 1.0f;
+    load8(rows + row * Dpad + x, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += p < 0 ? 0.0f : w * v[j];
   }
@@ -1262,7 +1172,6 @@ struct ForwardWork {
   int32_t* tmp;
   uint16_t* h;
   float* rows;
-  float* scales;
   Padded pad;
 };
 
@@ -1272,7 +1181,6 @@ ForwardWork take_forward(Carver& c, const Sizes& z, bool keep, bool padded) {
   w.tmp = c.take<int32_t>(dispatch_tmp_elems(z.n, z.E));
   w.h = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
-  w.scales = c.take<float>(z.n * scale_blocks(z.Dp));
   if (padded) w.pad = take_padded(c, z, false);
   return w;
 }
@@ -1281,7 +1189,6 @@ struct BackwardWork {
   uint16_t* dgu;
   uint16_t* hw;
   float* rows;
-  float* scales;
   float* part;
   Padded pad;
 };
@@ -1294,7 +1201,6 @@ BackwardWork take_backward(Carver& c, const Sizes& z, bool padded) {
   w.dgu = c.take<uint16_t>(z.n * z.S2);
   w.hw = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
-  w.scales = c.take<float>(z.n * scale_blocks(z.Dp));
   w.part = c.take<float>(z.n * dval_parts(z, 64));
   if (padded) w.pad = take_padded(c, z, true);
   return w;
@@ -1368,12 +1274,11 @@ ProductArgs base_args(const Sizes& z, const Dispatch& d) {
   return a;
 }
 
-template <typename T, bool k16>
-void combine(const Sizes& z, const void* rows, const float* scales, const int32_t* pos,
-             const float* val, void* out, hipStream_t s) {
-  hipLaunchKernelGGL((k_combine<T, k16>), dim3((unsigned)((z.T * (z.Dp / 8) + 255) / 256)),
-                     dim3(256), 0, s, z.T, z.k, (int)z.D, (int)z.Dp, rows, scales, pos, val,
-                     (T*)out);
+template <typename T>
+void combine(const Sizes& z, const float* rows, const int32_t* pos, const float* val, void* out,
+             hipStream_t s) {
+  hipLaunchKernelGGL((k_combine<T>), dim3((unsigned)((z.T * (z.Dp / 8) + 255) / 256)), dim3(256), 0,
+                     s, z.T, z.k, (int)z.D, (int)z.Dp, rows, pos, val, (T*)out);
 }
 
 template <typename T>
@@ -1437,14 +1342,12 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
                        dim3(kFewTokenWaves * kWave), 0, s, a);
     return;
   }
-  a.scales = w.scales;
   if (path == kPathFew)
     hipLaunchKernelGGL((k_few_out<T>), dim3((unsigned)(few * ((z.D + 31) / 32))), dim3(kNT), 0, s,
                        a);
   else
     product_by_rows<T, kOut>(a, z, s);
-  if (path == kPathFew) combine<T, false>(z, w.rows, nullptr, kp.d.pos, val, y, s);
-  else combine<T, kRows16<T>>(z, w.rows, w.scales, kp.d.pos, val, y, s);
+  combine<T>(z, w.rows, kp.d.pos, val, y, s);
 }
 
 template <typename T>
@@ -1490,9 +1393,8 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.Kpad = (int)z.S2;
   a.c = w.rows;
   a.ldc = z.Dp;
-  a.scales = w.scales;
   product_by_rows<T, kGradX>(a, z, s);
-  combine<T, kRows16<T>>(z, w.rows, w.scales, kp.d.pos, nullptr, dx, s);
+  combine<T>(z, w.rows, kp.d.pos, nullptr, dx, s);
   hipLaunchKernelGGL(k_dval, dim3((unsigned)((z.n + 255) / 256)), dim3(256), 0, s, z.n,
                      parts, kp.d.pos, w.part, dval);
   a = base_args(z, kp.d);
