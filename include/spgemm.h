@@ -522,11 +522,15 @@ spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
  * values (T x k, fp32, 0 in empty slots), for the routing that the forward pass
  * was given (the kept block holds it).  Every element is written: 0 for
  * experts without tokens.  Sums in fp32, in an order that only the routing
- * fixes: the same call gives the same bits. */
+ * fixes: the same call gives the same bits.  The gradients of g and u, and
+ * w * h, are rounded once to the tensors' type before their products; in fp16
+ * in units of their row's or expert's largest magnitude, so that gradients and
+ * values of any size keep the type's 11 bits.  The values' gradient is fp32
+ * throughout. */
 spgemm_status spgemm_experts_backward(
     const spgemm_experts_desc *desc, const void *dX, const void *dWIn,
-    const void *dWOut, const void *dGradY, const void *dKept, void *dGradX, void *dGradWIn, void *dGradWOut,
-    float *dGradVal, void *dWork, int64_t work_bytes, void *stream);
+    const void *dWOut, const void *dGradY, const void *dKept, void *dGradX,
+    void *dGradWIn, void *dGradWOut, float *dGradVal, void *dWork, int64_t work_bytes, void *stream);
 
 /* The global norm of `count` tensors (fp32, bf16 or fp16, mixed at will) and
  * its clipping: norm = sqrt(sum g^2) in fp64, rounded into dNorm (1 fp32);

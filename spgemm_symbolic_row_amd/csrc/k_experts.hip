@@ -121,6 +121,11 @@ __device__ __forceinline__ float fast_sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g));
 }
 
+// 1 / x of a power of two with exponent in [-126, 126].
+__device__ __forceinline__ float inverse_power(float x) {
+  return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+
 static __device__ __align__(16) const uint32_t zeros16[4] = {0, 0, 0, 0};
 
 // ---- operand tiles ----
@@ -212,10 +217,24 @@ struct ProductArgs {
   void* hw;          // w h
   float* dval_part;  // per entry: one partial sum of each wave's columns
   int parts;
+  const float* size;   // by expert (kScaled): of the values (hidden gradient), or the unit of
+                       // the rows that a weight gradient sums
   int k;               // slots of a row of the routing matrix
   const int32_t* col;  // and its entries, where they are taken unsorted
   const float* val;
 };
+
+// float16 ends at 2^-24 and 65504, where incoming gradients and values may be of
+// any size, so [dg, du] and w h are held in units that are powers of two, undone
+// in fp32 after the products:
+//   [dg, du] for dx: the row's largest finite magnitude at 2^14 .. 2^15;
+//   [dg, du] for dW_in, which sums over rows: that of the expert's largest row;
+//   w h: |w| below 1 for the expert's largest.
+// An element keeps 11 bits down to 2^-28 of that magnitude, and an error of 2^-39
+// of it below.  bfloat16 has the range of fp32 and needs none.  The units of
+// [dg, du] are known only when a row is done, so it passes through fp32.
+template <typename T>
+constexpr bool kScaled = std::is_same<T, _Float16>::value;
 
 constexpr int kFewRows = 16;  // rows of a tile of the few-rows products
 
@@ -692,6 +711,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     auto epilogue = [&](auto is_full) {
       constexpr bool kFull = decltype(is_full)::value;
       float g[2][kUnit][8], u[2][kUnit][8], w[2][kUnit];
+      const float w_unit = kScaled<T> ? inverse_power(a.size[t.expert]) : 1.0f;
       // A wave all of whose rows are outside reads the tile's last one.
       const int rmax = rows_left - 1;
       const uint32_t lane_at = (uint32_t)(lr * a.Fpad + lc);
@@ -717,6 +737,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       wait_slice<63>();
       auto unit = [&](auto index) {
         constexpr int c = decltype(index)::value, buf = c % 2, m = c * kUnit / kPass;
+        typedef std::conditional_t<kScaled<T>, float, T> G;
         if constexpr (c + 1 < kUnits) fetch(c + 1, 1 - buf);
         if constexpr (c * kUnit % kPass == 0) stage_block(std::integral_constant<int, m>{});
 #pragma unroll
@@ -733,11 +754,11 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             dot += h * v[j];
             dg[j] = dh * uj * s * (1.0f + gj * (1.0f - s));
             du[j] = dh * silu;
-            hv[j] = ww * h;
+            hv[j] = kScaled<T> ? ww * w_unit * h : ww * h;
           }
           if (inside) {
             const int64_t row = row_w + r + lr;
-            T* o = (T*)a.c + row * a.ldc + xw + lc;
+            G* o = (G*)a.c + row * a.ldc + xw + lc;
             store8((T*)a.hw + row * a.Fpad + xw + lc, true, 8, hv);
             store8(o, vec, a.F - xw - lc, dg);
             store8(o + a.F, vec, a.F - xw - lc, du);
@@ -760,6 +781,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       constexpr bool kFull = decltype(is_full)::value;
       const int64_t ld = KIND == kIn ? a.Fpad : a.ldc;
       const uint32_t lane_at = (uint32_t)lr * (uint32_t)ld + lc;
+      const float unit = kWGrad && kScaled<T> ? a.size[t.expert] : 1.0f;
       auto block = [&](auto index) {
         constexpr int m = decltype(index)::value;
         stage_block(index);
@@ -789,6 +811,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
           } else if constexpr (KIND == kOut || KIND == kGradX) {
             if (inside) store8((float*)a.c + base + lane_at, true, 8, v);
           } else {
+            if constexpr (kScaled<T>) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] *= unit;
+            }
             if (inside) store8((T*)a.c + base + lane_at, vec, cols_left - lc, v);
           }
         }
@@ -1024,13 +1050,15 @@ __global__ __launch_bounds__(kFewTokenWaves * kWave) void k_few_token(ProductArg
 
 // ---- sums over a token's entries ----
 
-// out[t] = sum over its entries of w * rows[pos] (w = 1 without val), in the
-// entries' order, in fp32, rounded once.  8 columns to a thread.
+// out[t] = sum over its entries of w * rows[pos], in the entries' order, in fp32,
+// rounded once; w is the entry's val, or the row's unit, or 1.  8 columns to a
+// thread.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int Dpad,
                                                  const float* __restrict__ rows,
                                                  const int32_t* __restrict__ pos,
                                                  const float* __restrict__ val,
+                                                 const float* __restrict__ unit,
                                                  T* __restrict__ out) {
   const int per = Dpad / 8;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -1043,7 +1071,7 @@ __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int D
     const int p = pos[t * k + e];
     const int64_t row = max(p, 0);  // read in any case, so that the loads do not wait
     float v[8];
-    const float w = val ? val[t * k + e] : 1.0f;
+    const float w = val ? val[t * k + e] : unit ? unit[row] : 1.0f;
     load8(rows + row * Dpad + x, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] += p < 0 ? 0.0f : w * v[j];
@@ -1063,6 +1091,95 @@ __global__ __launch_bounds__(256) void k_dval(int64_t n, int parts,
   if (p >= 0)
     for (int i = 0; i < parts; ++i) s += part[(int64_t)p * parts + i];
   dval[e] = s;
+}
+
+// ---- units of the float16 gradients ----
+
+// size[e]: the power of two at the expert's largest finite |src| (above 0), or
+// the next one (1).  A work group to an expert.
+__global__ __launch_bounds__(1024) void k_expert_size(const int32_t* __restrict__ row_ptr,
+                                                      const float* __restrict__ src, int above,
+                                                      float* __restrict__ size) {
+  __shared__ uint32_t most[1024 / kWave];
+  uint32_t m = 0;
+  const int end = row_ptr[blockIdx.x + 1];
+  for (int64_t i = (int64_t)row_ptr[blockIdx.x] + threadIdx.x; i < end; i += 1024) {
+    const uint32_t b = __float_as_uint(src[i]) & 0x7fffffffu;
+    m = max(m, b < 0x7f800000u ? b : 0u);
+  }
+  m = wave_max_u32(m);
+  if (lane_id() == 0) most[threadIdx.x / kWave] = m;
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < 1024 / kWave; ++w) m = max(m, most[w]);
+  // Exponents whose inverse is a normal number, too.
+  size[blockIdx.x] = __uint_as_float(min(max(m >> 23, 1u) + above, 253u) << 23);
+}
+
+// Rows of [dg, du] from fp32 (2 F of the S2 columns) to float16 (S2 columns, zeros at
+// the end) in units of their own, which go to unit[row].  A wave to a row.
+__global__ __launch_bounds__(256) void k_scale_rows(const int32_t* __restrict__ rows, int cols,
+                                                    int S2, const float* __restrict__ src,
+                                                    _Float16* __restrict__ dst,
+                                                    float* __restrict__ unit) {
+  const int64_t step = (int64_t)gridDim.x * (256 / kWave), n = *rows;
+  for (int64_t r = (int64_t)blockIdx.x * (256 / kWave) + threadIdx.x / kWave; r < n; r += step) {
+    const float* from = src + r * S2;
+    auto load = [&](int c, float v[8]) {
+      load8(from + c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j >= cols) v[j] = 0.0f;
+    };
+    uint32_t m = 0;
+    for (int c = lane_id() * 8; c < S2; c += kWave * 8) {
+      float v[8];
+      load(c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
+        m = max(m, b < 0x7f800000u ? b : 0u);
+      }
+    }
+    // The exponent is kept where both powers of two are normal.
+    const uint32_t e = min(max(wave_max_u32(m) >> 23, 15u), 254u);
+    const float up = __uint_as_float((268u - e) << 23);
+    if (lane_id() == 0) unit[r] = __uint_as_float((e - 14u) << 23);
+    for (int c = lane_id() * 8; c < S2; c += kWave * 8) {
+      float v[8];
+      load(c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= up;
+      store8(dst + r * S2 + c, true, 8, v);
+    }
+  }
+}
+
+// The same rows in the unit of their expert.  Work group (x, y) takes every 8th row
+// of tile x.
+constexpr int kUnitRows = 8;
+__global__ __launch_bounds__(256) void k_unit_rows(Dispatch d, int tile_rows, int S2,
+                                                   const _Float16* __restrict__ src,
+                                                   const float* __restrict__ unit,
+                                                   const float* __restrict__ size,
+                                                   _Float16* __restrict__ dst) {
+  if ((int)blockIdx.x >= *d.ntiles) return;
+  const int expert = d.tiles[2 * blockIdx.x], row0 = d.tiles[2 * blockIdx.x + 1];
+  const int rows = min(tile_rows, d.row_ptr[expert + 1] - row0);
+  for (int i = blockIdx.y; i < rows; i += kUnitRows) {
+    const int64_t r = row0 + i;
+    // Both are powers of two and the row's is not the larger one.
+    const int e = (int)(__float_as_uint(unit[r]) >> 23) - (int)(__float_as_uint(size[expert]) >> 23);
+    const float f = __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
+    for (int c = threadIdx.x * 8; c < S2; c += 256 * 8) {
+      struct alignas(16) Pack { _Float16 v[8]; };
+      const Pack q = *(const Pack*)(src + r * S2 + c);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)q.v[j] * f;
+      store8(dst + r * S2 + c, true, 8, v);
+    }
+  }
 }
 
 // Copies rows of `cols` 16-bit values to rows of `pad`, filled up with zeros:
@@ -1189,6 +1306,12 @@ struct BackwardWork {
   uint16_t* dgu;
   uint16_t* hw;
   float* rows;
+  // Of float16 gradients: [dg, du] in fp32, and then in units of the experts;
+  // the unit of each row of dgu; units by expert of [dg, du] and of w h.
+  float* dgu32;
+  float* row_unit;
+  float* dgu_size;
+  float* w_size;
   float* part;
   Padded pad;
 };
@@ -1196,12 +1319,18 @@ struct BackwardWork {
 // Partial sums of a value's gradient: one for each wave's columns.
 int dval_parts(const Sizes& z, int cols) { return (int)((z.Fp + cols - 1) / cols); }
 
-BackwardWork take_backward(Carver& c, const Sizes& z, bool padded) {
+BackwardWork take_backward(Carver& c, const Sizes& z, bool scaled, bool padded) {
   BackwardWork w{};
   w.dgu = c.take<uint16_t>(z.n * z.S2);
   w.hw = c.take<uint16_t>(z.n * z.Fp);
   w.rows = c.take<float>(z.n * z.Dp);
   w.part = c.take<float>(z.n * dval_parts(z, 64));
+  if (scaled) {
+    w.dgu32 = c.take<float>(z.n * z.S2);
+    w.row_unit = c.take<float>(z.n);
+    w.dgu_size = c.take<float>(z.E);
+    w.w_size = c.take<float>(z.E);
+  }
   if (padded) w.pad = take_padded(c, z, true);
   return w;
 }
@@ -1275,10 +1404,10 @@ ProductArgs base_args(const Sizes& z, const Dispatch& d) {
 }
 
 template <typename T>
-void combine(const Sizes& z, const float* rows, const int32_t* pos, const float* val, void* out,
-             hipStream_t s) {
+void combine(const Sizes& z, const float* rows, const int32_t* pos, const float* val,
+             const float* unit, void* out, hipStream_t s) {
   hipLaunchKernelGGL((k_combine<T>), dim3((unsigned)((z.T * (z.Dp / 8) + 255) / 256)), dim3(256), 0,
-                     s, z.T, z.k, (int)z.D, (int)z.Dp, rows, pos, val, (T*)out);
+                     s, z.T, z.k, (int)z.D, (int)z.Dp, rows, pos, val, unit, (T*)out);
 }
 
 template <typename T>
@@ -1347,7 +1476,7 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
                        a);
   else
     product_by_rows<T, kOut>(a, z, s);
-  combine<T>(z, w.rows, kp.d.pos, val, y, s);
+  combine<T>(z, w.rows, kp.d.pos, val, nullptr, y, s);
 }
 
 template <typename T>
@@ -1361,7 +1490,10 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   const Rows gr = padded_rows(dy, desc.grad_ld, z.T, z.D, w.pad.dy, s);
   const Rows w1 = padded_rows(w_in, z.D, z.E * 2 * z.F, z.D, w.pad.w_in, s);
   const Rows w2 = padded_rows(w_out, z.F, z.E * z.D, z.F, w.pad.w_out, s);
-  if (z.S2 != 2 * z.F)
+  if constexpr (kScaled<T>)
+    hipLaunchKernelGGL(k_expert_size, dim3((unsigned)z.E), dim3(1024), 0, s, kp.d.row_ptr, kp.d.w,
+                       1, w.w_size);
+  else if (z.S2 != 2 * z.F)
     hipLaunchKernelGGL(k_zero16, dim3(grid_for(z.n * z.S2)), dim3(256), 0, s, w.dgu, z.n * z.S2);
   ProductArgs a = base_args(z, kp.d);
   a.a = gr.p;
@@ -1372,7 +1504,8 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.N = a.Npad = (int)z.Fp;
   a.K = (int)z.D;
   a.Kpad = (int)z.Dp;
-  a.c = w.dgu;
+  a.c = kScaled<T> ? (void*)w.dgu32 : w.dgu;
+  a.size = w.w_size;
   a.ldc = z.S2;
   a.g = kp.g;
   a.u = kp.u;
@@ -1381,6 +1514,20 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.parts = dval_parts(z, tile_rows(z) == 128 && narrow_tiles(z, z.Fp, false) ? 64 : 128);
   const int parts = a.parts;
   product_by_rows<T, kGradH>(a, z, s);
+  const void* dgu_w = w.dgu;  // as dW_in sums it
+  if constexpr (kScaled<T>) {
+    const int bm = tile_rows(z);
+    dgu_w = w.dgu32;
+    hipLaunchKernelGGL(k_scale_rows, dim3(grid_for(z.n * kWave)), dim3(256), 0, s,
+                       kp.d.row_ptr + z.E, (int)(2 * z.F), (int)z.S2, w.dgu32, (_Float16*)w.dgu,
+                       w.row_unit);
+    hipLaunchKernelGGL(k_expert_size, dim3((unsigned)z.E), dim3(1024), 0, s, kp.d.row_ptr,
+                       w.row_unit, 0, w.dgu_size);
+    hipLaunchKernelGGL(k_unit_rows,
+                       dim3((unsigned)dispatch_max_tiles(z.n, z.E, bm), kUnitRows), dim3(256), 0, s,
+                       kp.d, bm, (int)z.S2, (const _Float16*)w.dgu, w.row_unit, w.dgu_size,
+                       (_Float16*)dgu_w);
+  }
   a = base_args(z, kp.d);
   a.a = w.dgu;
   a.lda = z.S2;
@@ -1394,7 +1541,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.c = w.rows;
   a.ldc = z.Dp;
   product_by_rows<T, kGradX>(a, z, s);
-  combine<T>(z, w.rows, kp.d.pos, nullptr, dx, s);
+  combine<T>(z, w.rows, kp.d.pos, nullptr, w.row_unit, dx, s);
   hipLaunchKernelGGL(k_dval, dim3((unsigned)((z.n + 255) / 256)), dim3(256), 0, s, z.n,
                      parts, kp.d.pos, w.part, dval);
   a = base_args(z, kp.d);
@@ -1406,12 +1553,13 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.Mpad = (int)z.Dp;
   a.N = (int)z.F;
   a.Npad = (int)z.Fp;
+  a.size = w.w_size;
   a.c = dw_out;
   a.ldc = z.F;
   a.c_expert = z.D * z.F;
   weight_gradient<T, kGradWOut>(a, z, s);
   a = base_args(z, kp.d);
-  a.a = w.dgu;
+  a.a = dgu_w;
   a.lda = z.S2;
   a.b = xr.p;
   a.ldb = xr.ld;
@@ -1419,6 +1567,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   a.Mpad = (int)z.S2;
   a.N = (int)z.D;
   a.Npad = (int)z.Dp;
+  a.size = w.dgu_size;
   a.c = dw_in;
   a.ldc = z.D;
   a.c_expert = 2 * z.F * z.D;
@@ -1487,7 +1636,7 @@ extern "C" spgemm_status spgemm_experts_sizes(const spgemm_experts_desc* desc, i
   }
   if (backward_work) {
     Carver c(nullptr);
-    take_backward(c, z, padded);
+    take_backward(c, z, desc->dtype == SPGEMM_F16, padded);
     *backward_work = c.used;
   }
   return SPGEMM_OK;
@@ -1536,7 +1685,8 @@ extern "C" spgemm_status spgemm_experts_backward(
     return launched();
   }
   Carver c(dWork);
-  const BackwardWork w = take_backward(c, z, needs_padding(*desc, dX, dWIn, dWOut, dGradY));
+  const BackwardWork w = take_backward(c, z, desc->dtype == SPGEMM_F16,
+                                       needs_padding(*desc, dX, dWIn, dWOut, dGradY));
   if (work_bytes < c.used) return refuse(SPGEMM_ERR_INVALID_ARG, "experts: workspace too small");
   if (desc->dtype == SPGEMM_BF16)
     backward<__bf16>(*desc, dX, dWIn, dWOut, dGradY, dKept, dGradX, dGradWIn, dGradWOut,
