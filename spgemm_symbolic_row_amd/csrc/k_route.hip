@@ -84,6 +84,13 @@ __device__ __forceinline__ float sigmoid(float z) {
   return (z < 0.0f ? e : 1.0f) / (1.0f + e);
 }
 
+// Its slope s (1 - s) = e / (1 + e)^2 with e = exp(-|z|): 1 - s would keep few bits
+// where s is near 1.
+__device__ __forceinline__ float sigmoid_slope(float z) {
+  const float e = expf(-fabsf(z)), d = 1.0f / (1.0f + e);
+  return e * d * d;
+}
+
 // Ordered key of an expert, 0 where it is out: a logit or a key that is
 // minus infinity or NaN.
 template <bool kSig>
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(kRouteNT) void k_route_grad(RouteGradArgs a) {
       const float D = sum + 1e-20f, mean = dot / D;
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (in[j]) d[j] = (a.renorm ? (dw[j] - mean) / D : dw[j]) * p[j] * (1.0f - p[j]);
+        if (in[j]) d[j] = (a.renorm ? (dw[j] - mean) / D : dw[j]) * sigmoid_slope(z[j]);
     }
   }
   T* out = (T*)a.dlogits + t * a.E;

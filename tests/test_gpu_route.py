@@ -202,3 +202,25 @@ def test_refusals():
     with pytest.raises(TypeError):
         sg.route_backward(z, r, torch.zeros(4, 2, dtype=BF, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("k,renormalise", [(1, False), (3, False), (3, True)])
+def test_slope_of_a_saturated_sigmoid(k, renormalise):
+    """The slope s (1 - s) at large logits, where 1 - s has few bits left: every gradient to a
+    relative bound.  With z at +-12 .. +-80, exp and its argument are off by 2^-22 + |z| 2^-24 <=
+    2^-17, the rest by 2^-20; renormalised, a difference of two terms is held to their size."""
+    z = torch.tensor([[12.0, -12.0, 20.0], [-20.0, 17.0, 30.0], [-80.0, 80.0, 40.0],
+                      [0.5, -40.0, 16.6]])[:, :k].contiguous()
+    dv = torch.tensor([[1.0, -2.0, 0.5]])[:, :k].repeat(4, 1).contiguous()
+    r = sg.route(z.cuda(), k, scores="sigmoid", renormalise=renormalise)
+    got = sg.route_backward(z.cuda(), r, dv.cuda())
+    torch.cuda.synchronize()
+    s, e = torch.sigmoid(z.double()), torch.exp(-z.double().abs())
+    d, size = dv.double(), dv.double().abs()
+    if renormalise:
+        total = s.sum(1, keepdim=True) + 1e-20
+        mean = (s * d).sum(1, keepdim=True) / total
+        size = (size + (s * size).sum(1, keepdim=True) / total) / total
+        d = (d - mean) / total
+    slope = e / (1 + e) ** 2
+    ref.assert_within(got, d * slope, 2.0 ** -16 * size * slope + 1e-37, "grad_logits")
