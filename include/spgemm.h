@@ -530,11 +530,14 @@ spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
 spgemm_status spgemm_experts_backward(
     const spgemm_experts_desc *desc, const void *dX, const void *dWIn,
     const void *dWOut, const void *dGradY, const void *dKept, void *dGradX,
-    void *dGradWIn, void *dGradWOut, float *dGradVal, void *dWork, int64_t work_bytes, void *stream);
+    void *dGradWIn, void *dGradWOut, float *dGradVal, void *dWork,
+    int64_t work_bytes, void *stream);
 
 /* The global norm of `count` tensors (fp32, bf16 or fp16, mixed at will) and
  * its clipping: norm = sqrt(sum g^2) in fp64, rounded into dNorm (1 fp32);
- * out = g * min(1, max_norm / (norm + 1e-6)), rounded once to out's type.
+ * out = g * min(1, max_norm / (norm + 1e-6)) in fp64, rounded to fp32 and then
+ * to out's type; right also where the norm itself is beyond fp32 (and infinite
+ * in dNorm).
  * out[i] may be grads[i] itself; other overlaps are not allowed.  A norm that
  * is NaN makes every output NaN.  The tables of pointers, sizes (elements) and
  * types are host arrays, read during the call.

@@ -17,7 +17,7 @@ namespace sg {
 namespace {
 
 constexpr int kGnNT = 256;
-constexpr int kGnTable = 96;       // tensors of one launch (2.3 KB of kernel arguments)
+constexpr int kGnTable = 96;       // tensors of one launch (2.8 KB of kernel arguments)
 constexpr int kGnParts = 2048;     // partial sums, and work groups, of one launch
 constexpr int64_t kGnChunk = 16384;  // elements of one work item
 
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kGnNT) void k_grad_squares(GradTable t, double* __r
 }
 
 template <typename T, typename U>
-__device__ __forceinline__ void scale_into(const T* p, U* o, int64_t n, float c) {
+__device__ __forceinline__ void scale_into(const T* p, U* o, int64_t n, double c) {
   constexpr int V = 16 / (sizeof(T) > sizeof(U) ? sizeof(T) : sizeof(U));
   int64_t at = 0;
   if ((uintptr_t)p % (V * sizeof(T)) == 0 && (uintptr_t)o % (V * sizeof(U)) == 0) {
@@ -106,17 +106,17 @@ __device__ __forceinline__ void scale_into(const T* p, U* o, int64_t n, float c)
       const Pi q = ((const Pi*)p)[i];
       Po r;
 #pragma unroll
-      for (int j = 0; j < V; ++j) r.v[j] = from_f32<U>(to_f32(q.v[j]) * c);
+      for (int j = 0; j < V; ++j) r.v[j] = from_f32<U>((float)(to_f32(q.v[j]) * c));
       ((Po*)o)[i] = r;
     }
     at = packs * V;
   }
-  for (int64_t i = at + threadIdx.x; i < n; i += kGnNT) o[i] = from_f32<U>(to_f32(p[i]) * c);
+  for (int64_t i = at + threadIdx.x; i < n; i += kGnNT) o[i] = from_f32<U>((float)(to_f32(p[i]) * c));
 }
 
 template <typename T>
 __device__ __forceinline__ void scale_from(const T* p, void* o, int out, int64_t off, int64_t n,
-                                           float c) {
+                                           double c) {
   if (out == SPGEMM_F32) scale_into(p, (float*)o + off, n, c);
   else if (out == SPGEMM_BF16) scale_into(p, (__bf16*)o + off, n, c);
   else scale_into(p, (_Float16*)o + off, n, c);
@@ -141,7 +141,9 @@ __global__ __launch_bounds__(kGnNT) void k_grad_scale(GradTable t,
   const double norm = sqrt(group_sum(s));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double q = max_norm / (norm + 1e-6);
-  const float c = q > 1.0 ? 1.0f : (float)q;  // NaN stays NaN
+  // In fp64: as the norm passes 2^126 the factor leaves fp32's normal numbers, and
+  // the products need not.  NaN stays NaN.
+  const double c = q > 1.0 ? 1.0 : q;
   for (int i = blockIdx.x; i < t.first[t.count]; i += gridDim.x) {
     const int x = tensor_of(t, i);
     const int64_t off = (int64_t)(i - t.first[x]) * kGnChunk;

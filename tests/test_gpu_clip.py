@@ -111,3 +111,18 @@ def test_refusals():
         assert e.value.status == -1
     torch.cuda.synchronize()
     assert bool((g == 1).all())
+
+
+def test_a_norm_beyond_fp32():
+    """The norm is infinite in fp32, the factor below its normal numbers; the elements are right."""
+    for dtype, size, n in ((F32, 3e38, 1000), (BF, 3e38, 5003), (F32, 1e36, 40_000_000)):
+        g = torch.full((n,), size, device="cuda").to(dtype)
+        norm64 = float(g[0]) * math.sqrt(n)
+        for max_norm in (1.0, 1e-3):
+            out = torch.empty(n, device="cuda")
+            norm = sg.clip_grad_norm([g], max_norm, out=[out])
+            torch.cuda.synchronize()
+            assert math.isinf(float(norm)) == (norm64 > 3.4028235e38)
+            want = float(g[0]) * (max_norm / norm64)
+            off = float(((out.double() - want).abs() / want).max())
+            assert off <= 4 * 2.0 ** -24, (dtype, size, max_norm)
