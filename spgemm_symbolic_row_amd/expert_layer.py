@@ -195,11 +195,12 @@ def _experts_desc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned):
 
 class _Kept:
     """What a forward pass keeps for its backward pass: its inputs (borrowed,
-    and not to be changed before) and the library's block."""
-    __slots__ = ("x", "w_in", "w_out", "val", "block")
+    and not to be changed before), the library's block, and the stream that
+    the block was taken from."""
+    __slots__ = ("x", "w_in", "w_out", "val", "block", "stream")
 
     def __init__(self, *a):
-        self.x, self.w_in, self.w_out, self.val, self.block = a
+        self.x, self.w_in, self.w_out, self.val, self.block, self.stream = a
 
 
 def _off16(*tensors):
@@ -234,11 +235,12 @@ def experts(x, w_in, w_out, col, val, keep=False):
         y = torch.empty(T, D, dtype=x.dtype, device=dev)
         block = torch.empty(kept_bytes, dtype=torch.uint8, device=dev) if keep else None
         work = torch.empty(max(work_bytes, 1), dtype=torch.uint8, device=dev)
+        stream = _stream(x)
         _check(_lib().spgemm_experts_forward(d, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(),
                                              col.data_ptr(), val.data_ptr(), y.data_ptr(),
                                              block.data_ptr() if keep else None, work.data_ptr(),
-                                             work_bytes, _stream(x)))
-    return (y, _Kept(x, w_in, w_out, val, block)) if keep else y
+                                             work_bytes, stream))
+    return (y, _Kept(x, w_in, w_out, val, block, stream)) if keep else y
 
 
 def experts_backward(grad_y, kept):
@@ -258,11 +260,16 @@ def experts_backward(grad_y, kept):
         gx = torch.empty(T, D, dtype=x.dtype, device=dev)
         gw_in, gw_out = torch.empty_like(w_in), torch.empty_like(w_out)
         gval = torch.empty_like(val)
+        stream = _stream(x)
+        if stream != kept.stream:
+            # What only `kept` may still hold is not given away before this stream is done with it.
+            for t in (x, w_in, w_out, kept.block):
+                t.record_stream(torch.cuda.current_stream(dev))
         work = torch.empty(max(work_bytes, 1), dtype=torch.uint8, device=dev)
         _check(_lib().spgemm_experts_backward(
             d, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), grad_y.data_ptr(),
             kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
-            gw_out.data_ptr(), gval.data_ptr(), work.data_ptr(), work_bytes, _stream(x)))
+            gw_out.data_ptr(), gval.data_ptr(), work.data_ptr(), work_bytes, stream))
     return gx, gw_in, gw_out, gval
 
 

@@ -1,0 +1,39 @@
+"""The expert layer beside torch's own machinery: gradients that torch was to
+make, streams, and counters of in-place changes."""
+import pytest
+
+torch = pytest.importorskip("torch")
+sg = pytest.importorskip("spgemm_symbolic_row_amd")
+from test_gpu_experts import routing, tensors
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def layer(T=4, E=3, k=2, D=16, F=8):
+    col, val = routing(T, E, k, 0)
+    x, w_in, w_out, dy = tensors(T, E, D, F, BF, 0)
+    return [t.cuda() for t in (x, w_in, w_out, col, val)], dy.cuda()
+
+
+def test_kept_block_outlives_a_backward_pass_on_another_stream():
+    """What a forward pass kept is not given to its own stream again while a backward pass that
+    another stream has yet to run reads it."""
+    args, dy = layer(T=512, E=4, D=128, F=64)
+    want = [t.clone() for t in sg.experts_backward(dy, sg.experts(*args, keep=True)[1])]
+    torch.cuda.synchronize()
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    with torch.cuda.stream(side):
+        _, kept = sg.experts(*args, keep=True)
+    side.synchronize()
+    at, size = kept.block.data_ptr(), kept.block.numel()
+    torch.cuda._sleep(400_000_000)
+    got = sg.experts_backward(dy, kept)
+    del kept
+    with torch.cuda.stream(side):
+        new = torch.empty(size, dtype=torch.uint8, device="cuda")
+    busy = not main.query()
+    main.synchronize()
+    assert busy and new.data_ptr() != at
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
