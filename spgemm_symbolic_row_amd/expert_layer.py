@@ -12,7 +12,9 @@ k slots a row (`col`, `val`; column -1 in an empty slot, and those last).
     norm = sg.clip_grad_norm([dw_in, dw_out, dlogits], max_norm=1.0)
 
 Argument marshalling only: every step runs in the HIP library on the current
-stream of the tensors' device, asynchronously.
+stream of the tensors' device, asynchronously.  Nothing is recorded for torch's
+backward pass, the backward calls are the only way to the gradients: while torch
+records, tensors that require one are refused (torch.no_grad() or detach()).
 """
 from __future__ import annotations
 
@@ -60,6 +62,16 @@ def _stream(x):
     if _raw_stream is not None:
         return _raw_stream(x.get_device())
     return torch.cuda.current_stream(x.device).cuda_stream
+
+
+_requires_grad = torch.Tensor.requires_grad.__get__
+
+
+def _unrecorded(*tensors):
+    """A result of tensors that require a gradient would have no graph."""
+    if torch.is_grad_enabled() and True in map(_requires_grad, tensors):
+        raise TypeError("a tensor requires a gradient, and nothing is recorded here: use the "
+                        "backward calls, under torch.no_grad() or with detached tensors")
 
 
 def _rows(x, what):
@@ -132,6 +144,7 @@ def route(logits, k, scores="softmax", bias=None, groups=1, top_groups=0, renorm
         _dense(bias, (E,), torch.float32, dev, "bias")
     if active is not None:
         _dense(active, (T,), torch.bool, dev, "active")
+    _unrecorded(logits)
     o = _route_options(scores, groups, top_groups, bool(renormalise), float(scale))
     with _on(logits):
         col = torch.empty(T, max(k, 0), dtype=torch.int32, device=dev)
@@ -155,6 +168,7 @@ def route_backward(logits, routing, grad_val):
         raise ValueError("logits are not the ones of this routing")
     dev = logits.device
     _dense(grad_val, routing.col.shape, torch.float32, dev, "grad_val")
+    _unrecorded(grad_val)
     b = routing.bias
     with _on(logits):
         out = torch.empty(T, E, dtype=logits.dtype, device=dev)
@@ -229,6 +243,7 @@ def experts(x, w_in, w_out, col, val, keep=False):
     _dense(w_out, (E, D, F), x.dtype, dev, "w_out")
     _dense(col, (T, k), torch.int32, dev, "col")
     _dense(val, (T, k), torch.float32, dev, "val")
+    _unrecorded(x, w_in, w_out, val)
     d, kept_bytes, work_bytes, _ = _experts_desc(T, E, D, F, x_ld, D, k, _TYPES[x.dtype],
                                                  _off16(x, w_in, w_out))
     with _on(x):
@@ -251,6 +266,7 @@ def experts_backward(grad_y, kept):
         raise ValueError(f"grad_y must have shape {tuple(x.shape)}, got {tuple(grad_y.shape)}")
     if grad_y.dtype != x.dtype or grad_y.device != x.device:
         raise TypeError(f"grad_y must be {x.dtype} on {x.device}")
+    _unrecorded(grad_y)
     x_ld, g_ld = _rows(x, "x"), _rows(grad_y, "grad_y")
     T, D = x.shape
     E, F, k, dev = w_out.shape[0], w_out.shape[2], val.shape[1], x.device
@@ -293,6 +309,7 @@ def clip_grad_norm(grads, max_norm, out=None):
         raise ValueError("out must have as many elements as grads, each")
     if not (all(map(T.is_contiguous, grads)) and all(map(T.is_contiguous, outs))):
         raise TypeError("tensors must be contiguous")
+    _unrecorded(*(grads if outs is grads else grads + outs))
     try:
         types = array("i", [_TYPES[g.dtype] for g in grads])
         out_types = types if outs is grads else array("i", [_TYPES[o.dtype] for o in outs])

@@ -17,6 +17,40 @@ def layer(T=4, E=3, k=2, D=16, F=8):
     return [t.cuda() for t in (x, w_in, w_out, col, val)], dy.cuda()
 
 
+def test_tensors_that_require_a_gradient_are_refused():
+    """The calls record nothing for torch's backward pass, so a result without its graph would lose
+    gradients silently."""
+    args, dy = layer()
+    plain = sg.experts(*args)
+    for i in (0, 1, 2, 4):
+        bad = list(args)
+        bad[i] = args[i].clone().requires_grad_()
+        with pytest.raises(TypeError, match="gradient"):
+            sg.experts(*bad)
+        with torch.no_grad():
+            assert torch.equal(sg.experts(*bad), plain)
+        assert torch.equal(sg.experts(*(t.detach() for t in bad)), plain)
+    z = torch.randn(4, 8, device="cuda")
+    bad = z.clone().requires_grad_()
+    with pytest.raises(TypeError, match="gradient"):
+        sg.route(bad, 2)
+    with torch.no_grad():
+        assert torch.equal(sg.route(bad, 2).col, sg.route(z, 2).col)
+    # The bias enters the choice only: it has no gradient.
+    assert torch.equal(sg.route(z, 2, bias=torch.zeros(8, device="cuda").requires_grad_()).col,
+                       sg.route(z, 2).col)
+    _, kept = sg.experts(*args, keep=True)
+    with pytest.raises(TypeError, match="gradient"):
+        sg.experts_backward(dy.clone().requires_grad_(), kept)
+    r = sg.route(z, 2)
+    with pytest.raises(TypeError, match="gradient"):
+        sg.route_backward(z, r, torch.zeros(4, 2, device="cuda").requires_grad_())
+    g = torch.ones(4, device="cuda")
+    with pytest.raises(TypeError, match="gradient"):
+        sg.clip_grad_norm([g], 1.0, out=[g.clone().requires_grad_()])
+    torch.cuda.synchronize()
+
+
 def test_kept_block_outlives_a_backward_pass_on_another_stream():
     """What a forward pass kept is not given to its own stream again while a backward pass that
     another stream has yet to run reads it."""
