@@ -325,4 +325,6 @@ def clip_grad_norm(grads, max_norm, out=None):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         _check(L.spgemm_clip_grad_norm(n, *tables, float(max_norm), norm.data_ptr(),
                                        work.data_ptr(), need, _stream(norm)))
+    # Torch does not see the writes: tensors that it saved for a backward pass have changed.
+    torch.autograd.graph.increment_version(outs)
     return norm

@@ -51,6 +51,20 @@ def test_tensors_that_require_a_gradient_are_refused():
     torch.cuda.synchronize()
 
 
+def test_clipping_counts_as_a_change():
+    """Torch's check of tensors saved for a backward pass sees that they were clipped."""
+    a, g = torch.ones(5, device="cuda", requires_grad=True), torch.full((5,), 3.0, device="cuda")
+    y = (a * g).sum()   # saves g
+    sg.clip_grad_norm([g], 1.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+    g, o = torch.ones(5, device="cuda"), torch.ones(5, device="cuda")
+    before = g._version, o._version
+    sg.clip_grad_norm([g], 1.0, out=[o])
+    assert g._version == before[0] and o._version > before[1]
+    torch.cuda.synchronize()
+
+
 def test_kept_block_outlives_a_backward_pass_on_another_stream():
     """What a forward pass kept is not given to its own stream again while a backward pass that
     another stream has yet to run reads it."""
