@@ -14,14 +14,13 @@ names through `lib()`.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
 __all__ = [
     "lib", "Options", "Params", "Stats", "CsrDevice", "Plan", "matmul", "compute_params",
     "prune_colnorm", "SpgemmError", "to_device", "last_stats",
-    "Routing", "route", "route_backward", "dispatch", "experts", "experts_backward",
-    "clip_grad_norm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -430,6 +429,8 @@ def transpose(A, out_rowptr64=False, pattern_only=False, no_alloc=False):
 
 _EXPERT_LAYER = ("Routing", "route", "route_backward", "dispatch", "experts", "experts_backward",
                  "clip_grad_norm")
+if importlib.util.find_spec("torch"):  # else a star import would fail on these names
+    __all__ += _EXPERT_LAYER
 
 
 def __getattr__(name):
