@@ -1155,9 +1155,8 @@ __global__ __launch_bounds__(256) void k_scale_rows(const int32_t* __restrict__ 
   }
 }
 
-// The same rows in the unit of their expert.  Work group (x, y) takes every 8th row
-// of tile x.
-constexpr int kUnitRows = 8;
+// The same rows in the unit of their expert.  The work groups of one x share the
+// rows of tile x.
 __global__ __launch_bounds__(256) void k_unit_rows(Dispatch d, int tile_rows, int S2,
                                                    const _Float16* __restrict__ src,
                                                    const float* __restrict__ unit,
@@ -1166,7 +1165,7 @@ __global__ __launch_bounds__(256) void k_unit_rows(Dispatch d, int tile_rows, in
   if ((int)blockIdx.x >= *d.ntiles) return;
   const int expert = d.tiles[2 * blockIdx.x], row0 = d.tiles[2 * blockIdx.x + 1];
   const int rows = min(tile_rows, d.row_ptr[expert + 1] - row0);
-  for (int i = blockIdx.y; i < rows; i += kUnitRows) {
+  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
     const int64_t r = row0 + i;
     // Both are powers of two and the row's is not the larger one.
     const int e = (int)(__float_as_uint(unit[r]) >> 23) - (int)(__float_as_uint(size[expert]) >> 23);
@@ -1229,16 +1228,23 @@ Sizes sizes_of(const spgemm_experts_desc& d) {
 // rows, or by large tiles.
 enum Path { kPathDirect, kPathFew, kPathTiles };
 
+// Fewer than 2^32 work items, as a launch takes them.
+bool launchable(int64_t groups, int64_t size) { return groups * size < (int64_t)1 << 32; }
+
 Path path_of(const Sizes& z, bool keep) {
-  if (keep) return kPathTiles;
   // Unsorted entries read the weights of a shared expert once each, but save
   // the dispatch and the sum: 2 tokens of 8 picks among 128 experts 43 against
   // 46 us, 8 tokens 118 against 105 us.
-  if (z.T == 1 || z.n <= z.E / 4) return kPathDirect;
+  const bool direct = z.T == 1 || z.n <= z.E / 4;
   // 16 rows to a tile against 128: 3 entries to an expert 209 against 237 us, 4.5
   // 180 against 194, 6 186 against 228, 9 217 against 209.
-  if (z.n <= 6 * z.E) return kPathFew;
-  return kPathTiles;
+  if (keep || !(direct || z.n <= 6 * z.E)) return kPathTiles;
+  const int64_t tiles = direct ? z.n : dispatch_max_tiles(z.n, z.E, kFewRows);
+  if (!launchable(tiles * ((z.Fp + 15) / 16), kNT) ||
+      !(direct ? launchable(z.T * ((z.D + 15) / 16), kFewTokenWaves * kWave)
+               : launchable(tiles * ((z.D + 31) / 32), kNT)))
+    return kPathTiles;
+  return direct ? kPathDirect : kPathFew;
 }
 
 // Rows of a tile: 256 when the experts' rows fill such tiles to more than
@@ -1517,15 +1523,16 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   const void* dgu_w = w.dgu;  // as dW_in sums it
   if constexpr (kScaled<T>) {
     const int bm = tile_rows(z);
+    const int64_t tiles = dispatch_max_tiles(z.n, z.E, bm);
+    const unsigned share = launchable(tiles * 8, 256) ? 8 : 1;
     dgu_w = w.dgu32;
     hipLaunchKernelGGL(k_scale_rows, dim3(grid_for(z.n * kWave)), dim3(256), 0, s,
                        kp.d.row_ptr + z.E, (int)(2 * z.F), (int)z.S2, w.dgu32, (_Float16*)w.dgu,
                        w.row_unit);
     hipLaunchKernelGGL(k_expert_size, dim3((unsigned)z.E), dim3(1024), 0, s, kp.d.row_ptr,
                        w.row_unit, 0, w.dgu_size);
-    hipLaunchKernelGGL(k_unit_rows,
-                       dim3((unsigned)dispatch_max_tiles(z.n, z.E, bm), kUnitRows), dim3(256), 0, s,
-                       kp.d, bm, (int)z.S2, (const _Float16*)w.dgu, w.row_unit, w.dgu_size,
+    hipLaunchKernelGGL(k_unit_rows, dim3((unsigned)tiles, share), dim3(256), 0, s, kp.d,
+                       bm, (int)z.S2, (const _Float16*)w.dgu, w.row_unit, w.dgu_size,
                        (_Float16*)dgu_w);
   }
   a = base_args(z, kp.d);
@@ -1596,7 +1603,7 @@ spgemm_status check_desc(const spgemm_experts_desc* d) {
       2 * round8(d->hidden) * round8(d->width) >= (int64_t)1 << 31 ||
       d->tokens > INT32_MAX / d->k ||
       d->tokens * d->k / 128 + d->experts > INT32_MAX / ((d->width + d->hidden) / 128 + 1) / 2 ||
-      d->tokens > INT32_MAX / (d->width / 2048 + 1) ||
+      !launchable((d->tokens * (round8(d->width) / 8) + 255) / 256, 256) ||
       d->experts * ((d->width + 255) / 256 + 1) * ((2 * d->hidden + 255) / 256 + 1) >
           INT32_MAX / 2)
     return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "experts: too many entries or tiles");

@@ -391,11 +391,21 @@ __global__ __launch_bounds__(kRouteNT) void k_route_grad(RouteGradArgs a) {
 int width_of(int64_t E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
 int lanes_of(int64_t E) { return E <= 256 ? 16 : 64; }
 
+// Work groups of one launch at most: a launch takes fewer than 2^32 work items.
+constexpr int64_t kRouteGrid = ((int64_t)1 << 31) / kRouteNT;
+
 template <typename T, int L, int V, bool kSig>
-void launch_route(const RouteArgs& a, hipStream_t s) {
+void launch_route(RouteArgs a, hipStream_t s) {
   constexpr int kRows = kRouteNT / L;
-  hipLaunchKernelGGL((k_route<T, L, V, kSig>), dim3((unsigned)((a.T + kRows - 1) / kRows)),
-                     dim3(kRouteNT), (size_t)kRows * 2 * a.k * sizeof(uint32_t), s, a);
+  for (int64_t left = a.T; left > 0; left -= a.T) {
+    a.T = std::min(left, kRouteGrid * kRows);
+    hipLaunchKernelGGL((k_route<T, L, V, kSig>), dim3((unsigned)((a.T + kRows - 1) / kRows)),
+                       dim3(kRouteNT), (size_t)kRows * 2 * a.k * sizeof(uint32_t), s, a);
+    a.logits = (const T*)a.logits + a.T * a.ld;
+    if (a.active) a.active += a.T;
+    a.col += a.T * a.k;
+    a.val += a.T * a.k;
+  }
 }
 
 template <typename T, bool kSig>
@@ -410,15 +420,27 @@ void route_by_width(const RouteArgs& a, hipStream_t s) {
   }
 }
 
+template <typename T, int V, bool kSig>
+void launch_route_grad(RouteGradArgs a, hipStream_t s) {
+  for (int64_t left = a.T; left > 0; left -= a.T) {
+    a.T = std::min(left, kRouteGrid * kRouteRows);
+    hipLaunchKernelGGL((k_route_grad<T, V, kSig>),
+                       dim3((unsigned)((a.T + kRouteRows - 1) / kRouteRows)), dim3(kRouteNT),
+                       (size_t)kRouteRows * 2 * a.E * sizeof(float), s, a);
+    a.logits = (const T*)a.logits + a.T * a.ld;
+    a.col += a.T * a.k;
+    a.dval += a.T * a.k;
+    a.dlogits = (T*)a.dlogits + a.T * a.E;
+  }
+}
+
 template <typename T, bool kSig>
 void route_grad_by_width(const RouteGradArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + kRouteRows - 1) / kRouteRows)), nt(kRouteNT);
-  const size_t lds = (size_t)kRouteRows * 2 * a.E * sizeof(float);
-  if (a.E <= 64) hipLaunchKernelGGL((k_route_grad<T, 1, kSig>), grid, nt, lds, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((k_route_grad<T, 2, kSig>), grid, nt, lds, s, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((k_route_grad<T, 4, kSig>), grid, nt, lds, s, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((k_route_grad<T, 8, kSig>), grid, nt, lds, s, a);
-  else hipLaunchKernelGGL((k_route_grad<T, 16, kSig>), grid, nt, lds, s, a);
+  if (a.E <= 64) launch_route_grad<T, 1, kSig>(a, s);
+  else if (a.E <= 128) launch_route_grad<T, 2, kSig>(a, s);
+  else if (a.E <= 256) launch_route_grad<T, 4, kSig>(a, s);
+  else if (a.E <= 512) launch_route_grad<T, 8, kSig>(a, s);
+  else launch_route_grad<T, 16, kSig>(a, s);
 }
 
 int64_t type_bytes(spgemm_dtype t) { return t == SPGEMM_F32 ? 4 : 2; }

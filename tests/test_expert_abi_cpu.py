@@ -73,3 +73,13 @@ def test_clip_refuses():
     assert clip(m=-1.0) == -1 and clip(m=float("nan")) == -1
     assert clip(s=(ctypes.c_int64 * 1)(-1)) == -1
     assert clip(o=(ctypes.c_void_p * 1)()) == -1
+
+
+def test_sizes_that_no_launch_takes():
+    """Sums over 2^35 values take 2^32 work items: refused before anything is launched."""
+    L = sg.lib()
+    def size(T, D):
+        return L.spgemm_experts_sizes(ExpertsDesc(T, 4, D, 8, D, D, 1, 2, 0, 0), None, None, None)
+    assert size((1 << 24) - 1, 2048) == 0 and size(1 << 24, 2048) == -3
+    assert size((1 << 23) - 1, 4096) == 0 and size(1 << 23, 4096) == -3
+    assert size(1 << 30, 8) == 0

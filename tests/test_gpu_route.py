@@ -224,3 +224,23 @@ def test_slope_of_a_saturated_sigmoid(k, renormalise):
         d = (d - mean) / total
     slope = e / (1 + e) ** 2
     ref.assert_within(got, d * slope, 2.0 ** -16 * size * slope + 1e-37, "grad_logits")
+
+
+def test_more_rows_than_one_launch_takes():
+    """A launch has fewer than 2^32 work items: 16 or 64 to a row of logits."""
+    T = (1 << 28) + 1003
+    z = torch.zeros(T, 1, dtype=BF, device="cuda")
+    r = sg.route(z, 1)
+    assert int(torch.count_nonzero(r.col)) == 0 and float(r.val.min()) == 1.0 == float(r.val.max())
+    del z, r
+    T, E, k = (1 << 26) + 77, 3, 2
+    z = torch.randn(T, E, dtype=BF, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    active = torch.rand(T, device="cuda") > 0.1
+    r = sg.route(z, k, active=active)
+    g = torch.randn(T, k, device="cuda")
+    dz = sg.route_backward(z, r, g)
+    for part in (slice(0, 999), slice((1 << 25) - 50, (1 << 25) + 50), slice(T - 999, T)):
+        q = sg.route(z[part], k, active=active[part])
+        assert torch.equal(q.col, r.col[part]) and torch.equal(q.val, r.val[part])
+        assert torch.equal(sg.route_backward(z[part], q, g[part]), dz[part])
+    torch.cuda.synchronize()
