@@ -267,6 +267,7 @@ extern "C" spgemm_status spgemm_dispatch(int64_t T, int32_t k, int64_t E, const 
   d.pos = w.pos;
   d.tiles = w.tiles;
   d.ntiles = w.ntiles;
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   launch_dispatch(dCol, nullptr, n, k, E, 256, d, w.tmp, (hipStream_t)stream);
   const hipError_t e = hipGetLastError();
   if (e == hipSuccess) return SPGEMM_OK;

@@ -833,7 +833,9 @@ void launch_product(const ProductArgs& a, int64_t row_tiles, hipStream_t s) {
   auto kernel = k_product<T, KIND, BM, BN, kFar>;
   static std::atomic<uint64_t> allowed{0};  // devices whose LDS limit is set
   int device = 0;
-  if (hipGetDevice(&device) != hipSuccess) return;  // reported by the caller's last look
+  // After a failure nothing more is launched, and setting the limit, which leaves
+  // the error state clear, does not lose it: the caller's last look reports it.
+  if (hipPeekAtLastError() != hipSuccess || hipGetDevice(&device) != hipSuccess) return;
   const uint64_t bit = 1ull << (device & 63);
   if (!(allowed.load() & bit)) {
     allow_max_dynamic_lds((const void*)kernel);
@@ -1663,6 +1665,7 @@ extern "C" spgemm_status spgemm_experts_forward(const spgemm_experts_desc* desc,
   const ForwardWork w =
       take_forward(c, z, dKept != nullptr, needs_padding(*desc, dX, dWIn, dWOut, nullptr));
   if (work_bytes < c.used) return refuse(SPGEMM_ERR_INVALID_ARG, "experts: workspace too small");
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   const hipStream_t s = (hipStream_t)stream;
   if (desc->dtype == SPGEMM_BF16)
     forward<__bf16>(*desc, dX, dWIn, dWOut, dCol, dVal, dY, dKept, w, s);
@@ -1684,6 +1687,7 @@ extern "C" spgemm_status spgemm_experts_backward(
   if (desc->grad_ld < desc->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: a row stride below the width");
   const Sizes z = sizes_of(*desc);
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   const hipStream_t s = (hipStream_t)stream;
   if (desc->tokens == 0) {
     const int64_t n1 = z.E * 2 * z.F * z.D, n2 = z.E * z.D * z.F;

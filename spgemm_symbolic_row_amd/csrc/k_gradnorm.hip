@@ -198,6 +198,7 @@ extern "C" spgemm_status spgemm_clip_grad_norm(int64_t count, const void* const*
   }
   if (all > INT32_MAX)
     return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "clip_grad_norm: too many elements");
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   const hipStream_t s = (hipStream_t)stream;
   double* parts = (double*)dWork;
   auto add = [&](GradTable& t, int64_t i) {

@@ -498,6 +498,7 @@ extern "C" spgemm_status spgemm_route(int64_t T, int64_t E, int32_t k, const voi
                                       int32_t* dCol, float* dVal, void* stream) {
   const spgemm_status st = check_route(T, E, k, dLogits, ld, dtype, opts, dCol, dVal);
   if (st != SPGEMM_OK || T == 0) return st;
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   RouteArgs a{};
   a.logits = dLogits;
   a.ld = ld;
@@ -534,6 +535,7 @@ extern "C" spgemm_status spgemm_route_backward(int64_t T, int64_t E, int32_t k,
                                                void* dGradLogits, void* stream) {
   const spgemm_status st = check_route(T, E, k, dLogits, ld, dtype, opts, dCol, dGradVal);
   if (st != SPGEMM_OK || T == 0) return st;
+  (void)hipGetLastError();  // an error that earlier calls left is not this one's
   if (!dGradLogits) return refuse(SPGEMM_ERR_INVALID_ARG, "route: null array");
   RouteGradArgs a{};
   a.logits = dLogits;

@@ -85,3 +85,39 @@ def test_kept_block_outlives_a_backward_pass_on_another_stream():
     main.synchronize()
     assert busy and new.data_ptr() != at
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_an_error_that_another_call_left_is_not_reported():
+    """The runtime keeps the last error of a thread until it is read."""
+    args, dy = layer()
+    z = torch.randn(4, 8, device="cuda")
+    g = torch.ones(9, device="cuda")
+
+    def every_call():
+        left()
+        r = sg.route(z, 2)
+        left()
+        d = sg.route_backward(z, r, r.val)
+        left()
+        p = sg.dispatch(r.col, 8)
+        left()
+        y, kept = sg.experts(*args, keep=True)
+        left()
+        b = sg.experts_backward(dy, kept)
+        left()
+        return (d, *p, y, *b, sg.clip_grad_norm([g], 1.0, out=[torch.empty_like(g)]))
+
+    def left():
+        pass
+
+    want = every_call()
+    torch.cuda.synchronize()
+    hip = sg.lib()   # the runtime that the library is linked to
+
+    def left():
+        assert hip.hipSetDevice(1 << 20) != 0 and hip.hipPeekAtLastError() != 0
+
+    got = every_call()
+    hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
