@@ -81,7 +81,7 @@ def _rows(x, what):
     T, n = x.shape
     if n > 1 and x.stride(1) != 1:
         raise TypeError(f"{what} must have contiguous rows")
-    ld = x.stride(0) if T > 1 else max(n, x.stride(0))
+    ld = x.stride(0) if T > 1 else n  # the stride of a single row says nothing
     if ld < n:
         raise TypeError(f"{what} must not have overlapping rows")
     return ld

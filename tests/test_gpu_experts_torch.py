@@ -121,3 +121,34 @@ def test_an_error_that_another_call_left_is_not_reported():
     hip.hipGetLastError()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("stride", [17, 1 << 30])
+def test_stride_of_a_single_row(stride):
+    """One token out of a larger tensor: whatever its row stride is, there is one row."""
+    (x, w_in, w_out, col, val), dy = layer(T=1)
+    def alone(t):
+        v = torch.empty(stride + 64, dtype=t.dtype, device="cuda").as_strided(t.shape, (stride, 1))
+        v.copy_(t)
+        return v
+    want, kept = sg.experts(x, w_in, w_out, col, val, keep=True)
+    grads = sg.experts_backward(dy, kept)
+    got, kept = sg.experts(alone(x), w_in, w_out, col, val, keep=True)
+    assert torch.equal(got, want)
+    assert all(torch.equal(a, b) for a, b in zip(sg.experts_backward(alone(dy), kept), grads))
+    z = torch.randn(1, 8, device="cuda")
+    assert torch.equal(sg.route(alone(z), 2).val, sg.route(z, 2).val)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,E", [(1, 3), (2, 16), (40, 16), (300, 3), (9000, 3)])
+def test_no_row_has_an_entry(T, E, dtype):
+    D, F, k = 72, 24, 2
+    x, w_in, w_out, dy = (t.cuda() for t in tensors(T, E, D, F, dtype, 1))
+    col = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    val = torch.full((T, k), float("nan"), device="cuda")
+    y = sg.experts(x, w_in, w_out, col, val)
+    z, kept = sg.experts(x, w_in, w_out, col, val, keep=True)
+    for t in (y, z, *sg.experts_backward(dy, kept)):
+        assert torch.count_nonzero(t) == 0
