@@ -1157,22 +1157,19 @@ __global__ __launch_bounds__(256) void k_scale_rows(const int32_t* __restrict__ 
   }
 }
 
-// The same rows in the unit of their expert.  The work groups of one x share the
-// rows of tile x.
-__global__ __launch_bounds__(256) void k_unit_rows(Dispatch d, int tile_rows, int S2,
-                                                   const _Float16* __restrict__ src,
+// The same rows in the unit of their expert.  A wave to a row.
+__global__ __launch_bounds__(256) void k_unit_rows(const int32_t* __restrict__ row_ptr, int E,
+                                                   int S2, const _Float16* __restrict__ src,
                                                    const float* __restrict__ unit,
                                                    const float* __restrict__ size,
                                                    _Float16* __restrict__ dst) {
-  if ((int)blockIdx.x >= *d.ntiles) return;
-  const int expert = d.tiles[2 * blockIdx.x], row0 = d.tiles[2 * blockIdx.x + 1];
-  const int rows = min(tile_rows, d.row_ptr[expert + 1] - row0);
-  for (int i = blockIdx.y; i < rows; i += gridDim.y) {
-    const int64_t r = row0 + i;
+  const int64_t step = (int64_t)gridDim.x * (256 / kWave), n = row_ptr[E];
+  for (int64_t r = (int64_t)blockIdx.x * (256 / kWave) + threadIdx.x / kWave; r < n; r += step) {
+    const int64_t expert = wave_last_le(row_ptr, (int64_t)0, (int64_t)E, r);
     // Both are powers of two and the row's is not the larger one.
     const int e = (int)(__float_as_uint(unit[r]) >> 23) - (int)(__float_as_uint(size[expert]) >> 23);
     const float f = __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
-    for (int c = threadIdx.x * 8; c < S2; c += 256 * 8) {
+    for (int c = lane_id() * 8; c < S2; c += kWave * 8) {
       struct alignas(16) Pack { _Float16 v[8]; };
       const Pack q = *(const Pack*)(src + r * S2 + c);
       float v[8];
@@ -1524,17 +1521,14 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
   product_by_rows<T, kGradH>(a, z, s);
   const void* dgu_w = w.dgu;  // as dW_in sums it
   if constexpr (kScaled<T>) {
-    const int bm = tile_rows(z);
-    const int64_t tiles = dispatch_max_tiles(z.n, z.E, bm);
-    const unsigned share = launchable(tiles * 8, 256) ? 8 : 1;
     dgu_w = w.dgu32;
     hipLaunchKernelGGL(k_scale_rows, dim3(grid_for(z.n * kWave)), dim3(256), 0, s,
                        kp.d.row_ptr + z.E, (int)(2 * z.F), (int)z.S2, w.dgu32, (_Float16*)w.dgu,
                        w.row_unit);
     hipLaunchKernelGGL(k_expert_size, dim3((unsigned)z.E), dim3(1024), 0, s, kp.d.row_ptr,
                        w.row_unit, 0, w.dgu_size);
-    hipLaunchKernelGGL(k_unit_rows, dim3((unsigned)tiles, share), dim3(256), 0, s, kp.d,
-                       bm, (int)z.S2, (const _Float16*)w.dgu, w.row_unit, w.dgu_size,
+    hipLaunchKernelGGL(k_unit_rows, dim3(grid_for(z.n * kWave)), dim3(256), 0, s, kp.d.row_ptr,
+                       (int)z.E, (int)z.S2, (const _Float16*)w.dgu, w.row_unit, w.dgu_size,
                        (_Float16*)dgu_w);
   }
   a = base_args(z, kp.d);
