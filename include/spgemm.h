@@ -501,16 +501,20 @@ typedef struct spgemm_experts_desc {
 
 /* Bytes of the kept block and of the two workspaces (any may be NULL).
  * Operands whose rows do not begin at 16-byte boundaries (D, F or a stride no
- * multiple of 8, or `unaligned`) are copied, and the copies counted. */
+ * multiple of 8, or `unaligned`) are copied in every call, all experts' weights
+ * too, and the copies counted.
+ * Errors: INVALID_ARG (experts outside [1, 1024], k outside [1, 64], bad sizes,
+ * strides or dtype), INDEX_OVERFLOW (sizes or strides beyond the kernels'
+ * indexes or beyond one launch's 2^32 work items). */
 spgemm_status spgemm_experts_sizes(const spgemm_experts_desc *desc,
                                    int64_t *kept, int64_t *forward_work,
                                    int64_t *backward_work);
 
 /* y_t = sum over row t of w * W_out[e] (silu(W_gate[e] x_t) * (W_up[e] x_t)),
  * T x D contiguous; 0 for a row without entries.  Products and sums in fp32;
- * the hidden vector is rounded once to the tensors' type, y once.  Columns
- * outside [0, E) are no entries.  With dKept (the sizes call's bytes) the
- * pass leaves what the backward pass needs there. */
+ * the hidden vector is rounded once to the tensors' type (in fp16 it has to
+ * be below 65504), y once.  Columns outside [0, E) are no entries.  With dKept
+ * (the sizes call's bytes) the pass leaves what the backward pass needs there. */
 spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
                                      const void *dX, const void *dWIn,
                                      const void *dWOut, const int32_t *dCol,

@@ -115,8 +115,10 @@ __device__ __forceinline__ void wait_slice() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLeft) : "memory");
 }
 
-// 1 / (1 + exp(-g)) by the native base-2 exponential and reciprocal: within
-// (2 + |g|) 2^-24 of its value.  The exponential overflows where the result is 0.
+// 1 / (1 + exp(-g)) by the native base-2 exponential and reciprocal, each within an
+// ulp (2^-23): with the rounding of the exponent (1.5 |g| 2^-24) and of the sum,
+// within (5 + 1.5 |g|) 2^-24 of its value.  0 below g = -88, where the value is
+// subnormal.
 __device__ __forceinline__ float fast_sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896340736f * g));
 }
@@ -232,7 +234,9 @@ struct ProductArgs {
 //   w h: |w| below 1 for the expert's largest.
 // An element keeps 11 bits down to 2^-28 of that magnitude, and an error of 2^-39
 // of it below.  bfloat16 has the range of fp32 and needs none.  The units of
-// [dg, du] are known only when a row is done, so it passes through fp32.
+// [dg, du] are known only when a row is done, so it passes through fp32: 8192
+// tokens with 8 of 64 experts, 2048 x 1024, take 3541 us forward and backward,
+// where bfloat16 takes 3085.
 template <typename T>
 constexpr bool kScaled = std::is_same<T, _Float16>::value;
 
@@ -330,8 +334,9 @@ struct Stages {
 // Whether a work group takes tiles in turn, or there is one for every tile.  In
 // turn, at 64 experts of 2048 x 1024: the weight gradients 741 -> 638 us and 355
 // -> 328 us (1024 rows to an expert, whose unequal shares are evened out), W_in's
-// product 1108 -> 970-990 us (2048 rows); not where the loop leaves too few
-// registers: dx's product 514 -> 560 us, the hidden gradient 417 -> 470 us.
+// product 1108 -> 970-990 us (2048 rows); not the hidden gradient, whose loop leaves
+// too few registers (434 -> 498 us).  dx's product (582 -> 596 us) and W_out's (362
+// -> 352 us) hardly care.
 template <int KIND>
 constexpr bool kTurns = KIND == kIn || KIND == kGradWOut || KIND == kGradWIn;
 
@@ -1054,7 +1059,8 @@ __global__ __launch_bounds__(kFewTokenWaves * kWave) void k_few_token(ProductArg
 
 // out[t] = sum over its entries of w * rows[pos], in the entries' order, in fp32,
 // rounded once; w is the entry's val, or the row's unit, or 1.  8 columns to a
-// thread.
+// thread.  The rows' bytes bound it: 131,072 rows of 2048 in 220-240 us, 4.7-5.2
+// TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine(int64_t Tn, int k, int D, int Dpad,
                                                  const float* __restrict__ rows,

@@ -6,8 +6,8 @@
 // L2, which costs less than a launch between) and scales its share.  Tables
 // that do not fit one launch's arguments take several of each, and one work
 // group between that adds all partial sums up.  Every element is read twice and
-// written once; the bytes bound it (8 10^8 elements of two types, 2.1 GB: 1.32 ms,
-// 4.8 TB/s, the rate of a device copy).  The scaling goes backwards, so that it
+// written once; the bytes bound it (8 10^8 elements of two types, 2.1 GB: 1.27 ms,
+// 5.0 TB/s, the rate of a device copy).  The scaling goes backwards, so that it
 // begins with what the memory-side cache still holds.
 #include <algorithm>
 
