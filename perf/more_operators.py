@@ -1,0 +1,497 @@
+"""Measured cases of the operators around the expert layer: layer norm with its gradient, 8-bit activation checkpoints,
+and a whole expert layer for a few tokens, with 16-bit and 8-bit weights.
+
+Each case is one call (or one forward and backward pair) as a user's program makes it.  The plain forms
+are elementary torch operations in 32 bits (the router's product in 64), rounded once at the end.
+"""
+import math
+
+import torch
+
+own = False
+
+_TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+_BYTES = {"f32": 4, "bf16": 2, "f16": 2, "e4m3": 1}
+_BLOCK = 128  # columns (and rows, of weights) that share a scale
+
+
+# ---------------------------------------------------------------- the cases
+
+def listed():
+    return [
+        # The norm of one decode step: latency.
+        _norm("norm_decode", 5, 2048, "bf16"),
+        # A long prompt chunk, forward only.
+        _norm("norm_chunk", 16384, 2048, "bf16", bias=True),
+        # A training step with an odd width, rows cut out of a wider buffer, fp32 weights.
+        _norm("norm_train_odd", 4099, 1001, "f16", weight="f32", bias=True, pad=27, back=True),
+        # A training batch of a wide model in fp32.
+        _norm("norm_train_f32", 6000, 4096, "f32", weight="f32", bias=True, back=True),
+        # A training batch whose input is kept in 8 bits.
+        _norm("norm_train_e4m3", 32768, 2048, "bf16", weight="f32", keep="e4m3", back=True),
+        # One token of one request through a whole expert layer.
+        _layer("layer_token", 1, 64, 6, 2048, 1024, "bf16"),
+        # A decode batch with a balanced sigmoid router in expert groups; fp32 router.
+        _layer("layer_batch", 16, 128, 8, 2048, 768, "bf16", router="f32", scores="sigmoid", bias=True, groups=8, top=4,
+               scale=2.5),
+        # Ragged middle: widths that end inside every block, rows that are not routed, weights not renormalised.
+        _layer("layer_ragged", 7, 24, 3, 1001, 345, "f16", renorm=False, idle=0.2),
+        # One token, weights in 8 bits with a scale for each 128 x 128 block.
+        _layer("layer_token_e4m3", 1, 64, 6, 2048, 1024, "bf16", weights="e4m3"),
+        # A few speculative tokens, 8-bit weights of odd sizes.
+        _layer("layer_few_e4m3", 5, 60, 4, 2040, 1400, "f16", weights="e4m3"),
+        # A small training step with 8-bit checkpoints, odd sizes.
+        _train("checkpoint_small", 509, 16, 2, 520, 264, "f16", idle=0.02),
+        # A training step of an expert layer with 8-bit checkpoints: forward, and every gradient.
+        _train("checkpoint_train", 8192, 64, 8, 2048, 1024, "bf16"),
+    ]
+
+
+def _norm(name, T, D, dtype, weight=None, bias=False, pad=0, keep="rows", back=False):
+    c = dict(kind="norm", T=T, D=D, dtype=dtype, weight=weight or dtype, bias=bias, pad=pad, keep=keep, back=back)
+    return {"name": name, **c} if name else c
+
+
+def _layer(name, T, E, k, D, F, dtype, weights=None, router=None, scores="softmax", bias=False, groups=1, top=1,
+           renorm=True, scale=1.0, idle=0.0):
+    c = dict(kind="layer", T=T, E=E, k=k, D=D, F=F, dtype=dtype, weights=weights or dtype, router=router or dtype,
+             scores=scores, bias=bias, groups=groups, top=top, renorm=renorm, scale=scale, idle=idle)
+    return {"name": name, **c} if name else c
+
+
+def _train(name, T, E, k, D, F, dtype, idle=0.0):
+    c = dict(kind="train", T=T, E=E, k=k, D=D, F=F, dtype=dtype, idle=idle)
+    return {"name": name, **c} if name else c
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    kind = rng.choice(["norm", "norm", "layer", "layer", "train"])
+    if kind == "norm":
+        D = _log(rng, 16, 8192)
+        T = min(_log(rng, 1, 65536), max(1, 32768 * 2048 // (2 * D)))
+        dtype = rng.choice(["f32", "bf16", "f16"])
+        return _norm("", T, D, dtype, weight=rng.choice(["f32", dtype]), bias=rng.random() < 0.5,
+                     pad=rng.choice([0, 0, 8, 13]), keep=rng.choice(["rows", "e4m3"]), back=rng.random() < 0.7)
+    if kind == "layer":
+        groups = rng.choice([1, 1, 2, 4])
+        per = _log(rng, 4, 128 // groups)
+        top = rng.randint(1, groups)
+        k = rng.randint(1, min(8, per * top))
+        E = per * groups
+        D, F = _log(rng, 64, 4096), _log(rng, 32, 2048)
+        # No more weights than the largest listed case.
+        F = max(8, min(F, int(128 * 2048 * 768 / (E * D))))
+        dtype = rng.choice(["bf16", "f16"])
+        return _layer("", rng.randint(1, 16), E, k, D, F, dtype, weights=rng.choice([dtype, "e4m3"]),
+                      router=rng.choice(["f32", dtype]), scores=rng.choice(["softmax", "sigmoid"]),
+                      bias=rng.random() < 0.5, groups=groups, top=top, renorm=rng.random() < 0.6,
+                      scale=rng.choice([1.0, 2.5]), idle=rng.choice([0.0, 0.2]))
+    E = _log(rng, 4, 128)
+    k = rng.randint(1, min(8, E))
+    D, F = 8 * _log(rng, 16, 320), 8 * _log(rng, 16, 200)
+    T = _log(rng, 32, 6144)
+    # No more products, and no more weights, than the largest listed case.
+    T = max(1, min(T, int(8192 * 8 * 2048 * 1024 / 2 / (k * D * F))))
+    E = max(k, min(E, int(64 * 2048 * 1024 / (D * F))))
+    return _train("", T, E, k, D, F, rng.choice(["bf16", "f16"]), idle=rng.choice([0.0, 0.05]))
+
+
+# ---------------------------------------------------------------- inputs
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, scale=1.0, dtype=torch.float32):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=dtype).mul_(scale)
+
+    def share(n, p):
+        return torch.rand(n, generator=gen, device="cuda") < p
+
+    state = dict(case)
+    T, D, t = case["T"], case["D"], _TYPES[case["dtype"]]
+    if case["kind"] == "norm":
+        # A residual stream: rows of different size, a few channels far larger than the others.
+        x = normal(T, D + case["pad"])
+        x *= 1.0 + normal(T, 1).abs()
+        x *= torch.where(share(D + case["pad"], 0.01), 20.0, 1.0)
+        x += normal(1, D + case["pad"], scale=0.3)
+        state["x"] = x.to(t)[:, :D]
+        w = _TYPES[case["weight"]]
+        state["weight"] = (1.0 + normal(D, scale=0.2)).to(w)
+        state["bias"] = normal(D, scale=0.1).to(w) if case["bias"] else None
+        state["grad"] = normal(T, D, scale=0.01).to(t) if case["back"] else None
+        return state
+    E, k, F = case["E"], case["k"], case["F"]
+    # What a norm leaves: unit rows, some channels larger than the others.
+    state["x"] = (normal(T, D) * (0.5 + normal(1, D).abs())).to(t)
+    w_in = normal(E, 2 * F, D, scale=D ** -0.5, dtype=t)
+    w_out = normal(E, D, F, scale=F ** -0.5, dtype=t)
+    active = ~share(T, case["idle"]) if case["idle"] else None
+    if case["kind"] == "layer":
+        state["router"] = normal(E, D, scale=D ** -0.5).to(_TYPES[case["router"]])
+        state["bias"] = normal(E, scale=0.1) if case["bias"] else None
+        state["active"] = active
+        state["w_in"], state["in_scale"] = _weights(w_in, case["weights"])
+        state["w_out"], state["out_scale"] = _weights(w_out, case["weights"])
+        return state
+    best, col = torch.topk(normal(T, E) + normal(1, E, scale=0.3), k, dim=1)
+    col, at = torch.sort(col, dim=1)
+    val = torch.softmax(best, dim=1).gather(1, at)
+    if active is not None:
+        col = torch.where(active[:, None], col, -1)
+        val = torch.where(active[:, None], val, 0.0)
+    state["col"], state["val"] = col.to(torch.int32).contiguous(), val.contiguous()
+    state["w_in"], state["w_out"] = w_in, w_out
+    state["grad"] = normal(T, D).to(t)
+    return state
+
+
+def _spread(scale, rows, cols):
+    """The scale of every element from those of 128 x 128 blocks."""
+    return scale.repeat_interleave(_BLOCK, 1)[:, :rows].repeat_interleave(_BLOCK, 2)[:, :, :cols]
+
+
+def _weights(w, kind):
+    """Weights as a serving program holds them: as they are, or in 8 bits with a scale for each block."""
+    if kind != "e4m3":
+        return w, None
+    E, R, C = w.shape
+    r, c = -(-R // _BLOCK), -(-C // _BLOCK)
+    scale = torch.zeros(E, r, c, device=w.device)
+    for i in range(r):
+        for j in range(c):
+            block = w[:, i * _BLOCK:(i + 1) * _BLOCK, j * _BLOCK:(j + 1) * _BLOCK]
+            scale[:, i, j] = block.abs().amax((1, 2)).float() / 448.0
+    q = torch.empty(E, R, C, dtype=torch.float8_e4m3fn, device=w.device)
+    for e in range(E):
+        q[e] = (w[e].float() / _spread(scale[e:e + 1], R, C)[0]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return q, scale
+
+
+# ---------------------------------------------------------------- one pass
+
+def run(state):
+    if own:
+        return _run_own(state)
+    return {"norm": _plain_norm, "layer": _plain_layer, "train": _plain_train}[state["kind"]](state)
+
+
+def _run_own(s):
+    import spgemm_symbolic_row_amd as sg
+
+    if s["kind"] == "norm":
+        if s["grad"] is None:
+            return {"y": sg.layer_norm(s["x"], s["weight"], s["bias"])}
+        y, kept = sg.layer_norm(s["x"], s["weight"], s["bias"], keep="e4m3" if s["keep"] == "e4m3" else True)
+        dx, dw, db = sg.layer_norm_backward(s["grad"], kept)
+        out = {"y": y, "grad_x": dx, "grad_weight": dw}
+        if db is not None:
+            out["grad_bias"] = db
+        return out
+    if s["kind"] == "layer":
+        y, r = sg.expert_layer(s["x"], s["router"], s["w_in"], s["w_out"], s["k"], in_scale=s["in_scale"],
+                               out_scale=s["out_scale"], scores=s["scores"], bias=s["bias"], groups=s["groups"],
+                               top_groups=s["top"], renormalise=s["renorm"], scale=s["scale"], active=s["active"])
+        return {"y": y, "col": r.col, "val": r.val}
+    y, kept = sg.experts(s["x"], s["w_in"], s["w_out"], s["col"], s["val"], keep="e4m3")
+    dx, dw_in, dw_out, dval = sg.experts_backward(s["grad"], kept)
+    return {"y": y, "grad_x": dx, "grad_w_in": dw_in, "grad_w_out": dw_out, "grad_val": dval}
+
+
+def _power(e):
+    """2^e exactly (pow is not), as float32."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
+def _plain_kept(x):
+    """What is left of rows kept in 8 bits: for each 128 columns the smallest power of two s with max |x| <= 448 s, and
+    x / s rounded to e4m3."""
+    half = x.dtype == torch.float16
+    T, D = x.shape
+    v = torch.nn.functional.pad(x.float(), (0, -D % _BLOCK)).view(T, -1, _BLOCK)
+    finite = v.abs() < math.inf
+    m, p = torch.frexp(torch.where(finite, v.abs(), 0.0).amax(2, keepdim=True))
+    e = torch.clamp(torch.where(m <= 0.875, p - 9, p - 8), min=-15 if half else -117)
+    top = torch.where(e == (8 if half else 120), 240.0, 448.0)
+    q = torch.minimum(torch.maximum(v * _power(-e), -top), top).to(torch.float8_e4m3fn).float()
+    kept = torch.where(finite, q * _power(e), math.nan)
+    return kept.view(T, -1)[:, :D]
+
+
+def _plain_norm(s):
+    x, t, eps = s["x"].float(), s["x"].dtype, 1e-5
+    mean = x.mean(1, keepdim=True)
+    rstd = 1.0 / torch.sqrt((x - mean).square().mean(1, keepdim=True) + eps)
+    w = s["weight"].float()
+    y = (x - mean) * rstd * w
+    if s["bias"] is not None:
+        y = y + s["bias"].float()
+    out = {"y": y.to(t)}
+    if s["grad"] is None:
+        return out
+    if s["keep"] == "e4m3":
+        x = _plain_kept(s["x"])
+    n = (x - mean) * rstd
+    dy = s["grad"].float()
+    a = dy * w
+    out["grad_x"] = (rstd * (a - a.mean(1, keepdim=True) - n * (a * n).mean(1, keepdim=True))).to(t)
+    out["grad_weight"] = (dy * n).sum(0).to(s["weight"].dtype)
+    if s["bias"] is not None:
+        out["grad_bias"] = dy.sum(0).to(s["weight"].dtype)
+    return out
+
+
+def _plain_route(s, z):
+    T, E = z.shape
+    k, inf = s["k"], float("inf")
+    sig = 1.0 / (1.0 + torch.exp(-z))
+    key = z if s["scores"] == "softmax" else sig
+    if s["bias"] is not None:
+        key = key + s["bias"]
+    fits = (z > -inf) & (key > -inf)
+    if s["active"] is not None:
+        fits = fits & s["active"][:, None]
+    allowed = fits
+    if s["groups"] > 1:
+        G = s["groups"]
+        best = torch.sort(torch.where(fits, key, -inf).view(T, G, E // G), dim=2, descending=True).values
+        score = best[:, :, 0]
+        if s["scores"] == "sigmoid" and E // G > 1:
+            score = score + torch.where(best[:, :, 1] > -inf, best[:, :, 1], 0.0)
+        first = torch.sort(score, dim=1, descending=True, stable=True).indices[:, :s["top"]]
+        chosen = torch.zeros(T, G, dtype=torch.bool, device=z.device).scatter_(1, first, True)
+        allowed = fits & chosen.repeat_interleave(E // G, dim=1)
+    ranked, at = torch.sort(torch.where(allowed, key, -inf), dim=1, descending=True, stable=True)
+    there = torch.gather(allowed, 1, at)[:, :k]
+    col, order = torch.sort(torch.where(there, at[:, :k], E), dim=1)
+    there = torch.gather(there, 1, order)
+    pick = torch.where(there, col, 0)
+    if s["scores"] == "softmax":
+        among = torch.where(there, torch.gather(z, 1, pick), -inf)
+        every = among if s["renorm"] else torch.where(fits, z, -inf)
+        top = every.amax(1, keepdim=True)
+        top = torch.where(top > -inf, top, 0.0)
+        total = torch.exp(every - top).sum(1, keepdim=True)
+        w = torch.where(there, torch.exp(among - top) / total, 0.0)
+    else:
+        w = torch.where(there, torch.gather(sig, 1, pick), 0.0)
+        w = w / (w.sum(1, keepdim=True) + 1e-20 if s["renorm"] else 1.0)
+    return torch.where(there, col, -1).to(torch.int32), w * s["scale"]
+
+
+def _plain_layer(s):
+    # Which experts are picked depends on sums of long rows: 64 bits.
+    z = (s["x"].double() @ s["router"].double().t()).float()
+    col, val = _plain_route(s, z)
+    x, (T, D), F = s["x"].float(), s["x"].shape, s["w_out"].shape[2]
+    flat = col.reshape(-1).long()
+    there = flat >= 0
+    e = torch.where(there, flat, 0)
+    w1, w2 = s["w_in"][e].float(), s["w_out"][e].float()
+    if s["in_scale"] is not None:
+        w1 = w1 * _spread(s["in_scale"][e], 2 * F, D)
+        w2 = w2 * _spread(s["out_scale"][e], D, F)
+    rows = x.repeat_interleave(s["k"], 0)
+    gu = torch.bmm(w1, rows[:, :, None])[:, :, 0]
+    g, u = gu[:, :F], gu[:, F:]
+    h = g / (1.0 + torch.exp(-g)) * u
+    o = torch.bmm(w2, h[:, :, None])[:, :, 0]
+    o = torch.where(there[:, None], o, 0.0).view(T, s["k"], D)
+    return {"y": (o * val[:, :, None]).sum(1).to(s["x"].dtype), "col": col, "val": val}
+
+
+def _plain_train(s):
+    col, val, k, dy = s["col"].long(), s["val"], s["k"], s["grad"].float()
+    (T, D), E, F = s["x"].shape, s["w_in"].shape[0], s["w_out"].shape[2]
+    dev, n = col.device, T * k
+    flat = col.reshape(-1)
+    there = flat >= 0
+    # Every expert's rows side by side, filled up to the longest.
+    key = torch.where(there, flat, E)
+    order = torch.sort(key, stable=True).indices
+    count = torch.bincount(key, minlength=E + 1)
+    first = torch.cumsum(count, 0) - count
+    cap = max(1, int(count[:E].max()))
+    rank = torch.empty_like(flat)
+    rank[order] = torch.arange(n, device=dev) - first[key[order]]
+    slot = torch.where(there, key * cap + rank, E * cap)
+    token = torch.arange(n, device=dev) // k
+    w1, w2 = s["w_in"].float(), s["w_out"].float()
+
+    def grouped(rows):
+        out = rows.new_zeros(E * cap + 1, rows.shape[1])
+        out[slot] = rows[token]
+        return out[:-1].view(E, cap, -1)
+
+    def joined(o):
+        return torch.cat([o.reshape(E * cap, -1), o.new_zeros(1, o.shape[2])])[slot].view(T, k, -1)
+
+    def hidden(xs):
+        gu = torch.bmm(xs, w1.transpose(1, 2))
+        g, u = gu[:, :, :F], gu[:, :, F:]
+        sg = 1.0 / (1.0 + torch.exp(-g))
+        return g, u, sg, g * sg * u
+
+    h = hidden(grouped(s["x"].float()))[3]
+    y = (joined(torch.bmm(h, w2.transpose(1, 2))) * val[:, :, None]).sum(1)
+    xs = grouped(_plain_kept(s["x"]))
+    g, u, sg, h = hidden(xs)
+    ds = grouped(dy)
+    ws = val.new_zeros(E * cap + 1)
+    ws[slot] = val.reshape(-1)
+    ws = ws[:-1].view(E, cap, 1)
+    q = torch.bmm(ds, w2)
+    dval = joined((h * q).sum(2, keepdim=True)).view(T, k)
+    dh = q * ws
+    dgu = torch.cat([dh * u * sg * (1.0 + g * (1.0 - sg)), dh * g * sg], dim=2)
+    dx = joined(torch.bmm(dgu, w1)).sum(1)
+    dw_in = torch.bmm(dgu.transpose(1, 2), xs)
+    dw_out = torch.bmm(ds.transpose(1, 2), h * ws)
+    t = s["x"].dtype
+    return {"y": y.to(t), "grad_x": dx.to(t), "grad_w_in": dw_in.to(t), "grad_w_out": dw_out.to(t), "grad_val": dval}
+
+
+# ---------------------------------------------------------------- what a pass cannot do without
+
+def work(case):
+    T, D, b = case["T"], case["D"], _BYTES[case["dtype"]]
+    if case["kind"] == "norm":
+        size = 2 * T * D * b + D * _BYTES[case["weight"]] * (1 + case["bias"])
+        flops = 8 * T * D
+        if case["back"]:
+            size += 2 * T * D * b + D * _BYTES[case["weight"]] * (1 + case["bias"])
+            flops += 12 * T * D
+        return {"bytes": size, "flops": flops}
+    E, k, F = case["E"], case["k"], case["F"]
+    live = T * (1.0 - case["idle"])
+    used = E * (1.0 - (1.0 - k / E) ** live)  # experts with a token, were the choice uniform
+    if case["kind"] == "layer":
+        w = 3 * D * F * _BYTES[case["weights"]]
+        if case["weights"] == "e4m3":
+            w += 3 * D * F / _BLOCK ** 2 * 4
+        size = used * w + E * D * _BYTES[case["router"]] + 2 * T * D * b + T * k * 8
+        return {"bytes": size, "flops": 6.0 * live * k * D * F + 2.0 * T * E * D}
+    size = (used + E) * 3 * D * F * b + 4 * T * D * b + T * k * 12
+    return {"bytes": size, "flops": 22.0 * live * k * D * F}
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"norm": _exact_norm, "layer": _exact_layer, "train": _exact_train}[case["kind"]](s)
+
+
+def _exact_kept(x):
+    lo, hi = (-15, 15) if x.dtype == torch.float16 else (-117, 127)
+    out = x.double()
+    for c in range(0, x.shape[1], _BLOCK):
+        v = out[:, c:c + _BLOCK]
+        most = torch.where(torch.isfinite(v), v.abs(), 0.0).amax(1, keepdim=True)
+        s = torch.full_like(most, 2.0 ** lo)
+        for _ in range(lo, hi):  # the smallest one that is enough
+            more = most > 448.0 * s
+            if not bool(more.any()):
+                break
+            s = torch.where(more, 2.0 * s, s)
+        a = (v / s).abs()
+        step = torch.full_like(a, 2.0 ** -9)
+        for p in range(-5, 9):  # an eighth of the power of two at or below it, and no less than the smallest
+            step = torch.where(a >= 2.0 ** p, 2.0 ** (p - 3), step)
+        q = torch.round(a / step) * step
+        q = torch.minimum(q, torch.where(s == 2.0 ** (hi - 7), 240.0, 448.0))
+        out[:, c:c + _BLOCK] = torch.where(torch.isfinite(v), torch.sign(v) * q * s, math.nan)
+    return out
+
+
+def _exact_norm(s):
+    x, w = s["x"].double(), s["weight"].double()
+    var, mean = torch.var_mean(x, 1, correction=0, keepdim=True)
+    r = torch.rsqrt(var + 1e-5)
+    out = {"y": (x - mean) * r * w + (0.0 if s["bias"] is None else s["bias"].double())}
+    if s["grad"] is None:
+        return out
+    if s["keep"] == "e4m3":
+        x = _exact_kept(s["x"])
+    n, dy, D = (x - mean) * r, s["grad"].double(), x.shape[1]
+    p = n * dy
+    dot, total = p @ w, dy @ w
+    out["grad_x"] = r * (dy * w - (total / D)[:, None] - n * (dot / D)[:, None])
+    out["grad_weight"] = p.sum(0)
+    if s["bias"] is not None:
+        out["grad_bias"] = dy.sum(0)
+    return out
+
+
+def _exact_layer(s):
+    x = s["x"].double()
+    z = torch.nn.functional.linear(x, s["router"].double())
+    T, E = z.shape
+    k, G = s["k"], s["groups"]
+    key = (z if s["scores"] == "softmax" else torch.sigmoid(z)).clone()
+    if s["bias"] is not None:
+        key += s["bias"].double()
+    if s["active"] is not None:
+        key[~s["active"]] = -math.inf
+    alive = key > -math.inf
+    if G > 1:
+        cut = key.view(T, G, E // G)
+        two = 2 if s["scores"] == "sigmoid" and E // G > 1 else 1
+        rank = cut.topk(two, dim=2).values.sum(2).argsort(dim=1, descending=True, stable=True).argsort(dim=1)
+        cut[rank >= s["top"]] = -math.inf
+    rank = key.argsort(dim=1, descending=True, stable=True).argsort(dim=1)
+    taken = (rank < k) & (key > -math.inf)
+    if s["scores"] == "softmax":
+        p = torch.softmax(z.masked_fill(~(taken if s["renorm"] else alive), -math.inf), dim=1).nan_to_num(0.0)
+    else:
+        p = torch.sigmoid(z) * taken
+        if s["renorm"]:
+            p = p / (p.sum(1, keepdim=True) + 1e-20)
+    full = p * taken * s["scale"]
+    place = torch.where(taken, torch.cumsum(taken, 1) - 1, k)
+    val = torch.zeros(T, k + 1, dtype=torch.float64, device=x.device).scatter_(1, place, full)[:, :k]
+    y = torch.zeros_like(x)
+    F = s["w_out"].shape[2]
+
+    def weights(name, scale, e):
+        w = s[name][e].double()
+        if s[scale] is None:
+            return w
+        of_row = torch.arange(w.shape[0], device=w.device) // _BLOCK
+        of_col = torch.arange(w.shape[1], device=w.device) // _BLOCK
+        return w * s[scale][e].double()[of_row][:, of_col]
+
+    for e in range(E):
+        t = torch.nonzero(taken[:, e])[:, 0]
+        if len(t):
+            g, u = (x[t] @ weights("w_in", "in_scale", e).T).split(F, dim=1)
+            y[t] += full[t, e][:, None] * ((torch.nn.functional.silu(g) * u) @ weights("w_out", "out_scale", e).T)
+    return {"y": y, "col": None, "val": val}
+
+
+def _exact_train(s):
+    x, kept, col, val, dy = s["x"].double(), _exact_kept(s["x"]), s["col"], s["val"].double(), s["grad"].double()
+    E, F = s["w_in"].shape[0], s["w_out"].shape[2]
+    y, dx, dval = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(val)
+    dw_in = torch.zeros(s["w_in"].shape, dtype=torch.float64, device=x.device)
+    dw_out = torch.zeros(s["w_out"].shape, dtype=torch.float64, device=x.device)
+    for e in range(E):
+        t, i = torch.nonzero(col == e, as_tuple=True)
+        if not len(t):
+            continue
+        w1, w2, w = s["w_in"][e].double(), s["w_out"][e].double(), val[t, i][:, None]
+        g, u = (x[t] @ w1.T).split(F, dim=1)
+        y.index_add_(0, t, w * ((torch.nn.functional.silu(g) * u) @ w2.T))
+        g, u = (kept[t] @ w1.T).split(F, dim=1)
+        a, s1 = torch.nn.functional.silu(g), torch.sigmoid(g)
+        q = dy[t] @ w2
+        dval[t, i] = (a * u * q).sum(1)
+        dgu = torch.cat([w * q * u * (s1 + a * (1 - s1)), w * q * a], dim=1)
+        dx.index_add_(0, t, dgu @ w1)
+        dw_in[e] = dgu.T @ kept[t]
+        dw_out[e] = dy[t].T @ (w * a * u)
+    return {"y": y, "grad_x": dx, "grad_w_in": dw_in, "grad_w_out": dw_out, "grad_val": dval}
