@@ -555,6 +555,49 @@ spgemm_status spgemm_clip_grad_norm(int64_t count, const void *const *dGrads,
                                     float *dNorm, void *dWork,
                                     int64_t work_bytes, void *stream);
 
+/* ---- Layer norm, and rows kept in 8 bits ----------------------------------
+ * As the calls of the expert layer: asynchronous on `stream`, no allocation,
+ * workspaces and kept blocks of the caller. */
+
+typedef struct spgemm_layer_norm_desc {
+  int64_t rows, width;       /* T, D; D in [1, 16384]                          */
+  int64_t x_ld, grad_ld;     /* row strides of x and grad_y in elements, >= D  */
+  spgemm_dtype dtype;        /* of the rows: SPGEMM_F32, _BF16 or _F16         */
+  spgemm_dtype weight_dtype; /* of weight and bias: SPGEMM_F32 or dtype        */
+  float eps;                 /* >= 0                                           */
+  int32_t kept_form;         /* 0 nothing, 1 statistics, 2 rows in 8 bits too  */
+} spgemm_layer_norm_desc;
+
+/* Bytes of the kept block and of the backward pass's workspace (either may be
+ * NULL).  Errors of all three: INVALID_ARG (sizes, strides, types, eps,
+ * kept_form, null arrays, a workspace too small), INDEX_OVERFLOW, HIP. */
+spgemm_status spgemm_layer_norm_sizes(const spgemm_layer_norm_desc *desc,
+                                      int64_t *kept, int64_t *backward_work);
+
+/* y = (x - m) r w + b with m the row's mean and r = 1 / sqrt(v + eps), v the mean
+ * of (x - m)^2; y is T x D, contiguous, in x's type, rounded once.  w and b have D
+ * elements, b may be NULL.  Any alignment and stride.  kept_form 1 leaves m and r
+ * (fp32) in dKept; 2 also the rows of x in 8 bits, by blocks of 128 columns: with
+ * s the smallest power of two for which max |x| <= 448 s over the block's finite
+ * values, no smaller than 2^-15 (fp16) or 2^-117, x / s rounded to e4m3 (nearest,
+ * ties to even; at most 240 where s is 2^8, fp16, or 2^120); what is not finite
+ * is held as NaN. */
+spgemm_status spgemm_layer_norm_forward(const spgemm_layer_norm_desc *desc,
+                                        const void *dX, const void *dWeight,
+                                        const void *dBias, void *dY, void *dKept,
+                                        void *stream);
+
+/* With n = (x - m) r and a = dy w: dx = r (a - mean(a) - n mean(a n)) (T x D,
+ * contiguous, in x's type), dw = sum over rows of dy n and db = sum over rows of
+ * dy (dGradBias may be NULL) in the weights' type.  m and r are the kept ones; x
+ * is the tensor (kept_form 1) or what its 8 bits stand for (2; dX is not read and
+ * may be NULL).  Sums in fp32, in an order that the sizes alone fix.  Without rows
+ * dw and db are 0. */
+spgemm_status spgemm_layer_norm_backward(
+    const spgemm_layer_norm_desc *desc, const void *dX, const void *dWeight,
+    const void *dGradY, const void *dKept, void *dGradX, void *dGradWeight,
+    void *dGradBias, void *dWork, int64_t work_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

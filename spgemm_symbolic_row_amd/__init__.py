@@ -427,17 +427,22 @@ def transpose(A, out_rowptr64=False, pattern_only=False, no_alloc=False):
     return CsrDevice(trp, tcol, tval, X.n, X.m)
 
 
-_EXPERT_LAYER = ("Routing", "route", "route_backward", "dispatch", "experts", "experts_backward",
-                 "clip_grad_norm")
+_TORCH_MODULES = {
+    "expert_layer": ("Routing", "route", "route_backward", "dispatch", "experts",
+                     "experts_backward", "clip_grad_norm"),
+    "norm": ("layer_norm", "layer_norm_backward"),
+}
 if importlib.util.find_spec("torch"):  # else a star import would fail on these names
-    __all__ += _EXPERT_LAYER
+    for _names in _TORCH_MODULES.values():
+        __all__ += _names
 
 
 def __getattr__(name):
-    # The expert layer is loaded on first use: it imports torch.
-    if name in _EXPERT_LAYER:
-        from . import expert_layer
-        for n in _EXPERT_LAYER:
-            globals()[n] = getattr(expert_layer, n)
-        return globals()[name]
+    # The expert layer and the norm are loaded on first use: they import torch.
+    for module, names in _TORCH_MODULES.items():
+        if name in names:
+            found = importlib.import_module(f"{__name__}.{module}")
+            for n in names:
+                globals()[n] = getattr(found, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -17,6 +17,12 @@ class ExpertsDesc(ctypes.Structure):
                 ("unaligned", c_i32), ("reserved", c_i32)]
 
 
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("width", c_i64), ("x_ld", c_i64), ("grad_ld", c_i64),
+                ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("kept_form", c_i32)]
+
+
 def declare(L):
     """Argument types of the expert-layer entry points."""
     st, p64 = ctypes.c_int, ctypes.POINTER(c_i64)
@@ -41,3 +47,9 @@ def declare(L):
     L.spgemm_clip_grad_norm.restype = st
     L.spgemm_clip_grad_norm.argtypes = [c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.c_double,
                                         c_vp, c_vp, c_i64, c_vp]
+    L.spgemm_layer_norm_sizes.restype = st
+    L.spgemm_layer_norm_sizes.argtypes = [ctypes.POINTER(LayerNormDesc), p64, p64]
+    L.spgemm_layer_norm_forward.restype = st
+    L.spgemm_layer_norm_forward.argtypes = [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 6
+    L.spgemm_layer_norm_backward.restype = st
+    L.spgemm_layer_norm_backward.argtypes = [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 8 + [c_i64, c_vp]
