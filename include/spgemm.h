@@ -496,7 +496,9 @@ typedef struct spgemm_experts_desc {
   int32_t k;           /* slots of a row of R                                  */
   spgemm_dtype dtype;  /* SPGEMM_BF16 or SPGEMM_F16                            */
   int32_t unaligned;   /* 1: a base address is no multiple of 16 bytes         */
-  int32_t reserved;
+  int32_t kept_form;   /* 0: the kept block holds the pre-activations; 1: the
+                          rows of x in 8 bits (spgemm_layer_norm_forward has the
+                          form), about D bytes a token in place of 8 F an entry */
 } spgemm_experts_desc;
 
 /* Bytes of the kept block and of the two workspaces (any may be NULL).
@@ -524,7 +526,9 @@ spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
 
 /* Gradients of x (T x D), w_in, w_out (in the tensors' type) and of the
  * values (T x k, fp32, 0 in empty slots), for the routing that the forward pass
- * was given (the kept block holds it).  Every element is written: 0 for
+ * was given (the kept block holds it).  With kept_form 1 they are the gradients at
+ * the x that the 8 bits stand for, whose pre-activations are made again; dX is not
+ * read then and may be NULL.  Every element is written: 0 for
  * experts without tokens.  Sums in fp32, in an order that only the routing
  * fixes: the same call gives the same bits.  The gradients of g and u, and
  * w * h, are rounded once to the tensors' type before their products; in fp16

@@ -14,7 +14,7 @@ class RouteOptions(ctypes.Structure):
 class ExpertsDesc(ctypes.Structure):
     _fields_ = [("tokens", c_i64), ("experts", c_i64), ("width", c_i64), ("hidden", c_i64),
                 ("x_ld", c_i64), ("grad_ld", c_i64), ("k", c_i32), ("dtype", ctypes.c_int),
-                ("unaligned", c_i32), ("reserved", c_i32)]
+                ("unaligned", c_i32), ("kept_form", c_i32)]
 
 
 class LayerNormDesc(ctypes.Structure):

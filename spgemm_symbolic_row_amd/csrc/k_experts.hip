@@ -33,7 +33,7 @@
 #include <type_traits>
 #include <utility>
 
-#include "expert_common.hpp"
+#include "rows8.hpp"
 
 namespace sg {
 namespace {
@@ -1256,11 +1256,16 @@ Path path_of(const Sizes& z, bool keep) {
 // about half on average, else 128.
 int tile_rows(const Sizes& z) { return z.n > 256 * z.E ? 256 : 128; }
 
-// What the forward pass leaves for the backward pass.
+// What the forward pass leaves for the backward pass: the dispatch, and the
+// pre-activations (8 F bytes to an entry) or, in form 1, the rows of x in 8 bits,
+// from which the backward pass makes them again.  8192 tokens with 8 of 64 experts,
+// 2048 x 1024: 538 or 18 MB.
 struct Kept {
   Dispatch d;
   float* g;
   float* u;
+  uint8_t* code;
+  uint8_t* scale;
 };
 
 void take_dispatch(Carver& c, const Sizes& z, Dispatch& d) {
@@ -1273,9 +1278,14 @@ void take_dispatch(Carver& c, const Sizes& z, Dispatch& d) {
   d.ntiles = c.take<int32_t>(1);
 }
 
-Kept take_kept(Carver& c, const Sizes& z) {
+Kept take_kept(Carver& c, const Sizes& z, bool codes) {
   Kept k{};
   take_dispatch(c, z, k.d);
+  if (codes) {
+    k.code = c.take<uint8_t>(z.T * kept_pitch(z.D));
+    k.scale = c.take<uint8_t>(z.T * kept_blocks(z.D));
+    return k;
+  }
   k.g = c.take<float>(z.n * z.Fp);
   k.u = c.take<float>(z.n * z.Fp);
   return k;
@@ -1324,13 +1334,17 @@ struct BackwardWork {
   float* dgu_size;
   float* w_size;
   float* part;
+  // Of rows kept in 8 bits: what they stand for, and the pre-activations.
+  uint16_t* x;
+  float* g;
+  float* u;
   Padded pad;
 };
 
 // Partial sums of a value's gradient: one for each wave's columns.
 int dval_parts(const Sizes& z, int cols) { return (int)((z.Fp + cols - 1) / cols); }
 
-BackwardWork take_backward(Carver& c, const Sizes& z, bool scaled, bool padded) {
+BackwardWork take_backward(Carver& c, const Sizes& z, bool scaled, bool codes, bool padded) {
   BackwardWork w{};
   w.dgu = c.take<uint16_t>(z.n * z.S2);
   w.hw = c.take<uint16_t>(z.n * z.Fp);
@@ -1341,6 +1355,11 @@ BackwardWork take_backward(Carver& c, const Sizes& z, bool scaled, bool padded) 
     w.row_unit = c.take<float>(z.n);
     w.dgu_size = c.take<float>(z.E);
     w.w_size = c.take<float>(z.E);
+  }
+  if (codes) {
+    w.x = c.take<uint16_t>(z.T * z.Dp);
+    w.g = c.take<float>(z.n * z.Fp);
+    w.u = c.take<float>(z.n * z.Fp);
   }
   if (padded) w.pad = take_padded(c, z, true);
   return w;
@@ -1414,6 +1433,24 @@ ProductArgs base_args(const Sizes& z, const Dispatch& d) {
   return a;
 }
 
+// Of the first product: h to c, the pre-activations to g and u unless NULL.
+ProductArgs in_args(const Sizes& z, const Dispatch& d, const Rows& x, const Rows& w_in, void* h,
+                    float* g, float* u) {
+  ProductArgs a = base_args(z, d);
+  a.a = x.p;
+  a.lda = x.ld;
+  a.b = w_in.p;
+  a.ldb = w_in.ld;
+  a.b_expert = 2 * z.F * w_in.ld;
+  a.N = (int)z.F;
+  a.K = (int)z.D;
+  a.Kpad = (int)z.Dp;
+  a.c = h;
+  a.g = g;
+  a.u = u;
+  return a;
+}
+
 template <typename T>
 void combine(const Sizes& z, const float* rows, const int32_t* pos, const float* val,
              const float* unit, void* out, hipStream_t s) {
@@ -1429,7 +1466,9 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   Kept kp{};
   if (kept) {
     Carver c(kept);
-    kp = take_kept(c, z);
+    kp = take_kept(c, z, desc.kept_form);
+    if (desc.kept_form)
+      launch_rows_encode(desc.dtype, z.T, z.D, desc.x_ld, x, kp.code, kp.scale, s);
   } else {
     kp.d = w.d;
   }
@@ -1440,18 +1479,7 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   const Rows xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
   const Rows w1 = padded_rows(w_in, z.D, z.E * 2 * z.F, z.D, w.pad.w_in, s);
   const Rows w2 = padded_rows(w_out, z.F, z.E * z.D, z.F, w.pad.w_out, s);
-  ProductArgs a = base_args(z, kp.d);
-  a.a = xr.p;
-  a.lda = xr.ld;
-  a.b = w1.p;
-  a.ldb = w1.ld;
-  a.b_expert = 2 * z.F * w1.ld;
-  a.N = (int)z.F;
-  a.K = (int)z.D;
-  a.Kpad = (int)z.Dp;
-  a.c = w.h;
-  a.g = kp.g;
-  a.u = kp.u;
+  ProductArgs a = in_args(z, kp.d, xr, w1, w.h, kp.g, kp.u);
   a.k = z.k;
   a.col = col;
   const int64_t few = path == kPathDirect ? z.n : dispatch_max_tiles(z.n, z.E, kFewRows);
@@ -1496,8 +1524,12 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
               void* dw_in, void* dw_out, float* dval, const BackwardWork& w, hipStream_t s) {
   const Sizes z = sizes_of(desc);
   Carver kc((void*)kept);
-  const Kept kp = take_kept(kc, z);
-  const Rows xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
+  Kept kp = take_kept(kc, z, desc.kept_form);
+  Rows xr{w.x, z.Dp};
+  if (desc.kept_form)
+    launch_rows_decode(desc.dtype, z.T, z.D, kp.code, kp.scale, w.x, s);
+  else
+    xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
   const Rows gr = padded_rows(dy, desc.grad_ld, z.T, z.D, w.pad.dy, s);
   const Rows w1 = padded_rows(w_in, z.D, z.E * 2 * z.F, z.D, w.pad.w_in, s);
   const Rows w2 = padded_rows(w_out, z.F, z.E * z.D, z.F, w.pad.w_out, s);
@@ -1506,6 +1538,12 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
                        1, w.w_size);
   else if (z.S2 != 2 * z.F)
     hipLaunchKernelGGL(k_zero16, dim3(grid_for(z.n * z.S2)), dim3(256), 0, s, w.dgu, z.n * z.S2);
+  if (desc.kept_form) {
+    kp.g = w.g;
+    kp.u = w.u;
+    // h goes where w h will be.
+    product_by_rows<T, kIn>(in_args(z, kp.d, xr, w1, w.hw, w.g, w.u), z, s);
+  }
   ProductArgs a = base_args(z, kp.d);
   a.a = gr.p;
   a.lda = gr.ld;
@@ -1597,6 +1635,8 @@ spgemm_status check_desc(const spgemm_experts_desc* d) {
   if (d->tokens < 0 || d->experts < 1 || d->experts > kMaxExperts || d->k < 1 || d->k > 64)
     return refuse(SPGEMM_ERR_INVALID_ARG,
                   "experts: tokens < 0, experts outside [1, 1024] or k outside [1, 64]");
+  if (d->kept_form < 0 || d->kept_form > 1)
+    return refuse(SPGEMM_ERR_INVALID_ARG, "experts: kept_form outside [0, 1]");
   if (d->width < 1 || d->hidden < 1 || d->x_ld < d->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: empty width, or a row stride below it");
   if (d->x_ld >= 1 << 30 || d->grad_ld >= 1 << 30)
@@ -1635,7 +1675,7 @@ extern "C" spgemm_status spgemm_experts_sizes(const spgemm_experts_desc* desc, i
                       desc->grad_ld % 8;
   if (kept) {
     Carver c(nullptr);
-    take_kept(c, z);
+    take_kept(c, z, desc->kept_form);
     *kept = c.used;
   }
   if (forward_work) {
@@ -1645,7 +1685,7 @@ extern "C" spgemm_status spgemm_experts_sizes(const spgemm_experts_desc* desc, i
   }
   if (backward_work) {
     Carver c(nullptr);
-    take_backward(c, z, desc->dtype == SPGEMM_F16, padded);
+    take_backward(c, z, desc->dtype == SPGEMM_F16, desc->kept_form, padded);
     *backward_work = c.used;
   }
   return SPGEMM_OK;
@@ -1682,7 +1722,7 @@ extern "C" spgemm_status spgemm_experts_backward(
   if (st != SPGEMM_OK) return st;
   if (!dGradWIn || !dGradWOut || !dWork ||
       (desc->tokens > 0 &&
-       (!dX || !dWIn || !dWOut || !dGradY || !dKept || !dGradX || !dGradVal)))
+       ((!dX && !desc->kept_form) || !dWIn || !dWOut || !dGradY || !dKept || !dGradX || !dGradVal)))
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: null array");
   if (desc->grad_ld < desc->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: a row stride below the width");
@@ -1696,8 +1736,9 @@ extern "C" spgemm_status spgemm_experts_backward(
     return launched();
   }
   Carver c(dWork);
-  const BackwardWork w = take_backward(c, z, desc->dtype == SPGEMM_F16,
-                                       needs_padding(*desc, dX, dWIn, dWOut, dGradY));
+  const BackwardWork w =
+      take_backward(c, z, desc->dtype == SPGEMM_F16, desc->kept_form,
+                    needs_padding(*desc, desc->kept_form ? nullptr : dX, dWIn, dWOut, dGradY));
   if (work_bytes < c.used) return refuse(SPGEMM_ERR_INVALID_ARG, "experts: workspace too small");
   if (desc->dtype == SPGEMM_BF16)
     backward<__bf16>(*desc, dX, dWIn, dWOut, dGradY, dKept, dGradX, dGradWIn, dGradWOut,

@@ -108,4 +108,11 @@ __device__ __forceinline__ void store8_any(T* p, int n, const float v[8]) {
   }
 }
 
+// Rows of `ld` elements (bf16 or fp16) to rows of kept_pitch(D) codes and
+// kept_blocks(D) scales, and back to rows of kept_pitch(D) elements.
+void launch_rows_encode(spgemm_dtype type, int64_t rows, int64_t D, int64_t ld, const void* x,
+                        uint8_t* code, uint8_t* scale, hipStream_t s);
+void launch_rows_decode(spgemm_dtype type, int64_t rows, int64_t D, const uint8_t* code,
+                        const uint8_t* scale, void* x, hipStream_t s);
+
 }  // namespace sg

@@ -200,8 +200,8 @@ def dispatch(col, n_experts):
 
 
 @lru_cache(maxsize=1024)
-def _experts_desc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned):
-    d = ExpertsDesc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned, 0)
+def _experts_desc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned, kept_form):
+    d = ExpertsDesc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned, kept_form)
     sizes = [c_i64(), c_i64(), c_i64()]
     _check(_lib().spgemm_experts_sizes(d, *map(ctypes.byref, sizes)))
     return d, sizes[0].value, sizes[1].value, sizes[2].value
@@ -209,8 +209,8 @@ def _experts_desc(T, E, D, F, x_ld, grad_ld, k, dt, unaligned):
 
 class _Kept:
     """What a forward pass keeps for its backward pass: its inputs (borrowed,
-    and not to be changed before), the library's block, and the stream that
-    the block was taken from."""
+    and not to be changed before; x is None where the block holds it in 8 bits), the
+    library's block, and the stream that the block was taken from."""
     __slots__ = ("x", "w_in", "w_out", "val", "block", "stream")
 
     def __init__(self, *a):
@@ -229,8 +229,17 @@ def experts(x, w_in, w_out, col, val, keep=False):
     val * W_out[e] (silu(W_gate[e] x_t) * (W_up[e] x_t)).
 
     x: T x D (rows contiguous), w_in: E x 2F x D, an expert's gate rows before
-    its up rows, w_out: E x D x F; all bfloat16 or all float16.  With keep
-    also returns what experts_backward takes."""
+    its up rows, w_out: E x D x F; all bfloat16 or all float16.  With keep=True
+    also returns what experts_backward takes: the pre-activations, 8 F bytes for
+    every entry.  With keep="e4m3" that is x in 8 bits instead (a power-of-two
+    scale for each 128 columns), about D bytes a token: x need not stay, the
+    gradients are those at the values that the 8 bits stand for, and the
+    backward pass makes the first product again."""
+    form = 0
+    if isinstance(keep, str):
+        if keep != "e4m3":
+            raise ValueError("keep must be False, True or 'e4m3'")
+        form = 1
     x_ld = _rows(x, "x")
     T, D = x.shape
     if w_in.dim() != 3 or w_out.dim() != 3 or col.dim() != 2:
@@ -245,7 +254,7 @@ def experts(x, w_in, w_out, col, val, keep=False):
     _dense(val, (T, k), torch.float32, dev, "val")
     _unrecorded(x, w_in, w_out, val)
     d, kept_bytes, work_bytes, _ = _experts_desc(T, E, D, F, x_ld, D, k, _TYPES[x.dtype],
-                                                 _off16(x, w_in, w_out))
+                                                 _off16(x, w_in, w_out), form)
     with _on(x):
         y = torch.empty(T, D, dtype=x.dtype, device=dev)
         block = torch.empty(kept_bytes, dtype=torch.uint8, device=dev) if keep else None
@@ -255,36 +264,36 @@ def experts(x, w_in, w_out, col, val, keep=False):
                                              col.data_ptr(), val.data_ptr(), y.data_ptr(),
                                              block.data_ptr() if keep else None, work.data_ptr(),
                                              work_bytes, stream))
-    return (y, _Kept(x, w_in, w_out, val, block, stream)) if keep else y
+    return (y, _Kept(None if form else x, w_in, w_out, val, block, stream)) if keep else y
 
 
 def experts_backward(grad_y, kept):
     """Gradients (grad_x, grad_w_in, grad_w_out, grad_val) of `experts` for the
     gradient of y (T x D, rows contiguous), from what its pass kept."""
     x, w_in, w_out, val = kept.x, kept.w_in, kept.w_out, kept.val
-    if grad_y.shape != x.shape:
-        raise ValueError(f"grad_y must have shape {tuple(x.shape)}, got {tuple(grad_y.shape)}")
-    if grad_y.dtype != x.dtype or grad_y.device != x.device:
-        raise TypeError(f"grad_y must be {x.dtype} on {x.device}")
+    (T, k), (E, D, F), dtype, dev = val.shape, w_out.shape, w_in.dtype, w_in.device
+    if grad_y.shape != (T, D):
+        raise ValueError(f"grad_y must have shape {(T, D)}, got {tuple(grad_y.shape)}")
+    if grad_y.dtype != dtype or grad_y.device != dev:
+        raise TypeError(f"grad_y must be {dtype} on {dev}")
     _unrecorded(grad_y)
-    x_ld, g_ld = _rows(x, "x"), _rows(grad_y, "grad_y")
-    T, D = x.shape
-    E, F, k, dev = w_out.shape[0], w_out.shape[2], val.shape[1], x.device
-    d, _, _, work_bytes = _experts_desc(T, E, D, F, x_ld, g_ld, k, _TYPES[x.dtype],
-                                        _off16(x, w_in, w_out, grad_y))
-    with _on(x):
-        gx = torch.empty(T, D, dtype=x.dtype, device=dev)
+    inputs = (w_in, w_out) if x is None else (x, w_in, w_out)
+    d, _, _, work_bytes = _experts_desc(T, E, D, F, D if x is None else _rows(x, "x"),
+                                        _rows(grad_y, "grad_y"), k, _TYPES[dtype],
+                                        _off16(*inputs, grad_y), int(x is None))
+    with _on(w_in):
+        gx = torch.empty(T, D, dtype=dtype, device=dev)
         gw_in, gw_out = torch.empty_like(w_in), torch.empty_like(w_out)
         gval = torch.empty_like(val)
-        stream = _stream(x)
+        stream = _stream(w_in)
         if stream != kept.stream:
             # What only `kept` may still hold is not given away before this stream is done with it.
-            for t in (x, w_in, w_out, kept.block):
+            for t in (*inputs, kept.block):
                 t.record_stream(torch.cuda.current_stream(dev))
         work = torch.empty(max(work_bytes, 1), dtype=torch.uint8, device=dev)
         _check(_lib().spgemm_experts_backward(
-            d, x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(), grad_y.data_ptr(),
-            kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
+            d, None if x is None else x.data_ptr(), w_in.data_ptr(), w_out.data_ptr(),
+            grad_y.data_ptr(), kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
             gw_out.data_ptr(), gval.data_ptr(), work.data_ptr(), work_bytes, stream))
     return gx, gw_in, gw_out, gval
 
