@@ -193,7 +193,7 @@ def _run_own(s):
             out["grad_bias"] = db
         return out
     if s["kind"] == "layer":
-        y, r = sg.expert_layer(s["x"], s["router"], s["w_in"], s["w_out"], s["k"], in_scale=s["in_scale"],
+        y, r = sg.expert_step(s["x"], s["router"], s["w_in"], s["w_out"], s["k"], in_scale=s["in_scale"],
                                out_scale=s["out_scale"], scores=s["scores"], bias=s["bias"], groups=s["groups"],
                                top_groups=s["top"], renormalise=s["renorm"], scale=s["scale"], active=s["active"])
         return {"y": y, "col": r.col, "val": r.val}
