@@ -56,7 +56,8 @@ typedef enum spgemm_dtype {
   SPGEMM_F32 = 0, /* CSR values, logits, gradients */
   SPGEMM_F64 = 1, /* CSR values                    */
   SPGEMM_BF16 = 2, /* the expert layer's tensors   */
-  SPGEMM_F16 = 3
+  SPGEMM_F16 = 3,
+  SPGEMM_E4M3 = 4 /* weights of spgemm_expert_step   */
 } spgemm_dtype;
 
 /* Optional device allocator: return a device pointer of at least `bytes`
@@ -540,6 +541,39 @@ spgemm_status spgemm_experts_backward(
     const void *dWOut, const void *dGradY, const void *dKept, void *dGradX,
     void *dGradWIn, void *dGradWOut, float *dGradVal, void *dWork,
     int64_t work_bytes, void *stream);
+
+/* A whole expert layer for up to 16 tokens, as a decode step has them: logits,
+ * routing and the experts' products in two launches. */
+typedef struct spgemm_expert_step_desc {
+  int64_t tokens, experts, width, hidden; /* T, E, D, F; T in [0, 16]          */
+  int64_t x_ld;              /* row stride of x in elements, at least D        */
+  int32_t k;
+  spgemm_dtype dtype;        /* of x and y: SPGEMM_BF16 or SPGEMM_F16          */
+  spgemm_dtype weight_dtype; /* of w_in and w_out: dtype or SPGEMM_E4M3        */
+  spgemm_dtype router_dtype; /* dtype or SPGEMM_F32                            */
+  spgemm_route_options route;
+} spgemm_expert_step_desc;
+
+/* z = router x (router E x D; sums in 64 bits, rounded to fp32), then dCol and
+ * dVal (T x k) as spgemm_route gives them for z, then y (T x D, contiguous) as
+ * spgemm_experts_forward does; the columns are the routing's, so that y is the
+ * layer's whole result.  All arrays but x are contiguous; any alignment.
+ * With SPGEMM_E4M3 an expert's weight is W[r, c] = w[r, c] s[r / 128, c / 128]:
+ * dInScale is E x ceil(2F / 128) x ceil(D / 128), dOutScale E x ceil(D / 128) x
+ * ceil(F / 128), fp32; else they are not read.  The 8-bit values are multiplied as
+ * they are, in x's type, and the scales applied in fp32 to the sums over 64
+ * columns.  Products and sums in fp32, in an order that the sizes and the picked
+ * experts fix; the hidden vector is rounded once to x's type (in fp16 it has to be
+ * below 65504), y once.
+ * Errors: INVALID_ARG (as spgemm_route; more than 16 tokens; types, strides, null
+ * arrays, a workspace too small), INDEX_OVERFLOW (a width above 2^22), HIP. */
+spgemm_status spgemm_expert_step_workspace(const spgemm_expert_step_desc *desc,
+                                            int64_t *bytes);
+spgemm_status spgemm_expert_step(
+    const spgemm_expert_step_desc *desc, const void *dX, const void *dRouter,
+    const float *dBias, const uint8_t *dActive, const void *dWIn,
+    const float *dInScale, const void *dWOut, const float *dOutScale, void *dY,
+    int32_t *dCol, float *dVal, void *dWork, int64_t work_bytes, void *stream);
 
 /* The global norm of `count` tensors (fp32, bf16 or fp16, mixed at will) and
  * its clipping: norm = sqrt(sum g^2) in fp64, rounded into dNorm (1 fp32);

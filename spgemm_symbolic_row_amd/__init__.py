@@ -429,7 +429,7 @@ def transpose(A, out_rowptr64=False, pattern_only=False, no_alloc=False):
 
 _TORCH_MODULES = {
     "expert_layer": ("Routing", "route", "route_backward", "dispatch", "experts",
-                     "experts_backward", "clip_grad_norm"),
+                     "experts_backward", "expert_step", "clip_grad_norm"),
     "norm": ("layer_norm", "layer_norm_backward"),
 }
 if importlib.util.find_spec("torch"):  # else a star import would fail on these names

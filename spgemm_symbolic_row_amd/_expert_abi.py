@@ -17,6 +17,13 @@ class ExpertsDesc(ctypes.Structure):
                 ("unaligned", c_i32), ("kept_form", c_i32)]
 
 
+class ExpertStepDesc(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("experts", c_i64), ("width", c_i64), ("hidden", c_i64),
+                ("x_ld", c_i64), ("k", c_i32), ("dtype", ctypes.c_int),
+                ("weight_dtype", ctypes.c_int), ("router_dtype", ctypes.c_int),
+                ("route", RouteOptions)]
+
+
 class LayerNormDesc(ctypes.Structure):
     _fields_ = [("rows", c_i64), ("width", c_i64), ("x_ld", c_i64), ("grad_ld", c_i64),
                 ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("eps", ctypes.c_float),
@@ -53,3 +60,7 @@ def declare(L):
     L.spgemm_layer_norm_forward.argtypes = [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 6
     L.spgemm_layer_norm_backward.restype = st
     L.spgemm_layer_norm_backward.argtypes = [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 8 + [c_i64, c_vp]
+    L.spgemm_expert_step_workspace.restype = st
+    L.spgemm_expert_step_workspace.argtypes = [ctypes.POINTER(ExpertStepDesc), p64]
+    L.spgemm_expert_step.restype = st
+    L.spgemm_expert_step.argtypes = [ctypes.POINTER(ExpertStepDesc)] + [c_vp] * 12 + [c_i64, c_vp]

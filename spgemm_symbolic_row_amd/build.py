@@ -31,7 +31,7 @@ SOURCES = ["k_util.hip", "k_light.hip", "k_outer.hip", "k_multisplit.hip", "k_he
            "k_chunks.hip", "k_chunkhist.hip", "k_prune.hip", "k_transpose.hip", "k_estimate.hip",
            "noalloc.hip",
            "k_dispatch.hip", "k_route.hip", "k_experts.hip", "k_gradnorm.hip",
-           "k_norm.hip", "k_rows8.hip",
+           "k_norm.hip", "k_rows8.hip", "k_step.hip",
            "api.cpp",
            "params.cpp"]
 

@@ -28,9 +28,10 @@ import torch
 
 import spgemm_symbolic_row_amd as _package
 
-from ._expert_abi import ExpertsDesc, RouteOptions, c_i64
+from ._expert_abi import ExpertStepDesc, ExpertsDesc, RouteOptions, c_i64
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 2, torch.float16: 3}
+_E4M3 = 4
 
 
 def _lib():
@@ -296,6 +297,74 @@ def experts_backward(grad_y, kept):
             grad_y.data_ptr(), kept.block.data_ptr(), gx.data_ptr(), gw_in.data_ptr(),
             gw_out.data_ptr(), gval.data_ptr(), work.data_ptr(), work_bytes, stream))
     return gx, gw_in, gw_out, gval
+
+
+@lru_cache(maxsize=1024)
+def _step_desc(T, E, D, F, x_ld, k, dt, weight_dt, router_dt, *how):
+    o = _route_options(*how)
+    d = ExpertStepDesc(T, E, D, F, x_ld, k, dt, weight_dt, router_dt, o)
+    need = c_i64()
+    _check(_lib().spgemm_expert_step_workspace(d, ctypes.byref(need)))
+    return d, need.value, o
+
+
+def expert_step(x, w_router, w_in, w_out, k, in_scale=None, out_scale=None, scores="softmax",
+                bias=None, groups=1, top_groups=0, renormalise=True, scale=1.0, active=None):
+    """(y, Routing) of a whole expert layer for a few tokens, as a decode step
+    has them: route(x w_router^T, k, ...) and experts(...) in two launches.
+
+    x: T x D (T up to 16, rows contiguous; bfloat16 or float16), w_router: E x D (x's type or
+    float32), w_in: E x 2F x D and w_out: E x D x F in x's type; or both in
+    float8_e4m3fn, with float32 scales for every 128 x 128 block of an expert:
+    in_scale E x ceil(2F / 128) x ceil(D / 128), out_scale E x ceil(D / 128) x
+    ceil(F / 128).  The other arguments are route's.  The logits' sums are made in
+    64 bits.  Nothing is kept for gradients."""
+    x_ld = _rows(x, "x")
+    T, D = x.shape
+    if w_in.dim() != 3 or w_out.dim() != 3 or w_router.dim() != 2:
+        raise ValueError("w_in and w_out must have three dimensions, w_router two")
+    if T > 16:
+        raise ValueError("at most 16 tokens: route and experts take more")
+    E, F = w_out.shape[0], w_out.shape[2]
+    t, tw, dev = x.dtype, w_in.dtype, x.device
+    if t not in (torch.bfloat16, torch.float16):
+        raise TypeError("x must be bfloat16 or float16")
+    if tw not in (t, torch.float8_e4m3fn):
+        raise TypeError("weights must be of x's type or float8_e4m3fn")
+    if w_router.dtype not in (t, torch.float32):
+        raise TypeError("w_router must be float32 or of x's type")
+    _dense(w_router, (E, D), w_router.dtype, dev, "w_router")
+    _dense(w_in, (E, 2 * F, D), tw, dev, "w_in")
+    _dense(w_out, (E, D, F), tw, dev, "w_out")
+    if tw is t:
+        if in_scale is not None or out_scale is not None:
+            raise ValueError("only float8_e4m3fn weights have scales")
+        _unrecorded(x, w_router, w_in, w_out)
+    else:
+        if in_scale is None or out_scale is None:
+            raise ValueError("float8_e4m3fn weights need in_scale and out_scale")
+        _dense(in_scale, (E, -(-2 * F // 128), -(-D // 128)), torch.float32, dev, "in_scale")
+        _dense(out_scale, (E, -(-D // 128), -(-F // 128)), torch.float32, dev, "out_scale")
+        _unrecorded(x, w_router, in_scale, out_scale)
+    if bias is not None:
+        _dense(bias, (E,), torch.float32, dev, "bias")
+    if active is not None:
+        _dense(active, (T,), torch.bool, dev, "active")
+    d, need, o = _step_desc(T, E, D, F, x_ld, k, _TYPES[t], _TYPES.get(tw, _E4M3),
+                            _TYPES[w_router.dtype], scores, groups, top_groups, bool(renormalise),
+                            float(scale))
+    with _on(x):
+        y = torch.empty(T, D, dtype=t, device=dev)
+        col = torch.empty(T, k, dtype=torch.int32, device=dev)
+        val = torch.empty(T, k, dtype=torch.float32, device=dev)
+        work = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(_lib().spgemm_expert_step(
+            d, x.data_ptr(), w_router.data_ptr(), None if bias is None else bias.data_ptr(),
+            None if active is None else active.data_ptr(), w_in.data_ptr(),
+            None if in_scale is None else in_scale.data_ptr(), w_out.data_ptr(),
+            None if out_scale is None else out_scale.data_ptr(), y.data_ptr(), col.data_ptr(),
+            val.data_ptr(), work.data_ptr(), need, _stream(x)))
+    return y, Routing(col, val, E, o, bias)
 
 
 def clip_grad_norm(grads, max_norm, out=None):
