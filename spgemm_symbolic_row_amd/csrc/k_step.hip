@@ -16,6 +16,7 @@
 // below its own, whose holders run and never wait for higher ones: however few work
 // groups are on the chip at a time, every wait ends.
 #include <algorithm>
+#include <type_traits>
 
 #include "route_row.hpp"
 #include "rows8.hpp"
@@ -94,51 +95,55 @@ __global__ __launch_bounds__(256) void k_step_logits(LogitArgs a) {
 
 // ---- weights ----
 
-// A lane's share of one step of its row: 16 values from k = 64 s + 16 (l / 16).
-// 16-bit weights are the operands as they are; 8-bit ones are decoded when used,
-// exactly, to x's type.
+// A lane's share of one step of its row: 16 values from k = 64 s + 16 (l / 16), at
+// a uniform address plus the lane's offset.  16-bit weights are the operands as
+// they are; 8-bit ones are decoded when used, exactly, to x's type.
 template <typename T, bool k8>
 struct Share {
-  typedef T E;
+  static constexpr int kBytes = 2;
   s16x8 v[2];
-  __device__ void load(const void* row, int k) {
-    __builtin_memcpy(v, (const T*)row + k, 32);
-  }
-  __device__ void load_end(const void* row, int k, int K) {
-    const short* p = (const short*)row;
+  __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 32); }
+  // The n values that the row still has; zeros beyond.
+  __device__ void load_end(const char* base, uint32_t off, int n) {
+    const short* p = (const short*)(base + off);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = k + j < K ? p[k + j] : (short)0;
+    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = j < n ? p[j] : (short)0;
   }
   __device__ s16x8 half(int h) const { return v[h]; }
 };
 
 template <typename T>
 struct Share<T, true> {
-  typedef uint8_t E;
+  static constexpr int kBytes = 1;
   uint32_t v[4];
-  __device__ void load(const void* row, int k) {
-    __builtin_memcpy(v, (const uint8_t*)row + k, 16);
-  }
-  __device__ void load_end(const void* row, int k, int K) {
-    const uint8_t* p = (const uint8_t*)row;
+  __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 16); }
+  __device__ void load_end(const char* base, uint32_t off, int n) {
+    const uint8_t* p = (const uint8_t*)(base + off);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (k + 4 * i + j < K) v[i] |= (uint32_t)p[k + 4 * i + j] << (8 * j);
+        if (4 * i + j < n) v[i] |= (uint32_t)p[4 * i + j] << (8 * j);
     }
   }
   __device__ s16x8 half(int h) const {
-    s16x8 r;
+    uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float f[4];
-      decode4(v[2 * h + i], f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r[4 * i + j] = __builtin_bit_cast(short, from_f32<T>(f[j]));
+      if constexpr (__is_same(T, __bf16)) {
+        r[2 * i] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i], 1.0f, false));
+        r[2 * i + 1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i], 1.0f, true));
+      } else {
+        r[2 * i] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + i], 1.0f, false));
+        r[2 * i + 1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + i], 1.0f, true));
+      }
     }
-    return r;
+    return __builtin_bit_cast(s16x8, r);
   }
 };
 
@@ -199,7 +204,6 @@ template <typename T, bool k8, int V>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4, 4))) void k_step(
     LayerArgs a) {
   typedef Share<T, k8> W;
-  typedef typename W::E WE;
   extern __shared__ uint32_t lds[];
   const int k = a.row.k, n = a.T * k, E = a.row.E;
   int32_t* cols = (int32_t*)lds;                      // n
@@ -259,59 +263,71 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
   const uint32_t in_tiles = (uint32_t)used * in_cols, all = in_tiles + out_cols;
   const int quarter = l >> 4, column = l & 15;
   uint32_t tile = __builtin_amdgcn_readfirstlane(ticket);
-  while (tile < all) {
+  // The number of the tile after this one, taken early.
+  auto take = [&]() {
     __syncthreads();  // `ticket` and `part` have been read
     if (tid == 0) ticket = __hip_atomic_fetch_add(&a.counters->ticket, 1u, __ATOMIC_RELAXED,
                                                   __HIP_MEMORY_SCOPE_AGENT);
-    if (tile < in_tiles) {
+  };
+  while (tile < in_tiles) {
+      take();
       // h of expert u's tokens, 16 columns.
-      const int u = tile / in_cols, f0 = tile % in_cols * 16, e = expert[u];
-      const int f = min(f0 + column, a.F - 1);
-      const WE* base = (const WE*)a.w_in + (int64_t)e * 2 * a.F * a.D;
-      const WE* wg = base + (int64_t)f * a.D;
-      const WE* wu = base + (int64_t)(a.F + f) * a.D;
+      const int u = tile / in_cols, f0 = (int)(tile % in_cols) * 16;
+      const int e = __builtin_amdgcn_readfirstlane(expert[u]);
+      const int64_t row_bytes = (int64_t)a.D * W::kBytes;
+      const char* gate = (const char*)a.w_in + ((int64_t)e * 2 * a.F + f0) * row_bytes;
+      const char* up = gate + a.F * row_bytes;
+      const uint32_t off =
+          (uint32_t)min(column, a.F - 1 - f0) * (uint32_t)row_bytes + quarter * 16 * W::kBytes;
       Scales sg{}, su{};
       if constexpr (k8) {
         sg = scales_of(a.in_scale, e, f0, 2 * a.F, a.D);
         su = scales_of(a.in_scale, e, a.F + f0, 2 * a.F, a.D);
       }
-      const T* x = (const T*)a.x + min(column, a.T - 1) * a.x_ld;
-      f32x4 g = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+      const T* x = (const T*)a.x + min(column, a.T - 1) * a.x_ld + quarter * 16;
+      f32x4 g = {0, 0, 0, 0}, v = {0, 0, 0, 0};
       const int full = a.D / kStep;
-      constexpr int kBatch = 4;
-      for (int s0 = wave; s0 < full; s0 += kWaves * kBatch) {
-        W w1[kBatch], w2[kBatch];
-        s16x8 xf[kBatch][2];
+      int s = wave;
+      // B steps at once.
+      auto batches = [&](auto count) {
+        constexpr int B = decltype(count)::value;
+        for (; s + (B - 1) * kWaves < full; s += B * kWaves) {
+          W w1[B], w2[B];
+          s16x8 xf[B][2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int s = min(s0 + i * kWaves, full - 1);  // beyond the last, that again
-          w1[i].load(wg, s * kStep + quarter * 16);
-          w2[i].load(wu, s * kStep + quarter * 16);
-          __builtin_memcpy(xf[i], x + s * kStep + quarter * 16, 32);
-        }
+          for (int i = 0; i < B; ++i) {
+            const int64_t at = (int64_t)s * (kStep * W::kBytes) + i * kWaves * kStep * W::kBytes;
+            w1[i].load(gate + at, off);
+            w2[i].load(up + at, off);
+          }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int s = s0 + i * kWaves;
-          if (s < full) {
-            multiply<T, k8>(w1[i], xf[i], sg, s * kStep / kBlock, g);
-            multiply<T, k8>(w2[i], xf[i], su, s * kStep / kBlock, up);
+          for (int i = 0; i < B; ++i) __builtin_memcpy(xf[i], x + (s + i * kWaves) * kStep, 32);
+          __builtin_amdgcn_sched_barrier(0);  // all loads before the first product
+#pragma unroll
+          for (int i = 0; i < B; ++i) {
+            const int block = (s + i * kWaves) * kStep / kBlock;
+            multiply<T, k8>(w1[i], xf[i], sg, block, g);
+            multiply<T, k8>(w2[i], xf[i], su, block, v);
           }
         }
-      }
+      };
+      batches(std::integral_constant<int, 4>{});
+      batches(std::integral_constant<int, 2>{});
+      batches(std::integral_constant<int, 1>{});
       if (full * kStep < a.D && wave == full % kWaves) {
-        const int at = full * kStep + quarter * 16;
-        W w1, w2;
+        const int left = a.D - full * kStep - quarter * 16;
+        W w;
         Share<T, false> xe;
-        w1.load_end(wg, at, a.D);
-        w2.load_end(wu, at, a.D);
-        xe.load_end(x, at, a.D);
-        multiply<T, k8>(w1, xe.v, sg, full * kStep / kBlock, g);
-        multiply<T, k8>(w2, xe.v, su, full * kStep / kBlock, up);
+        xe.load_end((const char*)(x + full * kStep), 0, left);
+        w.load_end(gate + full * kStep * W::kBytes, off, left);
+        multiply<T, k8>(w, xe.v, sg, full * kStep / kBlock, g);
+        w.load_end(up + full * kStep * W::kBytes, off, left);
+        multiply<T, k8>(w, xe.v, su, full * kStep / kBlock, v);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         part[wave][0][quarter * 4 + j][column] = g[j];
-        part[wave][1][quarter * 4 + j][column] = up[j];
+        part[wave][1][quarter * 4 + j][column] = v[j];
       }
       __syncthreads();
       // A pair of columns to a thread.
@@ -333,69 +349,114 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
         __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + f0 + c), pair,
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+      // The stores are written through and done before the tile is counted.  A release
+      // at this scope would also write the L2's other lines back.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (tid == 0)
-        __hip_atomic_fetch_add(&a.counters->done, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
-    } else {
-      // 16 columns of y: the steps of all picked experts in one row, step q being
-      // step q % per of expert q / per.
+        __hip_atomic_fetch_add(&a.counters->done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      tile = __builtin_amdgcn_readfirstlane(ticket);
+  }
+  bool ready = false;  // all of h is there
+  while (tile < all) {
+      take();
+      // 16 columns of y: the steps of all picked experts in one row, of which a
+      // wave takes every eighth.
       const int n0 = (int)(tile - in_tiles) * 16;
-      const int row = min(n0 + column, a.D - 1);
-      const int full = a.F / kStep, steps = used * full;
-      constexpr int kBatch = 8;
-      W w[kBatch];
-      auto row_of = [&](int e) { return (const WE*)a.w_out + ((int64_t)e * a.D + row) * a.F; };
-      auto fetch = [&](int q0) {
+      const int full = a.F / kStep;
+      const int64_t row_bytes = (int64_t)a.F * W::kBytes;
+      const uint32_t off =
+          (uint32_t)min(column, a.D - 1 - n0) * (uint32_t)row_bytes + quarter * 16 * W::kBytes;
+      auto rows_of = [&](int u) {
+        const int e = __builtin_amdgcn_readfirstlane(expert[u]);
+        return (const char*)a.w_out + ((int64_t)e * a.D + n0) * row_bytes;
+      };
+      // Step s of expert u; beyond the last one there is none.
+      struct Place { int u, s; };
+      auto settle = [&](Place& p) {
+        while (p.s >= full && p.u < used) p.s -= full, ++p.u;
+      };
+      constexpr int kBatch = 8, kHalf = 4;
+      auto fetch = [&](Place p, W (&w)[kBatch]) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int q = min(q0 + i * kWaves, steps - 1);
-          w[i].load(row_of(expert[q / full]), q % full * kStep + quarter * 16);
+          settle(p);
+          const bool there = p.u < used;  // else the last one again
+          w[i].load(rows_of(there ? p.u : used - 1) +
+                        (int64_t)(there ? p.s : full - 1) * (kStep * W::kBytes), off);
+          p.s += kWaves;
         }
       };
-      if (steps) fetch(wave);
-      if (tid == 0)
-        while (__hip_atomic_load(&a.counters->done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <
-               in_tiles)
-          __builtin_amdgcn_s_sleep(4);
-      __syncthreads();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      auto wait = [&]() {
+        if (ready) return;
+        if (tid == 0)
+          while (__hip_atomic_load(&a.counters->done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <
+                 in_tiles)
+            __builtin_amdgcn_s_sleep(1);
+        __syncthreads();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+        ready = true;
+      };
       f32x4 sum = {0, 0, 0, 0};
-      // Adds expert u's products of one step, weighted by each token's value for it.
-      auto add = [&](const W& w, int u, int s, bool end) {
+      // The token's row of h for expert u, and its value; null where it did not pick it.
+      struct Row { const uint16_t* h; float value; };
+      auto row_of = [&](int u) {
         const int i = column < a.T ? slot[u * kTokens + column] : -1;
-        const int64_t entry = column * k + i;
-        Share<T, false> h;
-        if (i < 0) {
-          h.v[0] = h.v[1] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-        } else {
-          const uint16_t* p = a.h + entry * a.h_ld;
-          if (end) h.load_end(p, s * kStep + quarter * 16, a.F);
-          else h.load(p, s * kStep + quarter * 16);
-        }
+        const int entry = i < 0 ? 0 : column * k + i;
+        return Row{i < 0 ? nullptr : a.h + (int64_t)entry * a.h_ld + quarter * 16, vals[entry]};
+      };
+      auto add = [&](const W& w, const s16x8 (&h)[2], const Row& r, int u, int s) {
         Scales sc{};
-        if constexpr (k8) sc = scales_of(a.out_scale, expert[u], n0, a.D, a.F);
+        if constexpr (k8)
+          sc = scales_of(a.out_scale, __builtin_amdgcn_readfirstlane(expert[u]), n0, a.D, a.F);
         f32x4 acc = {0, 0, 0, 0};
-        multiply<T, k8>(w, h.v, sc, s * kStep / kBlock, acc);
-        const float weight = i < 0 ? 0.0f : vals[entry];
+        multiply<T, k8>(w, h, sc, s * kStep / kBlock, acc);
         // What a token did not pick adds nothing, whatever its weights hold.
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] += i < 0 ? 0.0f : weight * acc[j];
+        for (int j = 0; j < 4; ++j) sum[j] += r.h ? r.value * acc[j] : 0.0f;
       };
-      for (int q0 = wave; q0 < steps;) {
+      if (full && used) {
+        W w[kBatch];
+        Place at{0, wave};
+        settle(at);
+        fetch(at, w);
+        __builtin_amdgcn_sched_barrier(0);
+        wait();
+        while (true) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int q = q0 + i * kWaves;
-          if (q < steps) add(w[i], q / full, q % full, false);
+          for (int i0 = 0; i0 < kBatch; i0 += kHalf) {
+            Place p[kHalf];
+            Row r[kHalf];
+            s16x8 h[kHalf][2];
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+              p[i] = at;
+              r[i] = row_of(min(at.u, used - 1));
+              h[i][0] = h[i][1] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+              if (r[i].h && at.u < used) __builtin_memcpy(h[i], r[i].h + at.s * kStep, 32);
+              at.s += kWaves;
+              settle(at);
+            }
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i)
+              if (p[i].u < used) add(w[i0 + i], h[i], r[i], p[i].u, p[i].s);
+          }
+          if (at.u >= used) break;
+          fetch(at, w);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        q0 += kBatch * kWaves;
-        if (q0 < steps) fetch(q0);
+      } else {
+        wait();
       }
       if (full * kStep < a.F)
         for (int u = wave; u < used; u += kWaves) {
+          const int left = a.F - full * kStep - quarter * 16;
           W we;
-          we.load_end(row_of(expert[u]), full * kStep + quarter * 16, a.F);
-          add(we, u, full, true);
+          Share<T, false> he;
+          const Row r = row_of(u);
+          he.load_end((const char*)(r.h + full * kStep), 0, r.h ? left : 0);
+          we.load_end(rows_of(u) + full * kStep * W::kBytes, off, left);
+          add(we, he.v, r, u, full);
         }
 #pragma unroll
       for (int j = 0; j < 4; ++j) part[wave][0][quarter * 4 + j][column] = sum[j];
@@ -407,9 +468,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(4, 4))) voi
         for (int i = 0; i < kWaves; ++i) v += part[i][0][c][t];
         ((T*)a.y)[(int64_t)t * a.D + n0 + c] = from_f32<T>(v);
       }
-      __syncthreads();
-    }
-    tile = __builtin_amdgcn_readfirstlane(ticket);
+      tile = __builtin_amdgcn_readfirstlane(ticket);
   }
 }
 
