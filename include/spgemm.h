@@ -566,7 +566,7 @@ typedef struct spgemm_expert_step_desc {
  * experts fix; the hidden vector is rounded once to x's type (in fp16 it has to be
  * below 65504), y once.
  * Errors: INVALID_ARG (as spgemm_route; more than 16 tokens; types, strides, null
- * arrays, a workspace too small), INDEX_OVERFLOW (a width above 2^22), HIP. */
+ * arrays, a workspace too small), INDEX_OVERFLOW (a width above 2^20), HIP. */
 spgemm_status spgemm_expert_step_workspace(const spgemm_expert_step_desc *desc,
                                             int64_t *bytes);
 spgemm_status spgemm_expert_step(

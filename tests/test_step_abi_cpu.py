@@ -25,7 +25,7 @@ def test_descriptions():
                 dict(router=4), dict(route=RouteOptions(0, 3, 0, 0, 1.0)), dict(route=RouteOptions(0, 4, 5, 0, 1.0)),
                 dict(k=5, route=RouteOptions(0, 4, 1, 0, 1.0))):
         assert size(**bad) == -1, bad
-    assert size(D=(1 << 22) + 1, x_ld=1 << 23) == -3 and size(F=(1 << 22) + 1) == -3 and size(x_ld=1 << 30) == -3
+    assert size(D=(1 << 20) + 1, x_ld=1 << 23) == -3 and size(F=(1 << 20) + 1) == -3 and size(x_ld=1 << 30) == -3
     assert L.spgemm_expert_step_workspace(None, ctypes.byref(need)) == -1
     assert L.spgemm_expert_step_workspace(desc(), None) == -1
 
