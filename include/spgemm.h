@@ -545,7 +545,8 @@ spgemm_status spgemm_experts_backward(
 /* A whole expert layer for up to 16 tokens, as a decode step has them: logits,
  * routing and the experts' products in two launches. */
 typedef struct spgemm_expert_step_desc {
-  int64_t tokens, experts, width, hidden; /* T, E, D, F; T in [0, 16]          */
+  int64_t tokens, experts, width, hidden; /* T, E, D, F; T in [0, 16]; D and F
+                                             at least 16                       */
   int64_t x_ld;              /* row stride of x in elements, at least D        */
   int32_t k;
   spgemm_dtype dtype;        /* of x and y: SPGEMM_BF16 or SPGEMM_F16          */
@@ -565,7 +566,7 @@ typedef struct spgemm_expert_step_desc {
  * columns.  Products and sums in fp32, in an order that the sizes and the picked
  * experts fix; the hidden vector is rounded once to x's type (in fp16 it has to be
  * below 65504), y once.
- * Errors: INVALID_ARG (as spgemm_route; more than 16 tokens; types, strides, null
+ * Errors: INVALID_ARG (as spgemm_route; more than 16 tokens; a width below 16; types, strides, null
  * arrays, a workspace too small), INDEX_OVERFLOW (a width above 2^20), HIP. */
 spgemm_status spgemm_expert_step_workspace(const spgemm_expert_step_desc *desc,
                                             int64_t *bytes);

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kTokens = 16;  // columns of a tile
 constexpr int kNT = 512, kWaves = kNT / kWave;
+constexpr int kPitch = 20;   // of 16 floats in LDS
 constexpr int kStep = 64;    // K of one step: 16 for each quarter of a wave
 constexpr int kBlock = 128;  // rows and columns that share a scale
 
@@ -107,11 +108,12 @@ struct Share {
   static constexpr int kBytes = 2;
   s16x8 v[2];
   __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 32); }
-  // The n values that the row still has; zeros beyond.
-  __device__ void load_end(const char* base, uint32_t off, int n) {
-    const short* p = (const short*)(base + off);
+  // Without the first `drop` of them.
+  __device__ void keep_end(int drop) {
+    uint32_t* d = (uint32_t*)v;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = j < n ? p[j] : (short)0;
+    for (int i = 0; i < 8; ++i)
+      d[i] &= drop <= 2 * i ? ~0u : drop == 2 * i + 1 ? 0xffff0000u : 0u;
   }
   __device__ s16x8 half(int h) const { return v[h]; }
 };
@@ -121,15 +123,10 @@ struct Share<T, true> {
   static constexpr int kBytes = 1;
   uint32_t v[4];
   __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 16); }
-  __device__ void load_end(const char* base, uint32_t off, int n) {
-    const uint8_t* p = (const uint8_t*)(base + off);
+  __device__ void keep_end(int drop) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (4 * i + j < n) v[i] |= (uint32_t)p[4 * i + j] << (8 * j);
-    }
+    for (int i = 0; i < 4; ++i)
+      v[i] &= drop <= 4 * i ? ~0u : drop >= 4 * i + 4 ? 0u : ~0u << (8 * (drop - 4 * i));
   }
   __device__ s16x8 half(int h) const {
     uint32_t r[4];
@@ -150,6 +147,16 @@ struct Share<T, true> {
     return __builtin_bit_cast(s16x8, r);
   }
 };
+
+// The last step of K, where K is no multiple of 64: a lane whose 16 values reach
+// past the end takes the last 16 there are and drops those that other lanes have.
+struct End {
+  int k, drop;
+};
+__device__ __forceinline__ End end_of(int K, int quarter) {
+  const int k = K / kStep * kStep + quarter * 16, at = min(k, K - 16);
+  return {at, min(k - at, 16)};
+}
 
 struct StepArgs {
   RouteRow row;
@@ -221,7 +228,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint32_t* picked = packed + kNT / L * 2 * k;        // a bit for each of 1024 experts
   uint16_t* expert = (uint16_t*)(picked + 32);        // picked experts, rising
   int16_t* slot = (int16_t*)(expert + (a.most + 1) / 2 * 2);  // of expert u's entry of token t, or -1
-  __shared__ float part[kWaves][4][16][kTokens + 1];
+  __shared__ float part[kWaves][4][16][kPitch];  // [][gate or up, rows][column][row]
+  __shared__ float joined[2][kTokens][33];
   __shared__ uint32_t ticket[2];
   const int tid = threadIdx.x, l = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -313,12 +321,12 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     auto load = [&](const Place& p, int s) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int64_t at = min(s + i * kWaves, full - 1);
+        const int at = min(s + i * kWaves, full - 1);
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[i][o][j].load(p.rows[o] + at * (kStep * W::kBytes), p.off[j]);
+          for (int o = 0; o < 2; ++o)
+            w[i][o][j].load(p.rows[o], p.off[j] + (uint32_t)at * (kStep * W::kBytes));
         __builtin_memcpy(xf[i], x + at * kStep, 32);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -326,6 +334,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     Place p = place_of(tile);
     if (full) load(p, wave);
     // A tile's first loads are on their way while the one before it is joined.
+#pragma unroll 1
     while (true) {
       uint32_t later = 0;
       if (taker) later = take_ticket(a.counters);
@@ -343,7 +352,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       for (int o = 0; o < 2; ++o)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[o][j] = f32x4{0, 0, 0, 0};
-      for (int s = wave; s < full;) {
+      int s = wave;
+#pragma unroll 1
+      while (s < full) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int at = s + i * kWaves;
@@ -356,65 +367,77 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           }
         }
         s += kBatch * kWaves;
-        if (s < full) load(p, s);
+        if (s >= full) break;
+        load(p, s);
       }
       if (full * kStep < a.D && wave == full % kWaves) {
-        const int left = a.D - full * kStep - quarter * 16;
+        const End end = end_of(a.D, quarter);
         Share<T, false> xe;
-        xe.load_end((const char*)(x + full * kStep), 0, left);
+        xe.load((const char*)(x - quarter * 16 + end.k), 0);
+        xe.keep_end(end.drop);
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             W we;
-            we.load_end(p.rows[o] + full * kStep * W::kBytes, p.off[j], left);
+            we.load(p.rows[o], p.off[j] + (uint32_t)((end.k - quarter * 16) * W::kBytes));
+            we.keep_end(end.drop);
             multiply<T, k8>(we, xe.v, sc[o][j], full * kStep / kBlock, acc[o][j]);
           }
       }
-      const bool more = next < in_tiles;
-      const int u = p.u, f0 = p.f0;
-      if (more) {
-        p = place_of(next);
-        if (full) load(p, wave);
-      }
+      // Written out for either way, so that the loads' registers are free in the last.
+      auto join = [&](int u, int f0) {
 #pragma unroll
-      for (int o = 0; o < 2; ++o)
+        for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+          for (int j = 0; j < 2; ++j) *(f32x4*)&part[wave][2 * o + j][column][quarter * 4] = acc[o][j];
+        if (taker) ticket[0] = later;
+        __syncthreads();
+        // Sums of gate and up: token, column.
+        {
+          const int t = tid / 32, c = tid % 32;
+          float v[2] = {0.0f, 0.0f};
+#pragma unroll 4
+          for (int i = 0; i < kWaves; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) part[wave][2 * o + i][quarter * 4 + j][column] = acc[o][i][j];
-      if (taker) ticket[0] = later;
-      __syncthreads();
-      // A pair of columns to a thread.
-      const int t = tid / 16, c = tid % 16 * 2;
-      const int i = t < a.T ? slot[u * kTokens + t] : -1;
-      if (i >= 0 && f0 + c < a.h_ld) {
-        uint32_t pair = 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float gs = 0.0f, us = 0.0f;
-#pragma unroll
-          for (int v = 0; v < kWaves; ++v) {
-            gs += part[v][c / 16][c % 16 + q][t];
-            us += part[v][2 + c / 16][c % 16 + q][t];
-          }
-          const float hv = f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
-          pair |= (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(hv)) << (16 * q);
+            for (int o = 0; o < 2; ++o) v[o] += part[i][2 * o + c / 16][t][c % 16];
+          joined[0][t][c] = v[0];
+          joined[1][t][c] = v[1];
         }
-        __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + f0 + c), pair,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        // A pair of columns to a thread.
+        const int t = tid / 16, c = tid % 16 * 2;
+        const int i = t < a.T ? slot[u * kTokens + t] : -1;
+        if (i >= 0 && f0 + c < a.h_ld) {
+          uint32_t pair = 0;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float gs = joined[0][t][c + q], us = joined[1][t][c + q];
+            const float hv = f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
+            pair |= (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(hv)) << (16 * q);
+          }
+          __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + f0 + c), pair,
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        // The stores are written through and done before the tile is counted.  A release
+        // at this scope would also write the L2's other lines back.
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t after = __builtin_amdgcn_readfirstlane(ticket[0]);
+        __syncthreads();
+        if (tid == 0)
+          __hip_atomic_fetch_add(&a.counters->done[tile % kDone].n, 1u, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+        tile = next;
+        next = after;
+      };
+      const int u = p.u, f0 = p.f0;
+      if (next >= in_tiles) {
+        join(u, f0);
+        break;
       }
-      // The stores are written through and done before the tile is counted.  A release
-      // at this scope would also write the L2's other lines back.
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      const uint32_t after = __builtin_amdgcn_readfirstlane(ticket[0]);
-      __syncthreads();
-      if (tid == 0)
-        __hip_atomic_fetch_add(&a.counters->done[tile % kDone].n, 1u, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-      tile = next;
-      next = after;
-      if (!more) break;
+      p = place_of(next);
+      if (full) load(p, wave);
+      join(u, f0);
     }
   }
 
@@ -428,82 +451,71 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   if (tile >= all) return;
   const int full = a.F / kStep, steps = used * full;
   const int sub = column % out_width, my_part = column / out_width;
-  const float per = full ? 1.0f / (float)full : 0.0f;
+  struct Place { int u, s; };
+  // Of kWaves * cut steps.
+  const int ahead_u = full ? kWaves * cut / full : 0, ahead_s = kWaves * cut - ahead_u * full;
+  auto advance = [&](Place& p) {
+    p.u += ahead_u;
+    p.s += ahead_s;
+    if (p.s >= full) p.s -= full, ++p.u;
+  };
+  const int first = wave * cut + my_part;
+  const Place start{full ? first / full : 0, full ? first % full : 0};
+  // Steps of this wave, the last of which may lack some parts.
+  const int count = (steps - wave * cut + kWaves * cut - 1) / (kWaves * cut);
   bool ready = false;  // all of h is there
+#pragma unroll 1
   while (tile < all) {
-    const int n0 = (int)(tile - in_tiles) * out_width, row = min(n0 + sub, a.D - 1);
+    const int n0 = (int)(tile - in_tiles) * out_width;
+    const char* rows =
+        (const char*)a.w_out + ((int64_t)min(n0 + sub, a.D - 1) * a.F + quarter * 16) * W::kBytes;
+    const int64_t expert_bytes = (int64_t)a.D * a.F * W::kBytes;
     uint32_t later = 0;
     if (taker) later = take_ticket(a.counters);
-    struct Place { int u, s; };
-    auto place_of = [&](int q) {
-      Place p;
-      p.u = (int)((float)q * per);
-      p.s = q - p.u * full;
-      if (p.s < 0) --p.u, p.s += full;
-      if (p.s >= full) ++p.u, p.s -= full;
-      return p;
+    constexpr int kRing = 6;  // steps on their way
+    W w[kRing];
+    s16x8 h[kRing][2];
+    float value[kRing];  // of the token for the step's expert
+    bool there[kRing];   // whether it picked it
+    Place pw = start, ph = start;
+    auto load_w = [&](W& w) {
+      w.load(rows + expert[min(pw.u, used - 1)] * expert_bytes + (int64_t)pw.s * (kStep * W::kBytes), 0);
+      advance(pw);
     };
-    auto weights_at = [&](const Place& p) {
-      return (const char*)a.w_out +
-             (((int64_t)expert[p.u] * a.D + row) * a.F + p.s * kStep + quarter * 16) * W::kBytes;
-    };
-    constexpr int kBatch = 6, kHalf = 3;
-    W w[2][kBatch];
-    auto fetch = [&](int q, W (&w)[kBatch]) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        w[i].load(weights_at(place_of(min(q + i * kWaves * cut, steps - 1))), 0);
-      __builtin_amdgcn_sched_barrier(0);
-    };
-    f32x4 sum = {0, 0, 0, 0};
-    // The token's row of h for expert u, and its value; null where it did not pick it.
-    struct Row { const uint16_t* h; float value; };
-    auto row_of = [&](int u) {
+    auto load_h = [&](s16x8 (&h)[2], float& value, bool& there, auto end) {
+      const int u = min(ph.u, used - 1);
       const int i = sub < a.T ? slot[u * kTokens + sub] : -1;
+      there = i >= 0 && ph.u < used;
       const int entry = i < 0 ? 0 : sub * k + i;
-      return Row{i < 0 ? nullptr : a.h + (int64_t)entry * a.h_ld + quarter * 16, vals[entry]};
+      value = vals[entry];
+      // A lane's scale is that of its column's part, the only one whose products count.
+      if constexpr (k8)
+        value *= a.out_scale[((int64_t)expert[u] * ((a.D + kBlock - 1) / kBlock) + n0 / kBlock) *
+                                 ((a.F + kBlock - 1) / kBlock) + ph.s * kStep / kBlock];
+      // Rows that are not there are read as those of entry 0, and not used.
+      const uint16_t* from = a.h + (int64_t)entry * a.h_ld + ph.s * kStep + quarter * 16;
+      __builtin_memcpy(h, from + (decltype(end)::value ? end_of(a.F, quarter).k - full * kStep - quarter * 16 : 0), 32);
+      if constexpr (!decltype(end)::value) advance(ph);
     };
-    // A lane's scale is that of its column's part, the only one whose products count.
-    auto add = [&](const W& w, const s16x8 (&h)[2], const Row& r, const Place& p) {
-      Scales sc{};
-      float one = 1.0f;
-      if constexpr (k8) {
-        const int cols = (a.F + kBlock - 1) / kBlock, rows = (a.D + kBlock - 1) / kBlock;
-        one = a.out_scale[((int64_t)expert[p.u] * rows + n0 / kBlock) * cols + p.s * kStep / kBlock];
-      }
+    constexpr std::false_type kWhole{};
+    constexpr std::true_type kEnd{};
+    f32x4 sum = {0, 0, 0, 0};
+    auto add = [&](const W& w, const s16x8 (&h)[2], float value, bool there) {
       f32x4 acc = {0, 0, 0, 0};
       acc = mfma16(T{}, w.half(0), h[0], acc);
       acc = mfma16(T{}, w.half(1), h[1], acc);
       // What a token did not pick adds nothing, whatever its weights hold.
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += r.h ? r.value * one * acc[j] : 0.0f;
+      for (int j = 0; j < 4; ++j) sum[j] += there ? value * acc[j] : 0.0f;
     };
-    auto use = [&](int q0, const W (&w)[kBatch]) {
 #pragma unroll
-      for (int i0 = 0; i0 < kBatch; i0 += kHalf) {
-        Place p[kHalf];
-        Row r[kHalf];
-        s16x8 h[kHalf][2];
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) {
-          const int q = q0 + (i0 + i) * kWaves * cut;
-          p[i] = place_of(min(q, steps - 1));
-          r[i] = row_of(p[i].u);
-          if (q >= steps) r[i].h = nullptr;
-          h[i][0] = h[i][1] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-          if (r[i].h) __builtin_memcpy(h[i], r[i].h + p[i].s * kStep, 32);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < kHalf; ++i) add(w[i0 + i], h[i], r[i], p[i]);
-      }
-    };
-    const int stride = kBatch * kWaves * cut;
-    int q = wave * cut + my_part;
-    if (steps) fetch(q, w[0]);
-    if (wave * cut + stride < steps) fetch(q + stride, w[1]);
+    for (int i = 0; i < kRing; ++i)
+      if (i < count) load_w(w[i]);
+    __builtin_amdgcn_sched_barrier(0);
     if (!ready) {
-      if (wave == 0)
+      // One wave acquires for all: each invalidation of the caches holds the others up,
+      // 15 us where all eight waves of 256 work groups made one.
+      if (wave == 0) {
         while (true) {
           uint32_t c = 0;
           if (l < kDone)
@@ -512,41 +524,55 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (wave_sum(c) >= in_tiles) break;
           __builtin_amdgcn_s_sleep(4);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      }
       __syncthreads();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       ready = true;
     }
-    // The first part's place decides, for the whole wave.
-    for (int q1 = wave * cut; q1 < steps; q1 += 2 * stride, q += 2 * stride) {
-      use(q, w[0]);
-      if (q1 + 2 * stride < steps) fetch(q + 2 * stride, w[0]);
-      if (q1 + stride < steps) {
-        use(q + stride, w[1]);
-        if (q1 + 3 * stride < steps) fetch(q + 3 * stride, w[1]);
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      if (i < count) load_h(h[i], value[i], there[i], kWhole);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+    for (int j = 0; j < count; j += kRing) {
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) {
+        if (j + i >= count) break;
+        add(w[i], h[i], value[i], there[i]);
+        if (j + i + kRing < count) {
+          load_w(w[i]);
+          load_h(h[i], value[i], there[i], kWhole);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (full * kStep < a.F)
+#pragma unroll 1
       for (int u0 = wave * cut; u0 < used; u0 += kWaves * cut) {
-        const int u = min(u0 + my_part, used - 1), left = a.F - full * kStep - quarter * 16;
+        const End end = end_of(a.F, quarter);
         W we;
         Share<T, false> he;
-        Row r = row_of(u);
-        if (u0 + my_part >= used) r.h = nullptr;
-        he.load_end((const char*)(r.h + full * kStep), 0, r.h ? left : 0);
-        we.load_end(weights_at(Place{u, full}), 0, left);
-        add(we, he.v, r, Place{u, full});
+        float v;
+        bool is;
+        ph = Place{u0 + my_part, full};
+        load_h(he.v, v, is, kEnd);
+        he.keep_end(end.drop);
+        we.load(rows + expert[min(u0 + my_part, used - 1)] * expert_bytes +
+                    (int64_t)(end.k - quarter * 16) * W::kBytes, 0);
+        we.keep_end(end.drop);
+        add(we, he.v, v, is);
       }
     __syncthreads();  // `part` and `ticket` of the tile before have been read
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[wave][0][quarter * 4 + j][column] = sum[j];
+    *(f32x4*)&part[wave][0][column][quarter * 4] = sum;
     if (taker) ticket[0] = later;
     __syncthreads();
     const int t = tid / out_width, c = tid % out_width;
     if (t < a.T && n0 + c < a.D) {
       float v = 0.0f;
+#pragma unroll 1
       for (int i = 0; i < cut; ++i)
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += part[w][0][i * out_width + c][i * out_width + t];
+#pragma unroll 4
+        for (int w = 0; w < kWaves; ++w) v += part[w][0][i * out_width + t][i * out_width + c];
       ((T*)a.y)[(int64_t)t * a.D + n0 + c] = from_f32<T>(v);
     }
     tile = next;
@@ -588,8 +614,8 @@ spgemm_status check_desc(const spgemm_expert_step_desc* d) {
     return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: the router must be fp32 or of x's type");
   if (d->tokens < 0 || d->tokens > kTokens)
     return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: tokens outside [0, 16]");
-  if (d->width < 1 || d->hidden < 1 || d->x_ld < d->width)
-    return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: empty width, or a row stride below it");
+  if (d->width < 16 || d->hidden < 16 || d->x_ld < d->width)
+    return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: a width below 16, or a row stride below the width");
   if (d->width > 1 << 20 || d->hidden > 1 << 20 || d->x_ld >= 1 << 30)
     return refuse(SPGEMM_ERR_INDEX_OVERFLOW, "expert_step: a width above 2^20, or a stride of 2^30 or more");
   return check_route_options(d->experts, d->k, &d->route);

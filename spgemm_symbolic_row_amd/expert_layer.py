@@ -313,7 +313,7 @@ def expert_step(x, w_router, w_in, w_out, k, in_scale=None, out_scale=None, scor
     """(y, Routing) of a whole expert layer for a few tokens, as a decode step
     has them: route(x w_router^T, k, ...) and experts(...) in two launches.
 
-    x: T x D (T up to 16, rows contiguous; bfloat16 or float16), w_router: E x D (x's type or
+    x: T x D (T up to 16, D and F at least 16, rows contiguous; bfloat16 or float16), w_router: E x D (x's type or
     float32), w_in: E x 2F x D and w_out: E x D x F in x's type; or both in
     float8_e4m3fn, with float32 scales for every 128 x 128 block of an expert:
     in_scale E x ceil(2F / 128) x ceil(D / 128), out_scale E x ceil(D / 128) x

@@ -65,22 +65,24 @@ def check(t, k, how=None, dev=None):
 
 SIZES = [
     # T, E, k, D, F
-    (1, 1, 1, 1, 1),
+    (1, 1, 1, 16, 16),
+    (2, 3, 1, 17, 31),
+    (3, 4, 2, 47, 79),
     (1, 4, 2, 64, 64),
     (1, 64, 6, 256, 128),
-    (2, 8, 8, 63, 15),
+    (2, 8, 8, 63, 16),
     (3, 5, 2, 65, 17),
     (4, 24, 3, 100, 129),
     (5, 16, 2, 1001, 345),
     (7, 12, 4, 520, 63),
     (8, 3, 1, 130, 700),
-    (9, 40, 5, 8, 16),
+    (9, 40, 5, 18, 16),
     (13, 60, 4, 264, 200),
     (16, 128, 8, 512, 96),
     (16, 2, 2, 2056, 72),
     (16, 300, 10, 72, 33),
     (6, 1024, 3, 40, 24),
-    (16, 1024, 64, 16, 8),
+    (16, 1024, 64, 16, 18),
     (1, 6, 2, 4104, 1032),
     (11, 16, 16, 128, 256),
 ]

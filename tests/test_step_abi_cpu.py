@@ -20,7 +20,7 @@ def test_descriptions():
     assert size() == 0 and need.value >= 4 * 16 * 4 + 4 * 2 * 32 * 2
     assert size(T=0) == 0 and size(T=16) == 0
     assert size(weight=4) == 0 and size(router=0) == 0 and size(dtype=3, weight=3, router=3) == 0
-    for bad in (dict(T=-1), dict(T=17), dict(E=0), dict(E=1025), dict(D=0), dict(F=0), dict(x_ld=63), dict(k=0),
+    for bad in (dict(T=-1), dict(T=17), dict(E=0), dict(E=1025), dict(D=15), dict(F=15), dict(D=0), dict(F=0), dict(x_ld=63), dict(k=0),
                 dict(k=17), dict(E=128, k=65), dict(dtype=0), dict(dtype=4), dict(weight=3), dict(weight=0), dict(router=3),
                 dict(router=4), dict(route=RouteOptions(0, 3, 0, 0, 1.0)), dict(route=RouteOptions(0, 4, 5, 0, 1.0)),
                 dict(k=5, route=RouteOptions(0, 4, 1, 0, 1.0))):
