@@ -8,13 +8,13 @@
 // The logits: a work group to an expert; sums in 64 bits, so that the choice among
 // close experts does not depend on their order.
 //
-// The rest is one launch.  Every work group routes all tokens itself (a wave to a
-// token, up to two of them each), which costs less than waiting for another to do
-// it.  Then work groups take numbers from a counter: first the tiles of W_in, whose
-// results go to memory, then those of W_out, which wait until all the former are
-// there, their first weights already loaded.  A work group waits only for numbers
-// below its own, whose holders run and never wait for higher ones: however few work
-// groups are on the chip at a time, every wait ends.
+// The rest is one launch.  Every work group routes all tokens itself, which costs
+// less than waiting for another to do it.  Then work groups take tiles of W_in by
+// numbers from a counter; the results go to memory.  A work group that finds no
+// number left goes on to its tiles of W_out, loads their first weights and waits
+// until all results are there.  It waits only when every tile of W_in has been taken
+// by a work group that runs and that waits for nothing: however few work groups
+// are on the chip at a time, every wait ends.
 #include <algorithm>
 #include <type_traits>
 
@@ -236,11 +236,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   // Takes the numbers: a thread of a wave that has no row to route unless all have.
   const bool taker = tid == kNT - kWave;
 
+  // The second number is taken when every work group has surely taken its first.
   uint32_t mine[2] = {0, 0};
-  if (taker) {
-    mine[0] = take_ticket(a.counters);
-    mine[1] = take_ticket(a.counters);
-  }
+  if (taker) mine[0] = take_ticket(a.counters);
   if (tid < 32) picked[tid] = 0;
   for (int i = tid; i < a.most * kTokens; i += kNT) slot[i] = -1;
   for (int t0 = 0; t0 < a.T; t0 += kNT / L) {
@@ -263,8 +261,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if (a.sigmoid) route_row<L, V, true>(a.row, z, packed + tid / L * 2 * k, store);
     else route_row<L, V, false>(a.row, z, packed + tid / L * 2 * k, store);
   }
-  if (taker) ticket[0] = mine[0], ticket[1] = mine[1];
+  if (taker) ticket[0] = mine[0];
   __syncthreads();
+  if (taker) mine[1] = take_ticket(a.counters);
   for (int i = tid; i < n; i += kNT)
     if (cols[i] >= 0) atomicOr(&picked[cols[i] / 32], 1u << (cols[i] % 32));
   __syncthreads();
@@ -286,11 +285,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int cut = a.cut, out_width = 16 / cut;
   const int in_cols = (a.F + 31) / 32;
   const uint32_t in_tiles = (uint32_t)used * in_cols;
-  const uint32_t all = in_tiles + (a.D + out_width - 1) / out_width;
   const int quarter = l >> 4, column = l & 15;
   uint32_t tile = __builtin_amdgcn_readfirstlane(ticket[0]);
-  uint32_t next = __builtin_amdgcn_readfirstlane(ticket[1]);
-
   // ---- tiles of W_in: h of expert u's tokens, 32 columns ----
   if (tile < in_tiles) {
     const int64_t row_bytes = (int64_t)a.D * W::kBytes;
@@ -333,6 +329,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     Place p = place_of(tile);
     if (full) load(p, wave);
+    if (taker) ticket[1] = mine[1];
+    __syncthreads();
+    uint32_t next = __builtin_amdgcn_readfirstlane(ticket[1]);
     // A tile's first loads are on their way while the one before it is joined.
 #pragma unroll 1
     while (true) {
@@ -442,15 +441,17 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 
   // ---- tiles of W_out: 16 / cut columns of y ----
-  // With T tokens only T of the 16 columns of a product are of use.  Where 2 T <= 16,
-  // row r and column c of a tile stand for part r / width and c / width of K, so
-  // that its 16 rows are `cut` parts of `width` rows of W_out and there are `cut`
-  // times as many tiles; only the products of equal parts are taken.  The steps of
-  // all picked experts are one row, q being step q % full of expert q / full, and
+  // A tile's 16 rows are `cut` parts of K of `width` columns of y, so that there are
+  // tiles for every compute unit.  The 16 columns of a product are parts and tokens,
+  // and only the products of equal parts are taken; where parts and tokens do not
+  // fit 16 columns, a second product has the other half of the parts.  The steps
+  // of all picked experts are one row, q being step q % full of expert q / full, and
   // part i of a wave's step takes the i-th of `cut` neighbours.
-  if (tile >= all) return;
+  const int out_tiles = (a.D + out_width - 1) / out_width;
   const int full = a.F / kStep, steps = used * full;
-  const int sub = column % out_width, my_part = column / out_width;
+  const int passes = cut * a.T > 16 ? 2 : 1, room = 16 * passes / cut;  // columns for tokens
+  const int sub = column % out_width;  // as a row of the weights
+  const int token = column % room;     // as a column of h
   struct Place { int u, s; };
   // Of kWaves * cut steps.
   const int ahead_u = full ? kWaves * cut / full : 0, ahead_s = kWaves * cut - ahead_u * full;
@@ -459,54 +460,63 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     p.s += ahead_s;
     if (p.s >= full) p.s -= full, ++p.u;
   };
-  const int first = wave * cut + my_part;
-  const Place start{full ? first / full : 0, full ? first % full : 0};
+  auto start_of = [&](int part) {
+    const int q = wave * cut + part;
+    return Place{full ? q / full : 0, full ? q % full : 0};
+  };
+  const int w_part = column / out_width, h_part = column / room;
   // Steps of this wave, the last of which may lack some parts.
   const int count = (steps - wave * cut + kWaves * cut - 1) / (kWaves * cut);
   bool ready = false;  // all of h is there
 #pragma unroll 1
-  while (tile < all) {
-    const int n0 = (int)(tile - in_tiles) * out_width;
+  for (int out = blockIdx.x; out < out_tiles; out += gridDim.x) {
+    const int n0 = out * out_width;
     const char* rows =
         (const char*)a.w_out + ((int64_t)min(n0 + sub, a.D - 1) * a.F + quarter * 16) * W::kBytes;
     const int64_t expert_bytes = (int64_t)a.D * a.F * W::kBytes;
-    uint32_t later = 0;
-    if (taker) later = take_ticket(a.counters);
     constexpr int kRing = 6;  // steps on their way
     W w[kRing];
-    s16x8 h[kRing][2];
-    float value[kRing];  // of the token for the step's expert
-    bool there[kRing];   // whether it picked it
-    Place pw = start, ph = start;
+    struct Hidden {
+      s16x8 h[2];
+      float value;  // of the token for the step's expert
+      bool there;   // whether it picked it
+    };
+    Hidden h[2][kRing];
+    Place pw = start_of(w_part), ph[2] = {start_of(h_part), start_of(h_part + cut / 2)};
     auto load_w = [&](W& w) {
       w.load(rows + expert[min(pw.u, used - 1)] * expert_bytes + (int64_t)pw.s * (kStep * W::kBytes), 0);
       advance(pw);
     };
-    auto load_h = [&](s16x8 (&h)[2], float& value, bool& there, auto end) {
-      const int u = min(ph.u, used - 1);
-      const int i = sub < a.T ? slot[u * kTokens + sub] : -1;
-      there = i >= 0 && ph.u < used;
-      const int entry = i < 0 ? 0 : sub * k + i;
-      value = vals[entry];
-      // A lane's scale is that of its column's part, the only one whose products count.
+    // From step p, or from `end` values into it.
+    auto load_h = [&](Hidden& h, const Place& p, int end) {
+      const int u = min(p.u, used - 1);
+      const int i = token < a.T ? slot[u * kTokens + token] : -1;
+      h.there = i >= 0 && p.u < used;
+      const int entry = i < 0 ? 0 : token * k + i;
+      h.value = vals[entry];
+      // The scale of the column's part, the only one whose products count.
       if constexpr (k8)
-        value *= a.out_scale[((int64_t)expert[u] * ((a.D + kBlock - 1) / kBlock) + n0 / kBlock) *
-                                 ((a.F + kBlock - 1) / kBlock) + ph.s * kStep / kBlock];
+        h.value *= a.out_scale[((int64_t)expert[u] * ((a.D + kBlock - 1) / kBlock) + n0 / kBlock) *
+                                   ((a.F + kBlock - 1) / kBlock) + p.s * kStep / kBlock];
       // Rows that are not there are read as those of entry 0, and not used.
-      const uint16_t* from = a.h + (int64_t)entry * a.h_ld + ph.s * kStep + quarter * 16;
-      __builtin_memcpy(h, from + (decltype(end)::value ? end_of(a.F, quarter).k - full * kStep - quarter * 16 : 0), 32);
-      if constexpr (!decltype(end)::value) advance(ph);
+      __builtin_memcpy(h.h, a.h + (int64_t)entry * a.h_ld + p.s * kStep + quarter * 16 + end, 32);
     };
-    constexpr std::false_type kWhole{};
-    constexpr std::true_type kEnd{};
-    f32x4 sum = {0, 0, 0, 0};
-    auto add = [&](const W& w, const s16x8 (&h)[2], float value, bool there) {
+    auto load_both = [&](int i) {
+      load_h(h[0][i], ph[0], 0);
+      advance(ph[0]);
+      if (passes == 2) {
+        load_h(h[1][i], ph[1], 0);
+        advance(ph[1]);
+      }
+    };
+    f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    auto add = [&](const W& w, const Hidden& h, f32x4& sum) {
       f32x4 acc = {0, 0, 0, 0};
-      acc = mfma16(T{}, w.half(0), h[0], acc);
-      acc = mfma16(T{}, w.half(1), h[1], acc);
+      acc = mfma16(T{}, w.half(0), h.h[0], acc);
+      acc = mfma16(T{}, w.half(1), h.h[1], acc);
       // What a token did not pick adds nothing, whatever its weights hold.
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += there ? value * acc[j] : 0.0f;
+      for (int j = 0; j < 4; ++j) sum[j] += h.there ? h.value * acc[j] : 0.0f;
     };
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
@@ -531,17 +541,18 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
-      if (i < count) load_h(h[i], value[i], there[i], kWhole);
+      if (i < count) load_both(i);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll 1
     for (int j = 0; j < count; j += kRing) {
 #pragma unroll
       for (int i = 0; i < kRing; ++i) {
         if (j + i >= count) break;
-        add(w[i], h[i], value[i], there[i]);
+        add(w[i], h[0][i], sum[0]);
+        if (passes == 2) add(w[i], h[1][i], sum[1]);
         if (j + i + kRing < count) {
           load_w(w[i]);
-          load_h(h[i], value[i], there[i], kWhole);
+          load_both(i);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -550,33 +561,40 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll 1
       for (int u0 = wave * cut; u0 < used; u0 += kWaves * cut) {
         const End end = end_of(a.F, quarter);
+        const int shift = end.k - full * kStep - quarter * 16;
         W we;
-        Share<T, false> he;
-        float v;
-        bool is;
-        ph = Place{u0 + my_part, full};
-        load_h(he.v, v, is, kEnd);
-        he.keep_end(end.drop);
-        we.load(rows + expert[min(u0 + my_part, used - 1)] * expert_bytes +
+        we.load(rows + expert[min(u0 + w_part, used - 1)] * expert_bytes +
                     (int64_t)(end.k - quarter * 16) * W::kBytes, 0);
         we.keep_end(end.drop);
-        add(we, he.v, v, is);
+#pragma unroll 1
+        for (int pass = 0; pass < passes; ++pass) {
+          Hidden he;
+          load_h(he, Place{u0 + h_part + pass * (cut / 2), full}, shift);
+          Share<T, false> kept;
+          kept.v[0] = he.h[0], kept.v[1] = he.h[1];
+          kept.keep_end(end.drop);
+          he.h[0] = kept.v[0], he.h[1] = kept.v[1];
+          f32x4 one = {0, 0, 0, 0};
+          add(we, he, one);
+          if (pass) sum[1] += one;
+          else sum[0] += one;
+        }
       }
-    __syncthreads();  // `part` and `ticket` of the tile before have been read
-    *(f32x4*)&part[wave][0][column][quarter * 4] = sum;
-    if (taker) ticket[0] = later;
+    __syncthreads();  // `part` of the tile before has been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *(f32x4*)&part[wave][i][column][quarter * 4] = sum[i];
     __syncthreads();
     const int t = tid / out_width, c = tid % out_width;
     if (t < a.T && n0 + c < a.D) {
       float v = 0.0f;
+      const int per = cut / passes;  // parts of a product
 #pragma unroll 1
       for (int i = 0; i < cut; ++i)
 #pragma unroll 4
-        for (int w = 0; w < kWaves; ++w) v += part[w][0][i * out_width + t][i * out_width + c];
+        for (int w = 0; w < kWaves; ++w)
+          v += part[w][i / per][i % per * room + t][i * out_width + c];
       ((T*)a.y)[(int64_t)t * a.D + n0 + c] = from_f32<T>(v);
     }
-    tile = next;
-    next = __builtin_amdgcn_readfirstlane(ticket[0]);
   }
 }
 
@@ -593,9 +611,9 @@ struct Work {
 };
 Work take_work(Carver& c, const spgemm_expert_step_desc& d) {
   Work w{};
-  w.counters = c.take<Counters>(1);
   w.logits = c.take<float>(d.tokens * d.experts);
   w.h = c.take<uint16_t>(d.tokens * d.k * hidden_pitch(d.hidden));
+  w.counters = c.take<Counters>(1);
   return w;
 }
 
@@ -633,12 +651,13 @@ template <typename T, bool k8>
 void layer(const StepArgs& a, hipStream_t s) {
   const int n = a.T * a.row.k;
   const int64_t tiles =
-      (int64_t)a.most * ((a.F + 31) / 32) + (a.D + 16 / a.cut - 1) / (16 / a.cut);
+      std::max((int64_t)a.most * ((a.F + 31) / 32), ((int64_t)a.D + 16 / a.cut - 1) / (16 / a.cut));
   const dim3 grid((unsigned)std::min<int64_t>(tiles, kGroups));
   const int rows = a.row.E <= 256 ? kNT / 16 : kWaves;  // routed at a time
   const size_t lds = (2 * n + rows * 2 * a.row.k + 32) * 4 + (a.most + 1) / 2 * 4 +
                      (size_t)a.most * kTokens * 2;
   if (a.row.E <= 64) hipLaunchKernelGGL((k_step<T, k8, 16, 4>), grid, dim3(kNT), lds, s, a);
+  else if (a.row.E <= 128) hipLaunchKernelGGL((k_step<T, k8, 16, 8>), grid, dim3(kNT), lds, s, a);
   else if (a.row.E <= 256) hipLaunchKernelGGL((k_step<T, k8, 16, 16>), grid, dim3(kNT), lds, s, a);
   else hipLaunchKernelGGL((k_step<T, k8, 64, 16>), grid, dim3(kNT), lds, s, a);
 }
@@ -686,7 +705,7 @@ extern "C" spgemm_status spgemm_expert_step(
   z.D = (int)d.width;
   z.w32 = d.router_dtype == SPGEMM_F32;
   StepArgs a{};
-  a.row = route_row_of(d.experts, d.k, d.route, dBias, d.experts <= 64 ? 4 : 16);
+  a.row = route_row_of(d.experts, d.k, d.route, dBias, d.experts <= 64 ? 4 : d.experts <= 128 ? 8 : 16);
   a.sigmoid = d.route.sigmoid != 0;
   a.x = dX;
   a.x_ld = d.x_ld;
@@ -705,9 +724,11 @@ extern "C" spgemm_status spgemm_expert_step(
   a.D = z.D;
   a.F = (int)d.hidden;
   a.h_ld = (int)hidden_pitch(d.hidden);
-  // Parts as the tokens leave room for them, while there are fewer tiles than work groups.
+  // Parts as the tokens leave room for them in two products, while there are fewer
+  // tiles than work groups.
   a.cut = 1;
-  while (2 * a.cut * a.T <= kTokens && (d.width + 15) / 16 * 2 * a.cut <= kGroups) a.cut *= 2;
+  while (2 * a.cut * a.T <= 2 * kTokens && (d.width + 15) / 16 * 2 * a.cut <= kGroups) a.cut *= 2;
+  a.cut = std::min(a.cut, 16);
   a.most = (int)std::min<int64_t>(d.experts, d.tokens * d.k);
   (void)hipGetLastError();  // an error that earlier calls left is not this one's
   const hipStream_t s = (hipStream_t)stream;
