@@ -100,33 +100,63 @@ __global__ __launch_bounds__(256) void k_step_logits(LogitArgs a) {
 
 // ---- weights ----
 
-// A lane's share of one step of its row: 16 values from k = 64 s + 16 (l / 16), at
-// a uniform address plus the lane's offset.  16-bit weights are the operands as
-// they are; 8-bit ones are decoded when used, exactly, to x's type.
-template <typename T, bool k8>
-struct Share {
-  static constexpr int kBytes = 2;
-  s16x8 v[2];
-  __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 32); }
-  // Without the first `drop` of them.
-  __device__ void keep_end(int drop) {
-    uint32_t* d = (uint32_t*)v;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      d[i] &= drop <= 2 * i ? ~0u : drop == 2 * i + 1 ? 0xffff0000u : 0u;
+// A lane's share of one step of its row: 16 values.  In step s lane l has those from
+// k = 64 s + 16 (l / 16); one whose values reach past the end of K takes the last 16
+// there are and drops those that other lanes have.
+__device__ __forceinline__ int k_of(int s, int K) {
+  return min(s * kStep + (lane_id() >> 4) * 16, K - 16);
+}
+__device__ __forceinline__ int dropped(int s, int K) {
+  return min(s * kStep + (lane_id() >> 4) * 16 - k_of(s, K), 16);
+}
+
+// Loads at addresses that are no multiple of 4 bytes take four times as long as
+// others (1025 x 1025 bfloat16: 240 us, 1026 x 1026: 98 us), so unless `even` the words that hold
+// the values are loaded, all of which are at least in part the row's, and shifted
+// when they are used.  16-bit values are the operands as they are; 8-bit ones are
+// decoded when used, exactly, to x's type.
+template <int kWords>
+struct Words {
+  uint32_t v[kWords + 1];
+  __device__ void load(const char* p, bool even) {
+    if (even) {
+      __builtin_memcpy(v, p, kWords * 4);
+    } else {
+      const uint32_t off = (uint32_t)(uintptr_t)p & 3;
+      const char* q = p - off;
+      __builtin_memcpy(v, __builtin_assume_aligned(q, 4), kWords * 4);
+      v[kWords] = *(const uint32_t*)(q + (off ? kWords * 4 : kWords * 4 - 4));
+    }
   }
-  __device__ s16x8 half(int h) const { return v[h]; }
+  // Of a load at a multiple of 4 bytes plus off.
+  __device__ void shift(uint32_t off) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) v[i] = __builtin_amdgcn_alignbyte(v[i + 1], v[i], off);
+  }
+};
+
+template <typename T, bool k8>
+struct Share : Words<8> {
+  static constexpr int kBytes = 2;
+  // Without the first n values.
+  __device__ void drop(int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] &= n <= 2 * i ? ~0u : n == 2 * i + 1 ? 0xffff0000u : 0u;
+  }
+  __device__ s16x8 half(int h) const {
+    s16x8 r;
+    __builtin_memcpy(&r, v + 4 * h, 16);
+    return r;
+  }
 };
 
 template <typename T>
-struct Share<T, true> {
+struct Share<T, true> : Words<4> {
   static constexpr int kBytes = 1;
-  uint32_t v[4];
-  __device__ void load(const char* base, uint32_t off) { __builtin_memcpy(v, base + off, 16); }
-  __device__ void keep_end(int drop) {
+  __device__ void drop(int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] &= drop <= 4 * i ? ~0u : drop >= 4 * i + 4 ? 0u : ~0u << (8 * (drop - 4 * i));
+      v[i] &= n <= 4 * i ? ~0u : n >= 4 * i + 4 ? 0u : ~0u << (8 * (n - 4 * i));
   }
   __device__ s16x8 half(int h) const {
     uint32_t r[4];
@@ -148,16 +178,6 @@ struct Share<T, true> {
   }
 };
 
-// The last step of K, where K is no multiple of 64: a lane whose 16 values reach
-// past the end takes the last 16 there are and drops those that other lanes have.
-struct End {
-  int k, drop;
-};
-__device__ __forceinline__ End end_of(int K, int quarter) {
-  const int k = K / kStep * kStep + quarter * 16, at = min(k, K - 16);
-  return {at, min(k - at, 16)};
-}
-
 struct StepArgs {
   RouteRow row;
   const void* x;
@@ -177,40 +197,8 @@ struct StepArgs {
   int most;                // experts that the tokens can pick together
   int cut;                 // parts that a tile of W_out cuts K into
   bool sigmoid;
+  bool even_x, even_in, even_out;  // rows begin at multiples of 4 bytes
 };
-
-// The rows of a tile of 8-bit weights lie in one or two rows of blocks: those below
-// `edge` (an index into the tile) take the scale of the first.
-struct Scales {
-  const float* first;
-  const float* second;
-  int edge;
-};
-__device__ __forceinline__ Scales scales_of(const float* scale, int64_t expert, int row0, int rows,
-                                            int cols) {
-  const int per = (cols + kBlock - 1) / kBlock, r = row0 / kBlock;
-  const int all = (rows + kBlock - 1) / kBlock;
-  const float* p = scale + (expert * all + r) * per;
-  return {p, r + 1 < all ? p + per : p, (r + 1) * kBlock - row0};
-}
-
-// acc += the products of one step's halves, times the scales of its rows.
-template <typename T, bool k8>
-__device__ __forceinline__ void multiply(const Share<T, k8>& w, const s16x8 (&x)[2],
-                                         const Scales& sc, int block, f32x4& acc) {
-  if constexpr (!k8) {
-    acc = mfma16(T{}, w.half(0), x[0], acc);
-    acc = mfma16(T{}, w.half(1), x[1], acc);
-  } else {
-    f32x4 p = {0, 0, 0, 0};
-    p = mfma16(T{}, w.half(0), x[0], p);
-    p = mfma16(T{}, w.half(1), x[1], p);
-    const float s1 = sc.first[block], s2 = sc.second[block];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc[j] += ((lane_id() >> 4) * 4 + j < sc.edge ? s1 : s2) * p[j];
-  }
-}
 
 __device__ __forceinline__ uint32_t take_ticket(Counters* c) {
   return __hip_atomic_fetch_add(&c->ticket.n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -287,15 +275,21 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const uint32_t in_tiles = (uint32_t)used * in_cols;
   const int quarter = l >> 4, column = l & 15;
   uint32_t tile = __builtin_amdgcn_readfirstlane(ticket[0]);
+
   // ---- tiles of W_in: h of expert u's tokens, 32 columns ----
+  // Each wave takes every eighth step.  Four steps of a wave are on their way: as soon
+  // as one is used, the one four further on is loaded in its place, which at the end
+  // of a tile is one of the next.
   if (tile < in_tiles) {
-    const int64_t row_bytes = (int64_t)a.D * W::kBytes;
-    const T* x = (const T*)a.x + min(column, a.T - 1) * a.x_ld + quarter * 16;
-    const int full = a.D / kStep;
+    constexpr int kRing = 4;
+    const uint32_t row_bytes = (uint32_t)a.D * W::kBytes;
+    const char* x = (const char*)((const T*)a.x + min(column, a.T - 1) * a.x_ld);
+    const int steps = (a.D + kStep - 1) / kStep;
+    const int rounds = (steps + kRing * kWaves - 1) / (kRing * kWaves);
+    const int scale_cols = (a.D + kBlock - 1) / kBlock, scale_rows = (2 * a.F + kBlock - 1) / kBlock;
     struct Place {
       int u, f0, e;
       const char* rows[2];  // gate, up
-      uint32_t off[2];      // of the first and the second 16 rows
     };
     auto place_of = [&](uint32_t tile) {
       Place p;
@@ -303,89 +297,111 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       p.f0 = (int)(tile % in_cols) * 32;
       p.e = __builtin_amdgcn_readfirstlane(expert[p.u]);
       p.rows[0] = (const char*)a.w_in + ((int64_t)p.e * 2 * a.F + p.f0) * row_bytes;
-      p.rows[1] = p.rows[0] + a.F * row_bytes;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        p.off[j] = (uint32_t)min(16 * j + column, a.F - 1 - p.f0) * (uint32_t)row_bytes +
-                   quarter * 16 * W::kBytes;
+      p.rows[1] = p.rows[0] + (int64_t)a.F * row_bytes;
       return p;
     };
-    constexpr int kBatch = 4;
-    W w[kBatch][2][2];  // [][gate, up][rows]
-    s16x8 xf[kBatch][2];
-    // Steps s, s + kWaves, ..; beyond the last one that again.
-    auto load = [&](const Place& p, int s) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int at = min(s + i * kWaves, full - 1);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int o = 0; o < 2; ++o)
-            w[i][o][j].load(p.rows[o], p.off[j] + (uint32_t)at * (kStep * W::kBytes));
-        __builtin_memcpy(xf[i], x + at * kStep, 32);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+    // The lane's row of the first or second 16, from the tile's first.
+    auto row_of = [&](const Place& p, int j) {
+      return (uint32_t)min(16 * j + column, a.F - 1 - p.f0) * row_bytes;
     };
-    Place p = place_of(tile);
-    if (full) load(p, wave);
-    if (taker) ticket[1] = mine[1];
-    __syncthreads();
-    uint32_t next = __builtin_amdgcn_readfirstlane(ticket[1]);
-    // A tile's first loads are on their way while the one before it is joined.
-#pragma unroll 1
-    while (true) {
-      uint32_t later = 0;
-      if (taker) later = take_ticket(a.counters);
-      Scales sc[2][2]{};
+    // A lane's four rows of a product lie in one or two rows of blocks.
+    auto first_row = [&](const Place& p, int o, int j) {
+      return min(o * a.F + p.f0 + 16 * j + quarter * 4, 2 * a.F - 1);
+    };
+    struct Slot {
+      W w[2][2];  // [gate, up][rows]
+      Share<T, false> x;
+      float first[2][2], second[2][2];  // scales of 8-bit weights
+    };
+    Slot slots[kRing];
+    auto load = [&](Slot& s, const Place& p, int step) {
+      const int at = k_of(step, a.D);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+          s.w[o][j].load(p.rows[o] + (row_of(p, j) + (uint32_t)at * W::kBytes), a.even_in);
+      s.x.load(x + at * 2, a.even_x);
       if constexpr (k8) {
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            sc[o][j] = scales_of(a.in_scale, p.e, min(o * a.F + p.f0 + 16 * j, 2 * a.F - 1),
-                                 2 * a.F, a.D);
+          for (int j = 0; j < 2; ++j) {
+            const int row = first_row(p, o, j), last = min(row + 3, 2 * a.F - 1);
+            const float* from = a.in_scale + (int64_t)p.e * scale_rows * scale_cols + step * kStep / kBlock;
+            s.first[o][j] = from[row / kBlock * scale_cols];
+            // Four rows that begin at a multiple of four have one scale.
+            s.second[o][j] = a.F % 4 ? from[last / kBlock * scale_cols] : s.first[o][j];
+          }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    Place p = place_of(tile);
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      if (wave + i * kWaves < steps) load(slots[i], p, wave + i * kWaves);
+    if (taker) ticket[1] = mine[1];
+    __syncthreads();
+    uint32_t next = __builtin_amdgcn_readfirstlane(ticket[1]);
+#pragma unroll 1
+    while (true) {
+      uint32_t later = 0;
+      if (taker) later = take_ticket(a.counters);
+      const bool more = next < in_tiles;
+      const Place following = place_of(more ? next : tile);
       f32x4 acc[2][2];
 #pragma unroll
       for (int o = 0; o < 2; ++o)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[o][j] = f32x4{0, 0, 0, 0};
-      int s = wave;
-#pragma unroll 1
-      while (s < full) {
+      auto use = [&](Slot& s, int step) {
+        const int at = k_of(step, a.D);
+        if (!a.even_x) s.x.shift((uint32_t)(uintptr_t)(x + at * 2) & 3);
+        if (!a.even_in)
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = s + i * kWaves;
-          if (at < full) {
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int o = 0; o < 2; ++o)
+              s.w[o][j].shift(((uint32_t)(uintptr_t)p.rows[o] + row_of(p, j) + at * W::kBytes) & 3);
+        if (step * kStep + kStep > a.D) {
+          const int n = dropped(step, a.D);
+          s.x.drop(n);
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                multiply<T, k8>(w[i][o][j], xf[i], sc[o][j], at * kStep / kBlock, acc[o][j]);
-          }
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) s.w[o][j].drop(n);
         }
-        s += kBatch * kWaves;
-        if (s >= full) break;
-        load(p, s);
-      }
-      if (full * kStep < a.D && wave == full % kWaves) {
-        const End end = end_of(a.D, quarter);
-        Share<T, false> xe;
-        xe.load((const char*)(x - quarter * 16 + end.k), 0);
-        xe.keep_end(end.drop);
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            W we;
-            we.load(p.rows[o], p.off[j] + (uint32_t)((end.k - quarter * 16) * W::kBytes));
-            we.keep_end(end.drop);
-            multiply<T, k8>(we, xe.v, sc[o][j], full * kStep / kBlock, acc[o][j]);
+            if constexpr (!k8) {
+              acc[o][j] = mfma16(T{}, s.w[o][j].half(0), s.x.half(0), acc[o][j]);
+              acc[o][j] = mfma16(T{}, s.w[o][j].half(1), s.x.half(1), acc[o][j]);
+            } else {
+              f32x4 q = {0, 0, 0, 0};
+              q = mfma16(T{}, s.w[o][j].half(0), s.x.half(0), q);
+              q = mfma16(T{}, s.w[o][j].half(1), s.x.half(1), q);
+              const int edge = kBlock - first_row(p, o, j) % kBlock;  // rows of the first block
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[o][j][i] += (i < edge ? s.first[o][j] : s.second[o][j]) * q[i];
+            }
           }
+      };
+#pragma unroll 1
+      for (int r = 0; r < rounds; ++r) {
+        const bool last = r + 1 == rounds;
+        const Place& from = last ? following : p;
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) {
+          const int step = wave + (r * kRing + i) * kWaves;
+          const int ahead = last ? wave + i * kWaves : step + kRing * kWaves;
+          if (step < steps) use(slots[i], step);
+          if ((!last || more) && ahead < steps) load(slots[i], from, ahead);
+        }
       }
-      // Written out for either way, so that the loads' registers are free in the last.
-      auto join = [&](int u, int f0) {
+      // The waves' sums are joined and h is stored.
+      {
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
@@ -406,16 +422,16 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         __syncthreads();
         // A pair of columns to a thread.
         const int t = tid / 16, c = tid % 16 * 2;
-        const int i = t < a.T ? slot[u * kTokens + t] : -1;
-        if (i >= 0 && f0 + c < a.h_ld) {
+        const int i = t < a.T ? slot[p.u * kTokens + t] : -1;
+        if (i >= 0 && p.f0 + c < a.h_ld) {
           uint32_t pair = 0;
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float gs = joined[0][t][c + q], us = joined[1][t][c + q];
-            const float hv = f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
+            const float hv = p.f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
             pair |= (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(hv)) << (16 * q);
           }
-          __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + f0 + c), pair,
+          __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + p.f0 + c), pair,
                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         // The stores are written through and done before the tile is counted.  A release
@@ -428,15 +444,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                                  __HIP_MEMORY_SCOPE_AGENT);
         tile = next;
         next = after;
-      };
-      const int u = p.u, f0 = p.f0;
-      if (next >= in_tiles) {
-        join(u, f0);
-        break;
       }
-      p = place_of(next);
-      if (full) load(p, wave);
-      join(u, f0);
+      if (!more) break;
+      p = following;
     }
   }
 
@@ -445,78 +455,83 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   // tiles for every compute unit.  The 16 columns of a product are parts and tokens,
   // and only the products of equal parts are taken; where parts and tokens do not
   // fit 16 columns, a second product has the other half of the parts.  The steps
-  // of all picked experts are one row, q being step q % full of expert q / full, and
+  // of all picked experts are one row, q being step q % per of expert q / per, and
   // part i of a wave's step takes the i-th of `cut` neighbours.
   const int out_tiles = (a.D + out_width - 1) / out_width;
-  const int full = a.F / kStep, steps = used * full;
+  const int per = (a.F + kStep - 1) / kStep, steps = used * per;
   const int passes = cut * a.T > 16 ? 2 : 1, room = 16 * passes / cut;  // columns for tokens
   const int sub = column % out_width;  // as a row of the weights
   const int token = column % room;     // as a column of h
   struct Place { int u, s; };
   // Of kWaves * cut steps.
-  const int ahead_u = full ? kWaves * cut / full : 0, ahead_s = kWaves * cut - ahead_u * full;
+  const int ahead_u = kWaves * cut / per, ahead_s = kWaves * cut % per;
   auto advance = [&](Place& p) {
     p.u += ahead_u;
     p.s += ahead_s;
-    if (p.s >= full) p.s -= full, ++p.u;
+    if (p.s >= per) p.s -= per, ++p.u;
   };
   auto start_of = [&](int part) {
     const int q = wave * cut + part;
-    return Place{full ? q / full : 0, full ? q % full : 0};
+    return Place{q / per, q % per};
   };
   const int w_part = column / out_width, h_part = column / room;
   // Steps of this wave, the last of which may lack some parts.
   const int count = (steps - wave * cut + kWaves * cut - 1) / (kWaves * cut);
+  const bool ragged = a.F % kStep != 0;
   bool ready = false;  // all of h is there
 #pragma unroll 1
   for (int out = blockIdx.x; out < out_tiles; out += gridDim.x) {
     const int n0 = out * out_width;
-    const char* rows =
-        (const char*)a.w_out + ((int64_t)min(n0 + sub, a.D - 1) * a.F + quarter * 16) * W::kBytes;
+    const char* rows = (const char*)a.w_out + (int64_t)min(n0 + sub, a.D - 1) * a.F * W::kBytes;
     const int64_t expert_bytes = (int64_t)a.D * a.F * W::kBytes;
     constexpr int kRing = 6;  // steps on their way
-    W w[kRing];
-    struct Hidden {
-      s16x8 h[2];
-      float value;  // of the token for the step's expert
-      bool there;   // whether it picked it
+    struct Slot {
+      W w;
+      uint32_t off;  // of its address, from a multiple of 4 bytes
+      int drop;
     };
+    struct Hidden {
+      Share<T, false> h;
+      float value;  // of the token for the step's expert, 0 where it did not pick it
+      int drop;     // or -1: what it did not pick adds nothing, whatever its weights hold
+    };
+    Slot w[kRing];
     Hidden h[2][kRing];
     Place pw = start_of(w_part), ph[2] = {start_of(h_part), start_of(h_part + cut / 2)};
-    auto load_w = [&](W& w) {
-      w.load(rows + expert[min(pw.u, used - 1)] * expert_bytes + (int64_t)pw.s * (kStep * W::kBytes), 0);
+    auto load_w = [&](Slot& s) {
+      const char* from = rows + expert[min(pw.u, used - 1)] * expert_bytes + k_of(pw.s, a.F) * W::kBytes;
+      s.w.load(from, a.even_out);
+      s.off = (uint32_t)(uintptr_t)from & 3;
+      s.drop = dropped(pw.s, a.F);
       advance(pw);
     };
-    // From step p, or from `end` values into it.
-    auto load_h = [&](Hidden& h, const Place& p, int end) {
+    auto load_h = [&](Hidden& h, Place& p) {
       const int u = min(p.u, used - 1);
       const int i = token < a.T ? slot[u * kTokens + token] : -1;
-      h.there = i >= 0 && p.u < used;
+      const bool there = i >= 0 && p.u < used;
       const int entry = i < 0 ? 0 : token * k + i;
       h.value = vals[entry];
+      h.drop = there ? dropped(p.s, a.F) : -1;
       // The scale of the column's part, the only one whose products count.
       if constexpr (k8)
         h.value *= a.out_scale[((int64_t)expert[u] * ((a.D + kBlock - 1) / kBlock) + n0 / kBlock) *
                                    ((a.F + kBlock - 1) / kBlock) + p.s * kStep / kBlock];
       // Rows that are not there are read as those of entry 0, and not used.
-      __builtin_memcpy(h.h, a.h + (int64_t)entry * a.h_ld + p.s * kStep + quarter * 16 + end, 32);
+      h.h.load((const char*)(a.h + (int64_t)entry * a.h_ld + k_of(p.s, a.F)), true);
+      advance(p);
     };
     auto load_both = [&](int i) {
-      load_h(h[0][i], ph[0], 0);
-      advance(ph[0]);
-      if (passes == 2) {
-        load_h(h[1][i], ph[1], 0);
-        advance(ph[1]);
-      }
+      load_h(h[0][i], ph[0]);
+      if (passes == 2) load_h(h[1][i], ph[1]);
     };
     f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    auto add = [&](const W& w, const Hidden& h, f32x4& sum) {
+    auto add = [&](const W& w, Hidden& h, f32x4& sum) {
+      if (ragged) h.h.drop(h.drop);
       f32x4 acc = {0, 0, 0, 0};
-      acc = mfma16(T{}, w.half(0), h.h[0], acc);
-      acc = mfma16(T{}, w.half(1), h.h[1], acc);
-      // What a token did not pick adds nothing, whatever its weights hold.
+      acc = mfma16(T{}, w.half(0), h.h.half(0), acc);
+      acc = mfma16(T{}, w.half(1), h.h.half(1), acc);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += h.there ? h.value * acc[j] : 0.0f;
+      for (int j = 0; j < 4; ++j) sum[j] += h.drop >= 0 ? h.value * acc[j] : 0.0f;
     };
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
@@ -548,8 +563,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
       for (int i = 0; i < kRing; ++i) {
         if (j + i >= count) break;
-        add(w[i], h[0][i], sum[0]);
-        if (passes == 2) add(w[i], h[1][i], sum[1]);
+        if (!a.even_out) w[i].w.shift(w[i].off);
+        if (ragged) w[i].w.drop(w[i].drop);
+        add(w[i].w, h[0][i], sum[0]);
+        if (passes == 2) add(w[i].w, h[1][i], sum[1]);
         if (j + i + kRing < count) {
           load_w(w[i]);
           load_both(i);
@@ -557,29 +574,6 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (full * kStep < a.F)
-#pragma unroll 1
-      for (int u0 = wave * cut; u0 < used; u0 += kWaves * cut) {
-        const End end = end_of(a.F, quarter);
-        const int shift = end.k - full * kStep - quarter * 16;
-        W we;
-        we.load(rows + expert[min(u0 + w_part, used - 1)] * expert_bytes +
-                    (int64_t)(end.k - quarter * 16) * W::kBytes, 0);
-        we.keep_end(end.drop);
-#pragma unroll 1
-        for (int pass = 0; pass < passes; ++pass) {
-          Hidden he;
-          load_h(he, Place{u0 + h_part + pass * (cut / 2), full}, shift);
-          Share<T, false> kept;
-          kept.v[0] = he.h[0], kept.v[1] = he.h[1];
-          kept.keep_end(end.drop);
-          he.h[0] = kept.v[0], he.h[1] = kept.v[1];
-          f32x4 one = {0, 0, 0, 0};
-          add(we, he, one);
-          if (pass) sum[1] += one;
-          else sum[0] += one;
-        }
-      }
     __syncthreads();  // `part` of the tile before has been read
 #pragma unroll
     for (int i = 0; i < 2; ++i) *(f32x4*)&part[wave][i][column][quarter * 4] = sum[i];
@@ -587,12 +581,12 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int t = tid / out_width, c = tid % out_width;
     if (t < a.T && n0 + c < a.D) {
       float v = 0.0f;
-      const int per = cut / passes;  // parts of a product
+      const int parts = cut / passes;  // of a product
 #pragma unroll 1
       for (int i = 0; i < cut; ++i)
 #pragma unroll 4
         for (int w = 0; w < kWaves; ++w)
-          v += part[w][i / per][i % per * room + t][i * out_width + c];
+          v += part[w][i / parts][i % parts * room + t][i * out_width + c];
       ((T*)a.y)[(int64_t)t * a.D + n0 + c] = from_f32<T>(v);
     }
   }
@@ -724,6 +718,10 @@ extern "C" spgemm_status spgemm_expert_step(
   a.D = z.D;
   a.F = (int)d.hidden;
   a.h_ld = (int)hidden_pitch(d.hidden);
+  const int64_t wb = scaled ? 1 : 2;
+  a.even_x = (uintptr_t)dX % 4 == 0 && d.x_ld % 2 == 0;
+  a.even_in = (uintptr_t)dWIn % 4 == 0 && d.width * wb % 4 == 0;
+  a.even_out = (uintptr_t)dWOut % 4 == 0 && d.hidden * wb % 4 == 0;
   // Parts as the tokens leave room for them in two products, while there are fewer
   // tiles than work groups.
   a.cut = 1;
