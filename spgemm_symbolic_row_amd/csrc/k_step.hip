@@ -16,6 +16,7 @@
 // by a work group that runs and that waits for nothing: however few work groups
 // are on the chip at a time, every wait ends.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "route_row.hpp"
@@ -115,63 +116,85 @@ __device__ __forceinline__ int dropped(int s, int K) {
 // the values are loaded, all of which are at least in part the row's, and shifted
 // when they are used.  16-bit values are the operands as they are; 8-bit ones are
 // decoded when used, exactly, to x's type.
-template <int kWords>
-struct Words {
-  uint32_t v[kWords + 1];
-  __device__ void load(const char* p, bool even) {
-    if (even) {
-      __builtin_memcpy(v, p, kWords * 4);
-    } else {
-      const uint32_t off = (uint32_t)(uintptr_t)p & 3;
-      const char* q = p - off;
-      __builtin_memcpy(v, __builtin_assume_aligned(q, 4), kWords * 4);
-      v[kWords] = *(const uint32_t*)(q + (off ? kWords * 4 : kWords * 4 - 4));
-    }
-  }
-  // Of a load at a multiple of 4 bytes plus off.
-  __device__ void shift(uint32_t off) {
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 any_u32x4 __attribute__((aligned(1)));
+typedef u32x4 word_u32x4 __attribute__((aligned(4)));
+
+// Without the first n of a word's values of kBytes, beginning with value `first`.
+template <int kBytes>
+__device__ __forceinline__ u32x4 without(u32x4 v, int first, int n) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) v[i] = __builtin_amdgcn_alignbyte(v[i + 1], v[i], off);
+  for (int i = 0; i < 4; ++i) {
+    const int gone = (n - first) * kBytes - 4 * i;  // bytes
+    v[i] &= gone <= 0 ? ~0u : gone >= 4 ? 0u : ~0u << (8 * gone);
   }
-};
+  return v;
+}
+__device__ __forceinline__ u32x4 shifted(u32x4 v, uint32_t next, uint32_t off) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __builtin_amdgcn_alignbyte(i < 3 ? v[(i + 1) & 3] : next, v[i], off);
+  return r;
+}
+// The words that begin at or before p and hold 16 values of kBytes: lo, hi where
+// values have 2 bytes, and one more unless `even`.
+template <int kBytes>
+__device__ __forceinline__ void load_words(const char* p, bool even, u32x4& lo, u32x4& hi,
+                                           uint32_t& more) {
+  if (even) {
+    lo = *(const any_u32x4*)p;
+    if constexpr (kBytes == 2) hi = *(const any_u32x4*)(p + 16);
+  } else {
+    const uint32_t off = (uint32_t)(uintptr_t)p & 3;
+    const char* q = p - off;
+    lo = *(const word_u32x4*)q;
+    if constexpr (kBytes == 2) hi = *(const word_u32x4*)(q + 16);
+    more = *(const uint32_t*)(q + (off ? 16 * kBytes : 16 * kBytes - 4));
+  }
+}
 
 template <typename T, bool k8>
-struct Share : Words<8> {
+struct Share {
   static constexpr int kBytes = 2;
+  u32x4 lo, hi;
+  uint32_t more;
+  __device__ void load(const char* p, bool even) { load_words<2>(p, even, lo, hi, more); }
+  // Of a load at a multiple of 4 bytes plus off.
+  __device__ void shift(uint32_t off) {
+    lo = shifted(lo, hi[0], off);
+    hi = shifted(hi, more, off);
+  }
   // Without the first n values.
   __device__ void drop(int n) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] &= n <= 2 * i ? ~0u : n == 2 * i + 1 ? 0xffff0000u : 0u;
+    lo = without<2>(lo, 0, n);
+    hi = without<2>(hi, 8, n);
   }
-  __device__ s16x8 half(int h) const {
-    s16x8 r;
-    __builtin_memcpy(&r, v + 4 * h, 16);
-    return r;
-  }
+  __device__ s16x8 half(int h) const { return __builtin_bit_cast(s16x8, h ? hi : lo); }
 };
 
 template <typename T>
-struct Share<T, true> : Words<4> {
+struct Share<T, true> {
   static constexpr int kBytes = 1;
-  __device__ void drop(int n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v[i] &= n <= 4 * i ? ~0u : n >= 4 * i + 4 ? 0u : ~0u << (8 * (n - 4 * i));
+  u32x4 lo;
+  uint32_t more;
+  __device__ void load(const char* p, bool even) {
+    u32x4 none;
+    load_words<1>(p, even, lo, none, more);
   }
+  __device__ void shift(uint32_t off) { lo = shifted(lo, more, off); }
+  __device__ void drop(int n) { lo = without<1>(lo, 0, n); }
   __device__ s16x8 half(int h) const {
-    uint32_t r[4];
+    u32x4 r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      const uint32_t q = h ? lo[2 + i] : lo[i];
       if constexpr (__is_same(T, __bf16)) {
-        r[2 * i] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i], 1.0f, false));
-        r[2 * i + 1] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * h + i], 1.0f, true));
+        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false));
+        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true));
       } else {
-        r[2 * i] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + i], 1.0f, false));
-        r[2 * i + 1] = __builtin_bit_cast(
-            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[2 * h + i], 1.0f, true));
+        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q, 1.0f, false));
+        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q, 1.0f, true));
       }
     }
     return __builtin_bit_cast(s16x8, r);
@@ -196,6 +219,7 @@ struct StepArgs {
   int T, D, F, h_ld;
   int most;                // experts that the tokens can pick together
   int cut;                 // parts that a tile of W_out cuts K into
+  int xs_at, xs_ld;        // where the rows of x begin in LDS, and their pitch; 0: they are not there
   bool sigmoid;
   bool even_x, even_in, even_out;  // rows begin at multiples of 4 bytes
 };
@@ -216,6 +240,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint32_t* picked = packed + kNT / L * 2 * k;        // a bit for each of 1024 experts
   uint16_t* expert = (uint16_t*)(picked + 32);        // picked experts, rising
   int16_t* slot = (int16_t*)(expert + (a.most + 1) / 2 * 2);  // of expert u's entry of token t, or -1
+  uint16_t* xs = (uint16_t*)((char*)lds + a.xs_at);  // rows of x, as the lanes take them, if there is room
   __shared__ float part[kWaves][4][16][kPitch];  // [][gate or up, rows][column][row]
   __shared__ float joined[2][kTokens][33];
   __shared__ uint32_t ticket[2];
@@ -229,6 +254,15 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   if (taker) mine[0] = take_ticket(a.counters);
   if (tid < 32) picked[tid] = 0;
   for (int i = tid; i < a.most * kTokens; i += kNT) slot[i] = -1;
+  if (a.xs_ld) {
+    const int per = (a.D + kStep - 1) / kStep * (kStep / 8);  // eights of a row
+    for (int i = tid; i < a.T * per; i += kNT) {
+      const int t = i / per, c = i % per * 8, k0 = c / 16 * 16, at = min(k0, a.D - 16);
+      const int n = k0 - at - c % 16;  // values that other lanes have
+      *(u32x4*)(xs + t * a.xs_ld + c) =
+          without<2>(*(const any_u32x4*)((const uint16_t*)a.x + t * a.x_ld + at + c % 16), 0, n);
+    }
+  }
   for (int t0 = 0; t0 < a.T; t0 += kNT / L) {
     const int t = t0 + tid / L, e0 = tid % L * V;
     if (t0 + wave * (kWave / L) >= a.T) break;  // the whole wave
@@ -304,14 +338,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     auto row_of = [&](const Place& p, int j) {
       return (uint32_t)min(16 * j + column, a.F - 1 - p.f0) * row_bytes;
     };
-    // A lane's four rows of a product lie in one or two rows of blocks.
-    auto first_row = [&](const Place& p, int o, int j) {
-      return min(o * a.F + p.f0 + 16 * j + quarter * 4, 2 * a.F - 1);
-    };
+    const uint16_t* xl = xs + min(column, a.T - 1) * a.xs_ld + quarter * 16;
     struct Slot {
       W w[2][2];  // [gate, up][rows]
-      Share<T, false> x;
-      float first[2][2], second[2][2];  // scales of 8-bit weights
+      Share<T, false> x;  // where it is not in LDS
+      // Of 8-bit weights: 16 rows lie in one or two rows of blocks, whose scales lane
+      // o + 2 j and lane 4 + o + 2 j hold.
+      float scales;
     };
     Slot slots[kRing];
     auto load = [&](Slot& s, const Place& p, int step) {
@@ -321,19 +354,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int o = 0; o < 2; ++o)
           s.w[o][j].load(p.rows[o] + (row_of(p, j) + (uint32_t)at * W::kBytes), a.even_in);
-      s.x.load(x + at * 2, a.even_x);
-      if constexpr (k8) {
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = first_row(p, o, j), last = min(row + 3, 2 * a.F - 1);
-            const float* from = a.in_scale + (int64_t)p.e * scale_rows * scale_cols + step * kStep / kBlock;
-            s.first[o][j] = from[row / kBlock * scale_cols];
-            // Four rows that begin at a multiple of four have one scale.
-            s.second[o][j] = a.F % 4 ? from[last / kBlock * scale_cols] : s.first[o][j];
-          }
-      }
+      if (!a.xs_ld) s.x.load(x + at * 2, a.even_x);
+      if constexpr (k8)
+        if (l < 8) {
+          const int row = (l & 1) * a.F + p.f0 + (l & 2) * 8 + (l & 4 ? 15 : 0);
+          s.scales = a.in_scale[((int64_t)p.e * scale_rows + min(row, 2 * a.F - 1) / kBlock) * scale_cols +
+                                step * kStep / kBlock];
+        }
       __builtin_amdgcn_sched_barrier(0);
     };
     Place p = place_of(tile);
@@ -355,43 +382,48 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[o][j] = f32x4{0, 0, 0, 0};
       auto use = [&](Slot& s, int step) {
-        const int at = k_of(step, a.D);
-        if (!a.even_x) s.x.shift((uint32_t)(uintptr_t)(x + at * 2) & 3);
-        if (!a.even_in)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-              s.w[o][j].shift(((uint32_t)(uintptr_t)p.rows[o] + row_of(p, j) + at * W::kBytes) & 3);
-        if (step * kStep + kStep > a.D) {
-          const int n = dropped(step, a.D);
-          s.x.drop(n);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int o = 0; o < 2; ++o) s.w[o][j].drop(n);
+        const int at = k_of(step, a.D), n = dropped(step, a.D);
+        const bool end = step * kStep + kStep > a.D;
+        s16x8 xf[2];
+        if (a.xs_ld) {
+          xf[0] = *(const s16x8*)(xl + step * kStep);
+          xf[1] = *(const s16x8*)(xl + step * kStep + 8);
+        } else {
+          if (!a.even_x) s.x.shift((uint32_t)(uintptr_t)(x + at * 2) & 3);
+          if (end) s.x.drop(n);
+          xf[0] = s.x.half(0), xf[1] = s.x.half(1);
         }
 #pragma unroll
         for (int o = 0; o < 2; ++o)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            W& w = s.w[o][j];
+            if (!a.even_in)
+              w.shift(((uint32_t)(uintptr_t)p.rows[o] + row_of(p, j) + at * W::kBytes) & 3);
+            if (end) w.drop(n);
             if constexpr (!k8) {
-              acc[o][j] = mfma16(T{}, s.w[o][j].half(0), s.x.half(0), acc[o][j]);
-              acc[o][j] = mfma16(T{}, s.w[o][j].half(1), s.x.half(1), acc[o][j]);
+              acc[o][j] = mfma16(T{}, w.half(0), xf[0], acc[o][j]);
+              acc[o][j] = mfma16(T{}, w.half(1), xf[1], acc[o][j]);
             } else {
               f32x4 q = {0, 0, 0, 0};
-              q = mfma16(T{}, s.w[o][j].half(0), s.x.half(0), q);
-              q = mfma16(T{}, s.w[o][j].half(1), s.x.half(1), q);
-              const int edge = kBlock - first_row(p, o, j) % kBlock;  // rows of the first block
+              q = mfma16(T{}, w.half(0), xf[0], q);
+              q = mfma16(T{}, w.half(1), xf[1], q);
+              auto scale = [&](int lane) {
+                return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s.scales), lane));
+              };
+              const float first = scale(o + 2 * j), second = scale(4 + o + 2 * j);
+              const int edge = kBlock - (o * a.F + p.f0 + 16 * j) % kBlock;  // rows of the first block
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[o][j][i] += (i < edge ? s.first[o][j] : s.second[o][j]) * q[i];
+              for (int i = 0; i < 4; ++i)
+                acc[o][j][i] += (quarter * 4 + i < edge ? first : second) * q[i];
             }
           }
       };
 #pragma unroll 1
       for (int r = 0; r < rounds; ++r) {
         const bool last = r + 1 == rounds;
-        const Place& from = last ? following : p;
+        Place from = p;
+        if (last) from = following;
 #pragma unroll
         for (int i = 0; i < kRing; ++i) {
           const int step = wave + (r * kRing + i) * kWaves;
@@ -484,7 +516,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int n0 = out * out_width;
     const char* rows = (const char*)a.w_out + (int64_t)min(n0 + sub, a.D - 1) * a.F * W::kBytes;
     const int64_t expert_bytes = (int64_t)a.D * a.F * W::kBytes;
-    constexpr int kRing = 6;  // steps on their way
+    constexpr int kRing = 5;  // steps on their way
     struct Slot {
       W w;
       uint32_t off;  // of its address, from a multiple of 4 bytes
@@ -595,6 +627,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 // ---- host ----
 
 constexpr int kGroups = 256;  // one to a compute unit
+// Dynamic LDS of a work group at most: what its static arrays leave.
+constexpr size_t kMostLds = kLdsPerGroup - 46 * 1024;
 
 int64_t hidden_pitch(int64_t F) { return (F + 7) / 8 * 8; }
 
@@ -642,18 +676,45 @@ void logits(const LogitArgs& a, hipStream_t s) {
 }
 
 template <typename T, bool k8>
-void layer(const StepArgs& a, hipStream_t s) {
+void layer(StepArgs a, hipStream_t s) {
   const int n = a.T * a.row.k;
   const int64_t tiles =
       std::max((int64_t)a.most * ((a.F + 31) / 32), ((int64_t)a.D + 16 / a.cut - 1) / (16 / a.cut));
   const dim3 grid((unsigned)std::min<int64_t>(tiles, kGroups));
   const int rows = a.row.E <= 256 ? kNT / 16 : kWaves;  // routed at a time
-  const size_t lds = (2 * n + rows * 2 * a.row.k + 32) * 4 + (a.most + 1) / 2 * 4 +
-                     (size_t)a.most * kTokens * 2;
-  if (a.row.E <= 64) hipLaunchKernelGGL((k_step<T, k8, 16, 4>), grid, dim3(kNT), lds, s, a);
-  else if (a.row.E <= 128) hipLaunchKernelGGL((k_step<T, k8, 16, 8>), grid, dim3(kNT), lds, s, a);
-  else if (a.row.E <= 256) hipLaunchKernelGGL((k_step<T, k8, 16, 16>), grid, dim3(kNT), lds, s, a);
-  else hipLaunchKernelGGL((k_step<T, k8, 64, 16>), grid, dim3(kNT), lds, s, a);
+  size_t lds = (2 * n + rows * 2 * a.row.k + 32) * 4 + (a.most + 1) / 2 * 4 +
+               (size_t)a.most * kTokens * 2;
+  // The rows of x, where they fit: an access of 16 bytes takes the vector memory path a
+  // cycle, and those of x half as many again as 8-bit weights (8 tokens, 34 experts of
+  // 2048 x 1408: W_in 69 -> 48 us).  8 more values to a row spread its columns over
+  // the banks.
+  const int ld = (a.D + kStep - 1) / kStep * kStep + 8;
+  const size_t at = (lds + 15) / 16 * 16, rows_bytes = (size_t)a.T * ld * 2;
+  if (at + rows_bytes <= kMostLds) {
+    a.xs_at = (int)at;
+    a.xs_ld = ld;
+    lds = at + rows_bytes;
+  }
+  const int row_kind = a.row.E <= 64 ? 0 : a.row.E <= 128 ? 1 : a.row.E <= 256 ? 2 : 3;
+  static std::atomic<uint64_t> allowed[4] = {};  // by kernel: devices whose LDS limit is set
+  auto launch = [&](auto kernel) {
+    int device = 0;
+    // After a failure nothing more is launched, and setting the limit, which leaves
+    // the error state clear, does not lose it: the caller's last look reports it.
+    if (hipPeekAtLastError() != hipSuccess || hipGetDevice(&device) != hipSuccess) return;
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(allowed[row_kind].load() & bit)) {
+      allow_max_dynamic_lds((const void*)kernel);
+      allowed[row_kind].fetch_or(bit);
+    }
+    hipLaunchKernelGGL(kernel, grid, dim3(kNT), lds, s, a);
+  };
+  switch (row_kind) {
+    case 0: return launch(k_step<T, k8, 16, 4>);
+    case 1: return launch(k_step<T, k8, 16, 8>);
+    case 2: return launch(k_step<T, k8, 16, 16>);
+    default: return launch(k_step<T, k8, 64, 16>);
+  }
 }
 
 }  // namespace
@@ -722,11 +783,12 @@ extern "C" spgemm_status spgemm_expert_step(
   a.even_x = (uintptr_t)dX % 4 == 0 && d.x_ld % 2 == 0;
   a.even_in = (uintptr_t)dWIn % 4 == 0 && d.width * wb % 4 == 0;
   a.even_out = (uintptr_t)dWOut % 4 == 0 && d.hidden * wb % 4 == 0;
-  // Parts as the tokens leave room for them in two products, while there are fewer
-  // tiles than work groups.
+  // Parts as the tokens leave room for them in two products, so that the compute units
+  // have the fewest columns to do one after the other.
+  auto turns = [&](int64_t cut) { return ((d.width * cut + 15) / 16 + kGroups - 1) / kGroups; };
   a.cut = 1;
-  while (2 * a.cut * a.T <= 2 * kTokens && (d.width + 15) / 16 * 2 * a.cut <= kGroups) a.cut *= 2;
-  a.cut = std::min(a.cut, 16);
+  for (int cut = 2; cut <= 16 && cut * a.T <= 2 * kTokens; cut *= 2)
+    if (turns(cut) * a.cut < turns(a.cut) * cut) a.cut = cut;
   a.most = (int)std::min<int64_t>(d.experts, d.tokens * d.k);
   (void)hipGetLastError();  // an error that earlier calls left is not this one's
   const hipStream_t s = (hipStream_t)stream;
