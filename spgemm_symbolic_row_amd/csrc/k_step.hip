@@ -239,7 +239,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint32_t* packed = (uint32_t*)(vals + n);           // 2 k for each row routed at a time
   uint32_t* picked = packed + kNT / L * 2 * k;        // a bit for each of 1024 experts
   uint16_t* expert = (uint16_t*)(picked + 32);        // picked experts, rising
-  int16_t* slot = (int16_t*)(expert + (a.most + 1) / 2 * 2);  // of expert u's entry of token t, or -1
+  int16_t* entry_of = (int16_t*)(expert + (a.most + 1) / 2 * 2);  // token t's for expert u, or -1
+  float* value_of = (float*)(entry_of + a.most * kTokens);        // and its value
   uint16_t* xs = (uint16_t*)((char*)lds + a.xs_at);  // rows of x, as the lanes take them, if there is room
   __shared__ float part[kWaves][4][16][kPitch];  // [][gate or up, rows][column][row]
   __shared__ float joined[2][kTokens][33];
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   uint32_t mine[2] = {0, 0};
   if (taker) mine[0] = take_ticket(a.counters);
   if (tid < 32) picked[tid] = 0;
-  for (int i = tid; i < a.most * kTokens; i += kNT) slot[i] = -1;
+  for (int i = tid; i < a.most * kTokens; i += kNT) entry_of[i] = -1;
   if (a.xs_ld) {
     const int per = (a.D + kStep - 1) / kStep * (kStep / 8);  // eights of a row
     for (int i = tid; i < a.T * per; i += kNT) {
@@ -299,7 +300,8 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     int u = __popc(picked[e / 32] & ((1u << (e % 32)) - 1));
     for (int j = 0; j < e / 32; ++j) u += __popc(picked[j]);
     expert[u] = (uint16_t)e;
-    slot[u * kTokens + i / k] = (int16_t)(i % k);
+    entry_of[u * kTokens + i / k] = (int16_t)i;
+    value_of[u * kTokens + i / k] = vals[i];
   }
   __syncthreads();
 
@@ -454,7 +456,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         __syncthreads();
         // A pair of columns to a thread.
         const int t = tid / 16, c = tid % 16 * 2;
-        const int i = t < a.T ? slot[p.u * kTokens + t] : -1;
+        const int i = t < a.T ? entry_of[p.u * kTokens + t] : -1;
         if (i >= 0 && p.f0 + c < a.h_ld) {
           uint32_t pair = 0;
 #pragma unroll
@@ -463,7 +465,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             const float hv = p.f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
             pair |= (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(hv)) << (16 * q);
           }
-          __hip_atomic_store((uint32_t*)(a.h + (int64_t)(t * k + i) * a.h_ld + p.f0 + c), pair,
+          __hip_atomic_store((uint32_t*)(a.h + (int64_t)i * a.h_ld + p.f0 + c), pair,
                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
         // The stores are written through and done before the tile is counted.  A release
@@ -493,7 +495,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int per = (a.F + kStep - 1) / kStep, steps = used * per;
   const int passes = cut * a.T > 16 ? 2 : 1, room = 16 * passes / cut;  // columns for tokens
   const int sub = column % out_width;  // as a row of the weights
-  const int token = column % room;     // as a column of h
+  const int token = min(column % room, a.T - 1);  // as a column of h, some of which are not used
   struct Place { int u, s; };
   // Of kWaves * cut steps.
   const int ahead_u = kWaves * cut / per, ahead_s = kWaves * cut % per;
@@ -515,7 +517,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   for (int out = blockIdx.x; out < out_tiles; out += gridDim.x) {
     const int n0 = out * out_width;
     const char* rows = (const char*)a.w_out + (int64_t)min(n0 + sub, a.D - 1) * a.F * W::kBytes;
-    const int64_t expert_bytes = (int64_t)a.D * a.F * W::kBytes;
+    const uint64_t expert_bytes = (uint64_t)a.D * a.F * W::kBytes;
+    const int scale_cols = (a.F + kBlock - 1) / kBlock;
+    const uint64_t scale_stride = (uint64_t)((a.D + kBlock - 1) / kBlock) * scale_cols;
+    const float* scales = a.out_scale + n0 / kBlock * (int64_t)scale_cols;
     constexpr int kRing = 5;  // steps on their way
     struct Slot {
       W w;
@@ -524,32 +529,32 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     struct Hidden {
       Share<T, false> h;
-      float value;  // of the token for the step's expert, 0 where it did not pick it
+      float value;  // of the token for the step's expert
+      float scale;  // of 8-bit weights: that of the column's part, whose products count
       int drop;     // or -1: what it did not pick adds nothing, whatever its weights hold
     };
     Slot w[kRing];
     Hidden h[2][kRing];
     Place pw = start_of(w_part), ph[2] = {start_of(h_part), start_of(h_part + cut / 2)};
     auto load_w = [&](Slot& s) {
-      const char* from = rows + expert[min(pw.u, used - 1)] * expert_bytes + k_of(pw.s, a.F) * W::kBytes;
+      const char* from = rows + expert[min(pw.u, used - 1)] * expert_bytes +
+                         (uint32_t)(k_of(pw.s, a.F) * W::kBytes);
       s.w.load(from, a.even_out);
       s.off = (uint32_t)(uintptr_t)from & 3;
       s.drop = dropped(pw.s, a.F);
       advance(pw);
     };
     auto load_h = [&](Hidden& h, Place& p) {
-      const int u = min(p.u, used - 1);
-      const int i = token < a.T ? slot[u * kTokens + token] : -1;
+      const int u = min(p.u, used - 1), at = u * kTokens + token;
+      const int i = entry_of[at];
       const bool there = i >= 0 && p.u < used;
-      const int entry = i < 0 ? 0 : token * k + i;
-      h.value = vals[entry];
+      h.value = value_of[at];
       h.drop = there ? dropped(p.s, a.F) : -1;
-      // The scale of the column's part, the only one whose products count.
       if constexpr (k8)
-        h.value *= a.out_scale[((int64_t)expert[u] * ((a.D + kBlock - 1) / kBlock) + n0 / kBlock) *
-                                   ((a.F + kBlock - 1) / kBlock) + p.s * kStep / kBlock];
+        h.scale = scales[expert[u] * scale_stride + (uint32_t)(p.s * kStep / kBlock)];
       // Rows that are not there are read as those of entry 0, and not used.
-      h.h.load((const char*)(a.h + (int64_t)entry * a.h_ld + k_of(p.s, a.F)), true);
+      h.h.load((const char*)(a.h + (uint64_t)(uint32_t)max(i, 0) * (uint32_t)a.h_ld +
+                             (uint32_t)k_of(p.s, a.F)), true);
       advance(p);
     };
     auto load_both = [&](int i) {
@@ -558,12 +563,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     auto add = [&](const W& w, Hidden& h, f32x4& sum) {
-      if (ragged) h.h.drop(h.drop);
+      if (ragged && __ballot(h.drop > 0)) h.h.drop(h.drop);
       f32x4 acc = {0, 0, 0, 0};
       acc = mfma16(T{}, w.half(0), h.h.half(0), acc);
       acc = mfma16(T{}, w.half(1), h.h.half(1), acc);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += h.drop >= 0 ? h.value * acc[j] : 0.0f;
+      for (int j = 0; j < 4; ++j)
+        sum[j] += h.drop >= 0 ? (k8 ? h.value * h.scale : h.value) * acc[j] : 0.0f;
     };
 #pragma unroll
     for (int i = 0; i < kRing; ++i)
@@ -590,15 +596,18 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int i = 0; i < kRing; ++i)
       if (i < count) load_both(i);
     __builtin_amdgcn_sched_barrier(0);
+    auto use = [&](int i) {
+      if (!a.even_out) w[i].w.shift(w[i].off);
+      // Only the last step of an expert has values to drop.
+      if (ragged && __ballot(w[i].drop > 0)) w[i].w.drop(w[i].drop);
+      add(w[i].w, h[0][i], sum[0]);
+      if (passes == 2) add(w[i].w, h[1][i], sum[1]);
+    };
 #pragma unroll 1
     for (int j = 0; j < count; j += kRing) {
 #pragma unroll
       for (int i = 0; i < kRing; ++i) {
-        if (j + i >= count) break;
-        if (!a.even_out) w[i].w.shift(w[i].off);
-        if (ragged) w[i].w.drop(w[i].drop);
-        add(w[i].w, h[0][i], sum[0]);
-        if (passes == 2) add(w[i].w, h[1][i], sum[1]);
+        if (j + i < count) use(i);
         if (j + i + kRing < count) {
           load_w(w[i]);
           load_both(i);
@@ -683,7 +692,7 @@ void layer(StepArgs a, hipStream_t s) {
   const dim3 grid((unsigned)std::min<int64_t>(tiles, kGroups));
   const int rows = a.row.E <= 256 ? kNT / 16 : kWaves;  // routed at a time
   size_t lds = (2 * n + rows * 2 * a.row.k + 32) * 4 + (a.most + 1) / 2 * 4 +
-               (size_t)a.most * kTokens * 2;
+               (size_t)a.most * kTokens * 6;
   // The rows of x, where they fit: an access of 16 bytes takes the vector memory path a
   // cycle, and those of x half as many again as 8-bit weights (8 tokens, 34 experts of
   // 2048 x 1408: W_in 69 -> 48 us).  8 more values to a row spread its columns over
