@@ -1,10 +1,11 @@
-"""Trains one sparse expert layer on synthetic data, then serves single tokens.
+"""Trains a norm and one sparse expert layer on synthetic data, then serves a few tokens.
 
     python examples/expert_layer.py [--steps N] [--tokens T] [--experts E] [--width D] [--hidden F]
 
-Every step: logits, routing, the experts' products, a squared error against a
-random target map, all gradients, clipping by their global norm, and plain
-gradient descent on fp32 copies of the parameters.  The bias of the router is
+Every step: layer norm, logits, routing, the experts' products, a squared error
+against a random target map, all gradients, clipping by their global norm, and
+plain gradient descent on fp32 copies of the parameters.  What the backward pass
+needs of the activations is kept in 8 bits.  The bias of the router is
 moved after every step towards experts with fewer tokens.  At the end the
 routing matrix R is taken as CSR and R^T R, the number of tokens that two
 experts share, is made by the library's sparse product.
@@ -28,7 +29,8 @@ def train(steps=30, tokens=4096, experts=16, width=256, hidden=128, k=2, lr=0.5,
         return torch.randn(shape, generator=gen, device=dev) * scale
 
     target = randn(width, width, scale=width ** -0.5)
-    main = {"router": randn(experts, width, scale=width ** -0.5),
+    main = {"norm": torch.ones(width, device=dev), "shift": torch.zeros(width, device=dev),
+            "router": randn(experts, width, scale=width ** -0.5),
             "w_in": randn(experts, 2 * hidden, width, scale=width ** -0.5),
             "w_out": randn(experts, width, hidden, scale=hidden ** -0.5)}
     bias = torch.zeros(experts, device=dev)
@@ -38,17 +40,21 @@ def train(steps=30, tokens=4096, experts=16, width=256, hidden=128, k=2, lr=0.5,
         want = torch.tanh(x.float() @ target.t())
         w_in, w_out = main["w_in"].to(bf), main["w_out"].to(bf)
 
-        logits = x.float() @ main["router"].t()
+        h, kept_norm = sg.layer_norm(x, main["norm"], main["shift"], keep="e4m3")
+        logits = h.float() @ main["router"].t()
         r = sg.route(logits, k, scores="sigmoid", bias=bias)
-        y, kept = sg.experts(x, w_in, w_out, r.col, r.val, keep=True)
+        y, kept = sg.experts(h, w_in, w_out, r.col, r.val, keep="e4m3")
 
         err = y.float() - want
         losses.append(err.square().mean())
         dy = (err * (2.0 / tokens)).to(bf)
 
-        _, dw_in, dw_out, dval = sg.experts_backward(dy, kept)
+        dh, dw_in, dw_out, dval = sg.experts_backward(dy, kept)
         dlogits = sg.route_backward(logits, r, dval)
-        grads = {"router": dlogits.t() @ x.float(), "w_in": dw_in, "w_out": dw_out}
+        dh = (dh.float() + dlogits @ main["router"]).to(bf)
+        _, dnorm, dshift = sg.layer_norm_backward(dh, kept_norm)
+        grads = {"norm": dnorm, "shift": dshift, "router": dlogits.t() @ h.float(), "w_in": dw_in,
+                 "w_out": dw_out}
         clipped = {n: torch.empty_like(main[n]) for n in main}
         sg.clip_grad_norm(grads.values(), 1.0, out=clipped.values())
         for n in main:
@@ -79,13 +85,13 @@ def main():
     row_ptr, col, val = shared_tokens(r)
     print(f"pairs of experts that share tokens: {int(row_ptr[-1])} of {a.experts ** 2}")
 
-    # Single tokens: the same layer, without what training keeps.
+    # A few tokens at a time: the same layer, without what training keeps.
     w_in, w_out = params["w_in"].bfloat16(), params["w_out"].bfloat16()
-    x = torch.randn(1, a.width, device="cuda").bfloat16()
+    x = torch.randn(4, a.width, device="cuda").bfloat16()
     for _ in range(3):
-        t = sg.route(x.float() @ params["router"].t(), 2, scores="sigmoid")
-        x = sg.experts(x, w_in, w_out, t.col, t.val)
-        print("token to experts", t.col[0].tolist())
+        h = sg.layer_norm(x, params["norm"], params["shift"])
+        x, t = sg.expert_step(h, params["router"], w_in, w_out, 2, scores="sigmoid")
+        print("tokens to experts", t.col.tolist())
 
 
 if __name__ == "__main__":
