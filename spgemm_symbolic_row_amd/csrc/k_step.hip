@@ -5,6 +5,12 @@
 // token picked is one tile of rows, whichever tokens those are: its weights are
 // read once, straight from memory to registers, and bound the layer.
 //
+// The hidden vector is kept in two terms of x's type, the second being what the
+// rounding to the first leaves: rounded once, its error would add to that of y's own
+// rounding and make y 1.4 times as far off (1.5 and more for few entries).  The
+// second products cost 1 us of 64 (5 tokens, 19 experts of 2040 x 1400 in 8 bits) and
+// 16 of 135 (16 tokens, 55 experts of 2048 x 768).
+//
 // The logits: a work group to an expert; sums in 64 bits, so that the choice among
 // close experts does not depend on their order.
 //
@@ -212,7 +218,7 @@ struct StepArgs {
   const float* out_scale;  // E x ceil(D / 128) x ceil(F / 128)
   const float* logits;
   Counters* counters;
-  uint16_t* h;             // by entry t k + i, rows of h_ld
+  uint16_t* h;             // by entry t k + i, rows of h_ld; then what they leave of h
   void* y;
   int32_t* col;
   float* val;
@@ -458,15 +464,19 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int t = tid / 16, c = tid % 16 * 2;
         const int i = t < a.T ? entry_of[p.u * kTokens + t] : -1;
         if (i >= 0 && p.f0 + c < a.h_ld) {
-          uint32_t pair = 0;
+          uint32_t pair[2] = {0, 0};
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float gs = joined[0][t][c + q], us = joined[1][t][c + q];
             const float hv = p.f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
-            pair |= (uint32_t)__builtin_bit_cast(uint16_t, from_f32<T>(hv)) << (16 * q);
+            const T first = from_f32<T>(hv), rest = from_f32<T>(hv - to_f32(first));
+            pair[0] |= (uint32_t)__builtin_bit_cast(uint16_t, first) << (16 * q);
+            pair[1] |= (uint32_t)__builtin_bit_cast(uint16_t, rest) << (16 * q);
           }
-          __hip_atomic_store((uint32_t*)(a.h + (int64_t)i * a.h_ld + p.f0 + c), pair,
-                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          uint32_t* to = (uint32_t*)(a.h + (int64_t)i * a.h_ld + p.f0 + c);
+          __hip_atomic_store(to, pair[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(to + (int64_t)n * a.h_ld / 2, pair[1], __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
         }
         // The stores are written through and done before the tile is counted.  A release
         // at this scope would also write the L2's other lines back.
@@ -512,6 +522,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   // Steps of this wave, the last of which may lack some parts.
   const int count = (steps - wave * cut + kWaves * cut - 1) / (kWaves * cut);
   const bool ragged = a.F % kStep != 0;
+  const int64_t rest_at = (int64_t)n * a.h_ld;  // h's second terms, from its first
   bool ready = false;  // all of h is there
 #pragma unroll 1
   for (int out = blockIdx.x; out < out_tiles; out += gridDim.x) {
@@ -521,14 +532,14 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int scale_cols = (a.F + kBlock - 1) / kBlock;
     const uint64_t scale_stride = (uint64_t)((a.D + kBlock - 1) / kBlock) * scale_cols;
     const float* scales = a.out_scale + n0 / kBlock * (int64_t)scale_cols;
-    constexpr int kRing = 5;  // steps on their way
+    constexpr int kRing = 3;  // steps on their way
     struct Slot {
       W w;
       uint32_t off;  // of its address, from a multiple of 4 bytes
       int drop;
     };
     struct Hidden {
-      Share<T, false> h;
+      Share<T, false> h, rest;
       float value;  // of the token for the step's expert
       float scale;  // of 8-bit weights: that of the column's part, whose products count
       int drop;     // or -1: what it did not pick adds nothing, whatever its weights hold
@@ -553,8 +564,9 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       if constexpr (k8)
         h.scale = scales[expert[u] * scale_stride + (uint32_t)(p.s * kStep / kBlock)];
       // Rows that are not there are read as those of entry 0, and not used.
-      h.h.load((const char*)(a.h + (uint64_t)(uint32_t)max(i, 0) * (uint32_t)a.h_ld +
-                             (uint32_t)k_of(p.s, a.F)), true);
+      const uint16_t* from = a.h + (uint64_t)(uint32_t)max(i, 0) * (uint32_t)a.h_ld + (uint32_t)k_of(p.s, a.F);
+      h.h.load((const char*)from, true);
+      h.rest.load((const char*)(from + rest_at), true);
       advance(p);
     };
     auto load_both = [&](int i) {
@@ -563,10 +575,12 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     };
     f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     auto add = [&](const W& w, Hidden& h, f32x4& sum) {
-      if (ragged && __ballot(h.drop > 0)) h.h.drop(h.drop);
+      if (ragged && __ballot(h.drop > 0)) h.h.drop(h.drop), h.rest.drop(h.drop);
       f32x4 acc = {0, 0, 0, 0};
       acc = mfma16(T{}, w.half(0), h.h.half(0), acc);
       acc = mfma16(T{}, w.half(1), h.h.half(1), acc);
+      acc = mfma16(T{}, w.half(0), h.rest.half(0), acc);
+      acc = mfma16(T{}, w.half(1), h.rest.half(1), acc);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         sum[j] += h.drop >= 0 ? (k8 ? h.value * h.scale : h.value) * acc[j] : 0.0f;
@@ -649,7 +663,7 @@ struct Work {
 Work take_work(Carver& c, const spgemm_expert_step_desc& d) {
   Work w{};
   w.logits = c.take<float>(d.tokens * d.experts);
-  w.h = c.take<uint16_t>(d.tokens * d.k * hidden_pitch(d.hidden));
+  w.h = c.take<uint16_t>(2 * d.tokens * d.k * hidden_pitch(d.hidden));
   w.counters = c.take<Counters>(1);
   return w;
 }
