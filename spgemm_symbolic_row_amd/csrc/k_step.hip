@@ -22,6 +22,15 @@
 // until all results are there.  It waits only when every tile of W_in has been taken
 // by a work group that runs and that waits for nothing: however few work groups
 // are on the chip at a time, every wait ends.
+//
+// One token with 6 of 64 experts of 2048 x 1024 takes 29 us where a copy of its 75 MB
+// takes 15: the logits' launch 3, routing and tables 6, W_in 10 (5 TB/s), the wait for
+// the slowest result 2, W_out, whose weights are there by then, 4.  16 tokens with 55
+// of 128 experts of 2048 x 768 take 139 us for 519 MB: W_in runs at 5.1 TB/s, W_out at
+// 3.9, whose loop over steps is bound by its instructions.
+//
+// A work group of 8 waves has a compute unit: two of them, with half the registers,
+// spill or have half the loads on their way (W_in's tiles 16 against 11 us).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
