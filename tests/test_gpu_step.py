@@ -85,6 +85,10 @@ SIZES = [
     (16, 1024, 64, 16, 18),
     (1, 6, 2, 4104, 1032),
     (11, 16, 16, 128, 256),
+    (10, 200, 6, 72, 40),
+    (16, 4, 2, 4160, 48),    # rows of x that do not fit LDS
+    (15, 3, 1, 4097, 40),
+    (16, 5, 1, 8200, 33),
 ]
 
 
@@ -175,6 +179,56 @@ def test_strides_and_alignment():
             x = buf[off:off + T * ld].view(T, ld)[:, :D]
             x.copy_(t[0])
             check(t, k, dev=[x, *(None if v is None else shifted(v) for v in t[1:])])
+
+
+@pytest.mark.parametrize("D", [4160, 4097])
+def test_strides_of_rows_that_stay_in_memory(D):
+    T, E, k, F = 16, 3, 2, 40
+    for wdtype in (BF, E4):
+        t = tensors(T, E, D, F, BF, wdtype, BF, 12)
+        for ld, off in ((D + 8, 0), (D + 3, 1), (D, 1), (D + 2, 2)):
+            buf = torch.full((T * ld + off + 8,), float("nan"), dtype=BF, device="cuda")
+            x = buf[off:off + T * ld].view(T, ld)[:, :D]
+            x.copy_(t[0])
+            check(t, k, dev=[x, *(None if v is None else v.cuda() for v in t[1:])])
+
+
+def test_an_error_that_another_call_left_is_not_reported():
+    """The runtime keeps the last error of a thread until it is read."""
+    t = [None if v is None else v.cuda() for v in tensors(4, 8, 64, 32, BF, BF, BF, 21)]
+    w = torch.ones(64, device="cuda")
+    hip = sg.lib()   # the runtime that the library is linked to
+
+    def every_call(left):
+        left()
+        h, kept = sg.layer_norm(t[0], w, keep="e4m3")
+        left()
+        d = sg.layer_norm_backward(h, kept)[:2]
+        left()
+        return (h, *d, sg.expert_step(*t[:4], 2)[0])
+
+    def left():
+        assert hip.hipSetDevice(1 << 20) != 0 and hip.hipPeekAtLastError() != 0
+
+    want = every_call(lambda: None)
+    torch.cuda.synchronize()
+    got = every_call(left)
+    hip.hipGetLastError()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_stride_of_a_single_row():
+    """One token out of a larger tensor: whatever its row stride is, there is one row."""
+    t = [v.cuda() for v in tensors(1, 4, 64, 32, BF, BF, BF, 23)[:4]]
+    w = torch.ones(64, device="cuda")
+    want, norm = sg.expert_step(*t, 2)[0], sg.layer_norm(t[0], w)
+    for stride in (17, 1 << 30):
+        x = torch.empty(stride + 64, dtype=BF, device="cuda").as_strided((1, 64), (stride, 1))
+        x.copy_(t[0])
+        assert torch.equal(sg.expert_step(x, *t[1:], 2)[0], want)
+        assert torch.equal(sg.layer_norm(x, w), norm)
+    torch.cuda.synchronize()
 
 
 def test_the_same_as_the_calls_that_it_joins():
