@@ -345,7 +345,7 @@ def expert_step(x, w_router, w_in, w_out, k, in_scale=None, out_scale=None, scor
             raise ValueError("float8_e4m3fn weights need in_scale and out_scale")
         _dense(in_scale, (E, -(-2 * F // 128), -(-D // 128)), torch.float32, dev, "in_scale")
         _dense(out_scale, (E, -(-D // 128), -(-F // 128)), torch.float32, dev, "out_scale")
-        _unrecorded(x, w_router, in_scale, out_scale)
+        _unrecorded(x, w_router, w_in, w_out, in_scale, out_scale)
     if bias is not None:
         _dense(bias, (E,), torch.float32, dev, "bias")
     if active is not None:

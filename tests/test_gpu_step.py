@@ -325,3 +325,15 @@ def test_no_tokens_and_refusals():
         args = [x, router, w_in, w_out]
         args[i] = args[i].clone().requires_grad_()
         bad(TypeError, *args, 2)
+
+
+def test_weights_in_8_bits_that_require_a_gradient():
+    t = tensors(4, 8, 64, 32, BF, E4, BF, 17)
+    given = [v.cuda() for v in t]
+    for i in range(6):
+        x, router, w_in, w_out, s_in, s_out = (v.clone().requires_grad_() if j == i else v
+                                               for j, v in enumerate(given))
+        with pytest.raises(TypeError, match="requires a gradient"):
+            sg.expert_step(x, router, w_in, w_out, 2, s_in, s_out)
+        with torch.no_grad():
+            sg.expert_step(x, router, w_in, w_out, 2, s_in, s_out)
