@@ -27,7 +27,9 @@
 // takes 15: the logits' launch 3, routing and tables 6, W_in 10 (5 TB/s), the wait for
 // the slowest result 2, W_out, whose weights are there by then, 4.  16 tokens with 55
 // of 128 experts of 2048 x 768 take 139 us for 519 MB: W_in runs at 5.1 TB/s, W_out at
-// 3.9, whose loop over steps is bound by its instructions.
+// 3.9: a step there has eight accesses of h to two of weights, of 16 cycles of the vector
+// memory path each, about half of its 44 us; neither the waits nor the addresses bound it
+// (without conditions between steps, 32-bit addresses: 145 against 144, side by side).
 //
 // A work group of 8 waves has a compute unit: two of them, with half the registers,
 // spill or have half the loads on their way (W_in's tiles 16 against 11 us).
