@@ -631,7 +631,7 @@ spgemm_status spgemm_layer_norm_forward(const spgemm_layer_norm_desc *desc,
  * dy (dGradBias may be NULL) in the weights' type.  m and r are the kept ones; x
  * is the tensor (kept_form 1) or what its 8 bits stand for (2; dX is not read and
  * may be NULL).  Sums in fp32, in an order that the sizes alone fix.  Without rows
- * dw and db are 0. */
+ * dw and db are 0, and of the inputs only dWeight may not be NULL. */
 spgemm_status spgemm_layer_norm_backward(
     const spgemm_layer_norm_desc *desc, const void *dX, const void *dWeight,
     const void *dGradY, const void *dKept, void *dGradX, void *dGradWeight,

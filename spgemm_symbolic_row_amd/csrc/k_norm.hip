@@ -512,9 +512,10 @@ extern "C" spgemm_status spgemm_layer_norm_backward(const spgemm_layer_norm_desc
   if (st != SPGEMM_OK) return st;
   if (desc->kept_form == kPlain)
     return refuse(SPGEMM_ERR_INVALID_ARG, "layer_norm: a backward pass needs what a forward kept");
-  if (!dGradWeight || !dWork ||
-      (desc->rows > 0 && ((!dX && desc->kept_form == kStats) || !dWeight || !dGradY || !dKept ||
-                          !dGradX)))
+  // Without rows the kernel that writes zeros reads the weight all the same.
+  if (!dWeight || !dGradWeight || !dWork ||
+      (desc->rows > 0 &&
+       ((!dX && desc->kept_form == kStats) || !dGradY || !dKept || !dGradX)))
     return refuse(SPGEMM_ERR_INVALID_ARG, "layer_norm: null array");
   NormArgs a = args_of(*desc, dX, dWeight);
   a.dy = dGradY;
