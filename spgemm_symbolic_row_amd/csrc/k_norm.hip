@@ -256,11 +256,12 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float gj = to_f32(raw[r].dy[v][j]), aj = gj * w[v][j];
-            const float nj = (n[r][v][j] - raw[r].mean) * rstd[r];
+            // Columns beyond the row have no dy; their -m r may be infinite where n is not.
+            const float nj = (v * L + lane) * 8 + j < a.D
+                                 ? (n[r][v][j] - raw[r].mean) * rstd[r] : 0.0f;
             g[r][v][j] = gj;
             n[r][v][j] = nj;
             db[v][j] += gj;
-            // Columns beyond the row have no dy, but an n.
             dw[v][j] += gj * nj;
             s[2 * r] += aj;
             s[2 * r + 1] += aj * nj;
