@@ -250,7 +250,8 @@ template <typename T, bool k8, int L, int V>
 __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_step(
     StepArgs a) {
   typedef Share<T, k8> W;
-  extern __shared__ uint32_t lds[];
+  // 16 bytes: x is read from here by that, from offsets that the host aligns.
+  extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int k = a.row.k, n = a.T * k, E = a.row.E;
   int32_t* cols = (int32_t*)lds;                      // n
   float* vals = (float*)(cols + n);                   // n
@@ -260,7 +261,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   int16_t* entry_of = (int16_t*)(expert + (a.most + 1) / 2 * 2);  // token t's for expert u, or -1
   float* value_of = (float*)(entry_of + a.most * kTokens);        // and its value
   uint16_t* xs = (uint16_t*)((char*)lds + a.xs_at);  // rows of x, as the lanes take them, if there is room
-  __shared__ float part[kWaves][4][16][kPitch];  // [][gate or up, rows][column][row]
+  __shared__ __attribute__((aligned(16))) float part[kWaves][4][16][kPitch];  // [][gate or up, rows][column][row]
   __shared__ float joined[2][kTokens][33];
   __shared__ uint32_t ticket[2];
   const int tid = threadIdx.x, l = lane_id();
