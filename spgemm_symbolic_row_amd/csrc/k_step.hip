@@ -482,7 +482,10 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           for (int q = 0; q < 2; ++q) {
             const float gs = joined[0][t][c + q], us = joined[1][t][c + q];
             const float hv = p.f0 + c + q < a.F ? gs / (1.0f + expf(-gs)) * us : 0.0f;
-            const T first = from_f32<T>(hv), rest = from_f32<T>(hv - to_f32(first));
+            const T first = from_f32<T>(hv);
+            // Nothing is left of a value beyond the type, or y were inf - inf.
+            const bool finite = fabsf(to_f32(first)) < INFINITY;
+            const T rest = from_f32<T>(finite ? hv - to_f32(first) : 0.0f);
             pair[0] |= (uint32_t)__builtin_bit_cast(uint16_t, first) << (16 * q);
             pair[1] |= (uint32_t)__builtin_bit_cast(uint16_t, rest) << (16 * q);
           }

@@ -42,3 +42,52 @@ def check(T, E, k, D, F, dtype, eight, unit, **how):
 @pytest.mark.parametrize("T,E,k,D,F", SIZES)
 def test_both_terms(T, E, k, D, F, dtype, eight):
     check(T, E, k, D, F, dtype, eight, 1.0)
+
+
+def beyond(dtype, eight, fp32):
+    """One token whose hidden value is beyond the type in every column, in fp32 too or just not, and one of others."""
+    E, D, F = 2, 32, 40
+    w_in, w_out = torch.zeros(E, 2 * F, D), torch.ones(E, D, F)
+    x = torch.ones(2, D)
+    w_out[:, 1::2] = -1.0
+    if dtype is HF:
+        w_in[0] = 12.0                             # h = 384 * 384
+    else:
+        # 2^128 (1 - 2^-9), half way between bfloat16's largest value and what would follow; or 2^130.
+        w_in[0] = 2.0 ** 59
+        w_in[0, F:, 16:] *= 1.0 - 2.0 ** -8
+        if fp32:
+            w_in[0] *= 2.0
+    w_in[1] = 2.0 ** -6
+    router = torch.zeros(E, D)
+    router[0, 0], router[1, 0] = 1.0, -1.0
+    x[1, 0] = -1.0
+    if not eight:
+        return [v.cuda() for v in (x.to(dtype), router, w_in.to(dtype), w_out.to(dtype))], {}
+    codes = torch.full((E, 2 * F, D), 1.0)
+    scale = torch.ones(E, 1, 1)
+    scale[0], scale[1] = w_in[0].max(), 2.0 ** -6   # one block: h = 2^128 or more for bfloat16
+    return ([v.cuda() for v in (x.to(dtype), router, codes.to(ref.E4), w_out.to(ref.E4))],
+            dict(in_scale=scale.cuda(), out_scale=torch.ones(E, 1, 1).cuda()))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype,fp32", [(BF, False), (BF, True), (HF, False)])
+def test_a_hidden_value_beyond_its_type_is_infinite(dtype, fp32, eight):
+    """As it is in `experts`, and not NaN."""
+    print(dtype, fp32, eight, flush=True)
+    args, how = beyond(dtype, eight, fp32)
+    y, r = sg.expert_step(*args, 1, **how)
+    torch.cuda.synchronize()
+    assert r.col.tolist() == [[0], [1]]
+    sign = torch.ones(32, device="cuda")
+    sign[1::2] = -1.0
+    assert torch.equal(y[0].float(), sign * float("inf"))
+    if not eight:
+        z = sg.experts(args[0], args[2], args[3], r.col, r.val)
+        assert torch.equal(y[0], z[0])
+    # g = u = 30 / 64 in every column, which sum to 40 h.
+    g = torch.tensor(30 / 64, dtype=torch.float64)
+    h = float(g * torch.sigmoid(g) * g) * 40
+    u = {BF: 2.0 ** -8, HF: 2.0 ** -11}[dtype]
+    assert bool(((y[1].double() - sign.double() * h).abs() <= (u + 2.0 ** -14) * h).all())
