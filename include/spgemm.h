@@ -564,8 +564,9 @@ typedef struct spgemm_expert_step_desc {
  * ceil(F / 128), fp32; else they are not read.  The 8-bit values are multiplied as
  * they are, in x's type, and the scales applied in fp32 to the sums over 64
  * columns.  Products and sums in fp32, in an order that the sizes and the picked
- * experts fix; the hidden vector is held in two terms of x's type, 16 or 22 bits (a value
- * beyond the type is infinite: in fp16 it has to be below 65520), y is rounded once.
+ * experts fix; the hidden vector is held in two terms of x's type, 16 or 22 bits (fp16: to
+ * 2^-36 below 2^-14; a value beyond the type is infinite: in fp16 it has to be
+ * below 65520), y is rounded once.
  * Errors: INVALID_ARG (as spgemm_route; more than 16 tokens; a width below 16; types, strides, null
  * arrays, a workspace too small), INDEX_OVERFLOW (a width above 2^20), HIP. */
 spgemm_status spgemm_expert_step_workspace(const spgemm_expert_step_desc *desc,

@@ -219,6 +219,12 @@ struct Share<T, true> {
   }
 };
 
+// What the second term of the hidden vector is multiplied by.  fp16 has no steps below
+// 2^-24: as it is, the second term of values below 2^-3 would lose bits, and below 2^-14
+// all of them.  The largest one is 2^4, so that its units fit the type.
+template <typename T>
+constexpr float kRestUnit = __is_same(T, __bf16) ? 1.0f : 2048.0f;
+
 struct StepArgs {
   RouteRow row;
   const void* x;
@@ -485,7 +491,7 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             const T first = from_f32<T>(hv);
             // Nothing is left of a value beyond the type, or y were inf - inf.
             const bool finite = fabsf(to_f32(first)) < INFINITY;
-            const T rest = from_f32<T>(finite ? hv - to_f32(first) : 0.0f);
+            const T rest = from_f32<T>(finite ? (hv - to_f32(first)) * kRestUnit<T> : 0.0f);
             pair[0] |= (uint32_t)__builtin_bit_cast(uint16_t, first) << (16 * q);
             pair[1] |= (uint32_t)__builtin_bit_cast(uint16_t, rest) << (16 * q);
           }
@@ -593,10 +599,13 @@ __global__ __launch_bounds__(kNT) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     auto add = [&](const W& w, Hidden& h, f32x4& sum) {
       if (ragged && __ballot(h.drop > 0)) h.h.drop(h.drop), h.rest.drop(h.drop);
       f32x4 acc = {0, 0, 0, 0};
-      acc = mfma16(T{}, w.half(0), h.h.half(0), acc);
-      acc = mfma16(T{}, w.half(1), h.h.half(1), acc);
       acc = mfma16(T{}, w.half(0), h.rest.half(0), acc);
       acc = mfma16(T{}, w.half(1), h.rest.half(1), acc);
+      if constexpr (kRestUnit<T> != 1.0f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] *= 1.0f / kRestUnit<T>;
+      acc = mfma16(T{}, w.half(0), h.h.half(0), acc);
+      acc = mfma16(T{}, w.half(1), h.h.half(1), acc);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         sum[j] += h.drop >= 0 ? (k8 ? h.value * h.scale : h.value) * acc[j] : 0.0f;

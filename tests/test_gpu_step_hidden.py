@@ -91,3 +91,24 @@ def test_a_hidden_value_beyond_its_type_is_infinite(dtype, fp32, eight):
     h = float(g * torch.sigmoid(g) * g) * 40
     u = {BF: 2.0 ** -8, HF: 2.0 ** -11}[dtype]
     assert bool(((y[1].double() - sign.double() * h).abs() <= (u + 2.0 ** -14) * h).all())
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -6, 2.0 ** -10])
+@pytest.mark.parametrize("T,E,k,D,F", SIZES)
+def test_float16_holds_small_values_in_both_terms(T, E, k, D, F, size, eight):
+    """The second term is held in units of 2^-11, so that what it leaves does not grow beside small values."""
+    check(T, E, k, D, F, HF, eight, 2.0 ** 11, size=size)
+
+
+@pytest.mark.parametrize("T,k", [(1, 2), (5, 2), (16, 3)])
+def test_small_values_of_float16_with_large_scales(T, k):
+    """Hidden values near 2^-12 that the scales of 8-bit weights bring back into y's range: the steps of an unscaled
+    second term would be 2^-13 of them and more."""
+    E, D, F = 6, 264, 130
+    t = list(ref.inputs(T, E, k, D, F, HF, True, 77 + T, size=2.0 ** -12))
+    t[5] = t[5] * 2.0 ** 12
+    g = [v.cuda() for v in t]
+    y, r = sg.expert_step(*g[:4], k, in_scale=g[4], out_scale=g[5])
+    torch.cuda.synchronize()
+    assert_within(y, *ref.layer(t, r.col.cpu(), r.val.cpu(), 2.0 ** 11), "y")

@@ -43,3 +43,15 @@ def test_small_values_of_float16_need_the_unit(eight):
     assert bool(((y - want).abs() <= rough).all())
     y = ref.layer(t, col, val, 1.0, lambda h, i: ref.held(h, HF, unit=2.0 ** 11))
     assert bool(((y - want).abs() <= bound).all())
+
+
+def test_large_scales_show_what_a_second_term_without_units_loses():
+    t = list(ref.inputs(5, 6, 2, 264, 130, HF, True, 82, size=2.0 ** -12))
+    t[5] = t[5] * 2.0 ** 12
+    col, val, _ = expert_reference.route((t[0].double() @ t[1].double().t()).float(), 2)
+    val = val.float()
+    want, bound = ref.layer(t, col, val, 2.0 ** 11)
+    y = ref.layer(t, col, val, 2.0 ** 11, lambda h, i: ref.held(h, HF)).to(HF).double()
+    assert bool(((y - want).abs() > bound).any())   # one value outside fails a test
+    y = ref.layer(t, col, val, 2.0 ** 11, lambda h, i: ref.held(h, HF, unit=2.0 ** 11)).to(HF).double()
+    assert bool(((y - want).abs() <= bound).all())
