@@ -488,6 +488,9 @@ spgemm_status spgemm_dispatch(int64_t T, int32_t k, int64_t E,
                               int32_t *dEntry, void *dWork, int64_t work_bytes,
                               void *stream);
 
+/* A kept_form that nothing but a caller who asks for it sets. */
+#define SPGEMM_KEPT_E4M3 0x45344d33
+
 /* An expert layer: x is T x D, w_in E x 2F x D (an expert's F gate rows, then
  * its F up rows), w_out E x D x F, all bf16 or fp16. */
 typedef struct spgemm_experts_desc {
@@ -497,9 +500,11 @@ typedef struct spgemm_experts_desc {
   int32_t k;           /* slots of a row of R                                  */
   spgemm_dtype dtype;  /* SPGEMM_BF16 or SPGEMM_F16                            */
   int32_t unaligned;   /* 1: a base address is no multiple of 16 bytes         */
-  int32_t kept_form;   /* 0: the kept block holds the pre-activations; 1: the
-                          rows of x in 8 bits (spgemm_layer_norm_forward has the
-                          form), about D bytes a token in place of 8 F an entry */
+  int32_t kept_form;   /* SPGEMM_KEPT_E4M3: the kept block holds the rows of x
+                          in 8 bits (spgemm_layer_norm_forward has the form),
+                          about D bytes a token in place of 8 F an entry; any
+                          other value: the pre-activations (this field was
+                          reserved, and callers may have left it unset)        */
 } spgemm_experts_desc;
 
 /* Bytes of the kept block and of the two workspaces (any may be NULL).
@@ -527,7 +532,7 @@ spgemm_status spgemm_experts_forward(const spgemm_experts_desc *desc,
 
 /* Gradients of x (T x D), w_in, w_out (in the tensors' type) and of the
  * values (T x k, fp32, 0 in empty slots), for the routing that the forward pass
- * was given (the kept block holds it).  With kept_form 1 they are the gradients at
+ * was given (the kept block holds it).  With SPGEMM_KEPT_E4M3 they are the gradients at
  * the x that the 8 bits stand for, whose pre-activations are made again; dX is not
  * read then and may be NULL.  Every element is written: 0 for
  * experts without tokens.  Sums in fp32, in an order that only the routing

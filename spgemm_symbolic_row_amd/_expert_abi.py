@@ -11,6 +11,9 @@ class RouteOptions(ctypes.Structure):
                 ("no_renormalise", c_i32), ("scale", ctypes.c_float)]
 
 
+KEPT_E4M3 = 0x45344d33  # SPGEMM_KEPT_E4M3
+
+
 class ExpertsDesc(ctypes.Structure):
     _fields_ = [("tokens", c_i64), ("experts", c_i64), ("width", c_i64), ("hidden", c_i64),
                 ("x_ld", c_i64), ("grad_ld", c_i64), ("k", c_i32), ("dtype", ctypes.c_int),

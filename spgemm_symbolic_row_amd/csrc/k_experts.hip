@@ -1257,9 +1257,11 @@ Path path_of(const Sizes& z, bool keep) {
 int tile_rows(const Sizes& z) { return z.n > 256 * z.E ? 256 : 128; }
 
 // What the forward pass leaves for the backward pass: the dispatch, and the
-// pre-activations (8 F bytes to an entry) or, in form 1, the rows of x in 8 bits,
+// pre-activations (8 F bytes to an entry) or, by keeps_codes, the rows of x in 8 bits,
 // from which the backward pass makes them again.  8192 tokens with 8 of 64 experts,
 // 2048 x 1024: 538 or 18 MB.
+bool keeps_codes(const spgemm_experts_desc& d) { return d.kept_form == SPGEMM_KEPT_E4M3; }
+
 struct Kept {
   Dispatch d;
   float* g;
@@ -1466,8 +1468,8 @@ void forward(const spgemm_experts_desc& desc, const void* x, const void* w_in, c
   Kept kp{};
   if (kept) {
     Carver c(kept);
-    kp = take_kept(c, z, desc.kept_form);
-    if (desc.kept_form)
+    kp = take_kept(c, z, keeps_codes(desc));
+    if (keeps_codes(desc))
       launch_rows_encode(desc.dtype, z.T, z.D, desc.x_ld, x, kp.code, kp.scale, s);
   } else {
     kp.d = w.d;
@@ -1524,9 +1526,9 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
               void* dw_in, void* dw_out, float* dval, const BackwardWork& w, hipStream_t s) {
   const Sizes z = sizes_of(desc);
   Carver kc((void*)kept);
-  Kept kp = take_kept(kc, z, desc.kept_form);
+  Kept kp = take_kept(kc, z, keeps_codes(desc));
   Rows xr{w.x, z.Dp};
-  if (desc.kept_form)
+  if (keeps_codes(desc))
     launch_rows_decode(desc.dtype, z.T, z.D, kp.code, kp.scale, w.x, s);
   else
     xr = padded_rows(x, desc.x_ld, z.T, z.D, w.pad.x, s);
@@ -1538,7 +1540,7 @@ void backward(const spgemm_experts_desc& desc, const void* x, const void* w_in,
                        1, w.w_size);
   else if (z.S2 != 2 * z.F)
     hipLaunchKernelGGL(k_zero16, dim3(grid_for(z.n * z.S2)), dim3(256), 0, s, w.dgu, z.n * z.S2);
-  if (desc.kept_form) {
+  if (keeps_codes(desc)) {
     kp.g = w.g;
     kp.u = w.u;
     // h goes where w h will be.
@@ -1635,8 +1637,6 @@ spgemm_status check_desc(const spgemm_experts_desc* d) {
   if (d->tokens < 0 || d->experts < 1 || d->experts > kMaxExperts || d->k < 1 || d->k > 64)
     return refuse(SPGEMM_ERR_INVALID_ARG,
                   "experts: tokens < 0, experts outside [1, 1024] or k outside [1, 64]");
-  if (d->kept_form < 0 || d->kept_form > 1)
-    return refuse(SPGEMM_ERR_INVALID_ARG, "experts: kept_form outside [0, 1]");
   if (d->width < 1 || d->hidden < 1 || d->x_ld < d->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: empty width, or a row stride below it");
   if (d->x_ld >= 1 << 30 || d->grad_ld >= 1 << 30)
@@ -1675,7 +1675,7 @@ extern "C" spgemm_status spgemm_experts_sizes(const spgemm_experts_desc* desc, i
                       desc->grad_ld % 8;
   if (kept) {
     Carver c(nullptr);
-    take_kept(c, z, desc->kept_form);
+    take_kept(c, z, keeps_codes(*desc));
     *kept = c.used;
   }
   if (forward_work) {
@@ -1685,7 +1685,7 @@ extern "C" spgemm_status spgemm_experts_sizes(const spgemm_experts_desc* desc, i
   }
   if (backward_work) {
     Carver c(nullptr);
-    take_backward(c, z, desc->dtype == SPGEMM_F16, desc->kept_form, padded);
+    take_backward(c, z, desc->dtype == SPGEMM_F16, keeps_codes(*desc), padded);
     *backward_work = c.used;
   }
   return SPGEMM_OK;
@@ -1722,7 +1722,8 @@ extern "C" spgemm_status spgemm_experts_backward(
   if (st != SPGEMM_OK) return st;
   if (!dGradWIn || !dGradWOut || !dWork ||
       (desc->tokens > 0 &&
-       ((!dX && !desc->kept_form) || !dWIn || !dWOut || !dGradY || !dKept || !dGradX || !dGradVal)))
+       ((!dX && !keeps_codes(*desc)) || !dWIn || !dWOut || !dGradY || !dKept || !dGradX ||
+        !dGradVal)))
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: null array");
   if (desc->grad_ld < desc->width)
     return refuse(SPGEMM_ERR_INVALID_ARG, "experts: a row stride below the width");
@@ -1737,8 +1738,8 @@ extern "C" spgemm_status spgemm_experts_backward(
   }
   Carver c(dWork);
   const BackwardWork w =
-      take_backward(c, z, desc->dtype == SPGEMM_F16, desc->kept_form,
-                    needs_padding(*desc, desc->kept_form ? nullptr : dX, dWIn, dWOut, dGradY));
+      take_backward(c, z, desc->dtype == SPGEMM_F16, keeps_codes(*desc),
+                    needs_padding(*desc, keeps_codes(*desc) ? nullptr : dX, dWIn, dWOut, dGradY));
   if (work_bytes < c.used) return refuse(SPGEMM_ERR_INVALID_ARG, "experts: workspace too small");
   if (desc->dtype == SPGEMM_BF16)
     backward<__bf16>(*desc, dX, dWIn, dWOut, dGradY, dKept, dGradX, dGradWIn, dGradWOut,

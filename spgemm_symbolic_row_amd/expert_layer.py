@@ -28,7 +28,7 @@ import torch
 
 import spgemm_symbolic_row_amd as _package
 
-from ._expert_abi import ExpertStepDesc, ExpertsDesc, RouteOptions, c_i64
+from ._expert_abi import KEPT_E4M3, ExpertStepDesc, ExpertsDesc, RouteOptions, c_i64
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 2, torch.float16: 3}
 _E4M3 = 4
@@ -240,7 +240,7 @@ def experts(x, w_in, w_out, col, val, keep=False):
     if isinstance(keep, str):
         if keep != "e4m3":
             raise ValueError("keep must be False, True or 'e4m3'")
-        form = 1
+        form = KEPT_E4M3
     x_ld = _rows(x, "x")
     T, D = x.shape
     if w_in.dim() != 3 or w_out.dim() != 3 or col.dim() != 2:
@@ -281,7 +281,7 @@ def experts_backward(grad_y, kept):
     inputs = (w_in, w_out) if x is None else (x, w_in, w_out)
     d, _, _, work_bytes = _experts_desc(T, E, D, F, D if x is None else _rows(x, "x"),
                                         _rows(grad_y, "grad_y"), k, _TYPES[dtype],
-                                        _off16(*inputs, grad_y), int(x is None))
+                                        _off16(*inputs, grad_y), KEPT_E4M3 if x is None else 0)
     with _on(w_in):
         gx = torch.empty(T, D, dtype=dtype, device=dev)
         gw_in, gw_out = torch.empty_like(w_in), torch.empty_like(w_out)
