@@ -14,7 +14,8 @@ k slots a row (`col`, `val`; column -1 in an empty slot, and those last).
 Argument marshalling only: every step runs in the HIP library on the current
 stream of the tensors' device, asynchronously.  Nothing is recorded for torch's
 backward pass, the backward calls are the only way to the gradients: while torch
-records, tensors that require one are refused (torch.no_grad() or detach()).
+records, tensors that require one are refused (torch.no_grad() or detach()).  So are tensors
+that carry a tangent of torch's forward mode.
 """
 from __future__ import annotations
 
@@ -68,11 +69,24 @@ def _stream(x):
 _requires_grad = torch.Tensor.requires_grad.__get__
 
 
+_forward_ad = torch.autograd.forward_ad
+
+
 def _unrecorded(*tensors):
-    """A result of tensors that require a gradient would have no graph."""
+    """A result of tensors that require a gradient would have no graph, and one of tensors
+    that carry a tangent no tangent."""
     if torch.is_grad_enabled() and True in map(_requires_grad, tensors):
         raise TypeError("a tensor requires a gradient, and nothing is recorded here: use the "
                         "backward calls, under torch.no_grad() or with detached tensors")
+    if _forward_ad._current_level >= 0:  # else no tensor has one
+        _without_tangents(*tensors)
+
+
+def _without_tangents(*tensors):
+    for t in tensors:
+        if _forward_ad.unpack_dual(t).tangent is not None:
+            raise TypeError("a tensor carries a tangent, and forward-mode derivatives are not "
+                            "made here: pass its primal")
 
 
 def _rows(x, what):
@@ -170,6 +184,7 @@ def route_backward(logits, routing, grad_val):
     dev = logits.device
     _dense(grad_val, routing.col.shape, torch.float32, dev, "grad_val")
     _unrecorded(grad_val)
+    _without_tangents(logits)
     b = routing.bias
     with _on(logits):
         out = torch.empty(T, E, dtype=logits.dtype, device=dev)
