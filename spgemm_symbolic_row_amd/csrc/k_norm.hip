@@ -254,13 +254,17 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a) {
             for (int j = 0; j < 8; ++j) n[r][v][j] = to_f32(raw[r].x[v][j]);
           }
 #pragma unroll
+          for (int j = 0; j < 8; ++j) n[r][v][j] = (n[r][v][j] - raw[r].mean) * rstd[r];
+          // Columns beyond the row have no dy; their -m r may be infinite where n is not.
+          const int left = a.D - (v * L + lane) * 8;
+          if (left < 8)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j >= left) n[r][v][j] = 0.0f;
+#pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float gj = to_f32(raw[r].dy[v][j]), aj = gj * w[v][j];
-            // Columns beyond the row have no dy; their -m r may be infinite where n is not.
-            const float nj = (v * L + lane) * 8 + j < a.D
-                                 ? (n[r][v][j] - raw[r].mean) * rstd[r] : 0.0f;
+            const float gj = to_f32(raw[r].dy[v][j]), aj = gj * w[v][j], nj = n[r][v][j];
             g[r][v][j] = gj;
-            n[r][v][j] = nj;
             db[v][j] += gj;
             dw[v][j] += gj * nj;
             s[2 * r] += aj;
