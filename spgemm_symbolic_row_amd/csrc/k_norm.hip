@@ -222,7 +222,8 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a) {
     }
   };
   // Every work group takes the same number of turns, so that all lanes of a row meet.
-  // The rows of the next turn are loaded ahead where they fit the registers.
+  // The rows of the next turn are loaded ahead, but not those of two chunks, which do not fit
+  // the registers (2000 x 16384 fp32 152 us, without 95).
   constexpr bool kAhead = V == 1;
   const int64_t step = (int64_t)gridDim.x * kGroups * R;
   Raw raw[R];
@@ -348,11 +349,21 @@ __global__ __launch_bounds__(1024) void k_norm_sum(const float* __restrict__ par
 
 constexpr int64_t kMostColumns = 16384;
 
-// Work groups of a gradient, each of which leaves a partial row: as many as run at
-// a time.  Of 256 threads (32768 x 2048 bfloat16, rows kept in 8 bits, forward and
-// backward): 512 work groups 142 us, 768 139, 1024 148.
+// Work groups of a gradient, each of which leaves a partial row: three of 256 threads
+// to a compute unit, else one.  More run at a time, but leave more partial rows.  us of the
+// backward pass:
+//   256 threads, work groups        512   768  1024  1536
+//     32768 x 2048 bf16              83    82    96    89
+//     the same kept in 8 bits        80    73    84    77
+//     65536 x 256 bf16               45    36    34    40
+//     4099 x 1001 fp16               17    18    22    21
+//   512 and 1024 threads            128   192   256   384   512
+//     6000 x 4096 fp32               66    56    54    62    62
+//     2000 x 4096 bf16               20    18    17    20    22
+//     8192 x 8192 bf16              105    84    84    91    89
+//     2000 x 16384 fp32             120   100    96   107   109
 int64_t grad_groups(int64_t T, int64_t rows, int threads) {
-  const int64_t most = threads == 256 ? 768 : threads == 512 ? 512 : 256;
+  const int64_t most = threads == 256 ? 768 : 256;
   return std::max<int64_t>(1, std::min((T + rows - 1) / rows, most));
 }
 
