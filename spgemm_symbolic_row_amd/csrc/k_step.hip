@@ -23,13 +23,24 @@
 // by a work group that runs and that waits for nothing: however few work groups
 // are on the chip at a time, every wait ends.
 //
-// One token with 6 of 64 experts of 2048 x 1024 takes 29 us where a copy of its 75 MB
-// takes 15: the logits' launch 3, routing and tables 6, W_in 10 (5 TB/s), the wait for
-// the slowest result 2, W_out, whose weights are there by then, 4.  16 tokens with 55
-// of 128 experts of 2048 x 768 take 139 us for 519 MB: W_in runs at 5.1 TB/s, W_out at
-// 3.9: a step there has eight accesses of h to two of weights, of 16 cycles of the vector
-// memory path each, about half of its 44 us; neither the waits nor the addresses bound it
-// (without conditions between steps, 32-bit addresses: 145 against 144, side by side).
+// One token with 6 of 64 experts of 2048 x 1024 takes 30 us where a copy of its 76 MB
+// takes 15: the logits' launch 3, routing and tables 6, W_in 11 (5 TB/s), the wait for
+// the slowest result 3, W_out, whose weights are there by then, 5.  16 tokens with 55
+// of 128 experts of 2048 x 768 take 144 to 150 us for 519 MB: W_in runs at 5.1 TB/s, W_out
+// at 3.3: a step there has eight accesses of h to two of weights.  The unit of the vector
+// memory path that takes the addresses is busy 71% of the whole kernel, the one that
+// returns the data 85%, 60 of them waiting for the caches; neither the waits of the loop
+// nor its addresses bound it (without conditions between steps, 32-bit addresses: 145
+// against 144, side by side).
+//
+// route, the router's product and experts, the calls that this joins, take longer at 1, 4
+// and 8 tokens and less at 2 and from 12 on, by up to 8% (12 tokens, 6 of 64 experts of
+// 2048 x 1024: 126 against 133 us); they round the hidden vector once.  16 tokens are what
+// the columns of a product hold.
+//
+// The hand-over of h below is written for gfx950's caches: stores of agent scope are
+// written through and done once vmcnt is 0.  No other target has the products and
+// conversions used here, so that the file is not built for one.
 //
 // A work group of 8 waves has a compute unit: two of them, with half the registers,
 // spill or have half the loads on their way (W_in's tiles 16 against 11 us).
@@ -129,8 +140,8 @@ __device__ __forceinline__ int dropped(int s, int K) {
   return min(s * kStep + (lane_id() >> 4) * 16 - k_of(s, K), 16);
 }
 
-// Loads at addresses that are no multiple of 4 bytes take four times as long as
-// others (1025 x 1025 bfloat16: 240 us, 1026 x 1026: 98 us), so unless `even` the words that hold
+// Loads at addresses that are no multiple of 4 bytes make a whole call 2.4 times as long
+// (1025 x 1025 bfloat16 240 us, 1026 x 1026 98), so unless `even` the words that hold
 // the values are loaded, all of which are at least in part the row's, and shifted
 // when they are used.  16-bit values are the operands as they are; 8-bit ones are
 // decoded when used, exactly, to x's type.

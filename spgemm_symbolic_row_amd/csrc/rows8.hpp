@@ -6,8 +6,9 @@
 // What is not finite is held as NaN.  The code depends on x's bits alone: every
 // step but the one rounding is exact.
 //
-// Half a step of e4m3 is 2^-4 of the value down to 2^-14 of the block's maximum,
-// and an error of at most 2^-18 of it below (448 s < 2 max, 2^-10 s).
+// Half a step of e4m3 is 2^-4 of the value down to 2^-6 s, and below that the error is
+// at most 2^-10 s.  Where s is above its floor, 448 s < 2 max: the two are less than
+// max / 14336 and max / 229376 of the block's maximum.
 //
 // A lane holds 8 neighbouring columns, so 16 lanes hold a block: its maximum is
 // four DPP steps inside a row of lanes.

@@ -43,10 +43,11 @@ def layer_norm(x, weight, bias=None, eps=1e-5, keep=False):
 
     x: T x D (rows contiguous; float32, bfloat16 or float16; D up to 16384),
     weight and bias: D elements, float32 or x's type, both alike.  With keep=True also returns
-    what layer_norm_backward takes; with keep="e4m3" that holds x in 8 bits (a
-    power-of-two scale for each 128 columns of a row), and x itself need not stay:
-    the gradients are then those at the values that the 8 bits stand for, with
-    the mean and the variance of x."""
+    what layer_norm_backward takes, and x and weight must not change before; with
+    keep="e4m3" that holds x in 8 bits (a power-of-two scale for each 128 columns of
+    a row), and x itself need not stay: the gradients are then those at the values
+    that the 8 bits stand for, with the mean and the variance of x.  They are up to
+    1/16 of |x| off, so take keep=True for rows whose mean is many deviations."""
     x_ld = _rows(x, "x")
     T, D = x.shape
     dt = _TYPES.get(x.dtype)
