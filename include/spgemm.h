@@ -563,7 +563,8 @@ typedef struct spgemm_expert_step_desc {
 /* z = router x (router E x D; sums in 64 bits, rounded to fp32), then dCol and
  * dVal (T x k) as spgemm_route gives them for z, then y (T x D, contiguous) as
  * spgemm_experts_forward does; the columns are the routing's, so that y is the
- * layer's whole result.  All arrays but x are contiguous; any alignment.
+ * layer's whole result.  All arrays but x are contiguous; any alignment that their
+ * elements have, dWork at a multiple of 4 bytes.
  * With SPGEMM_E4M3 an expert's weight is W[r, c] = w[r, c] s[r / 128, c / 128]:
  * dInScale is E x ceil(2F / 128) x ceil(D / 128), dOutScale E x ceil(D / 128) x
  * ceil(F / 128), fp32; else they are not read.  The 8-bit values are multiplied as

@@ -34,7 +34,7 @@
 // against 144, side by side).
 //
 // route, the router's product and experts, the calls that this joins, take longer at 1, 4
-// and 8 tokens and less at 2 and from 12 on, by up to 8% (12 tokens, 6 of 64 experts of
+// and 8 tokens and less at 2 and from 12 on, by up to 9% (12 tokens, 6 of 64 experts of
 // 2048 x 1024: 126 against 133 us); they round the hidden vector once.  16 tokens are what
 // the columns of a product hold.
 //
@@ -805,6 +805,8 @@ extern "C" spgemm_status spgemm_expert_step(
   if (!dX || !dRouter || !dWIn || !dWOut || !dY || !dCol || !dVal || !dWork ||
       (scaled && (!dInScale || !dOutScale)))
     return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: null array");
+  if ((uintptr_t)dWork % 4)  // its counters and h are accessed by atomic operations
+    return refuse(SPGEMM_ERR_INVALID_ARG, "expert_step: workspace not at a multiple of 4 bytes");
   Carver c(dWork);
   const Work w = take_work(c, d);
   if (work_bytes < c.used)
