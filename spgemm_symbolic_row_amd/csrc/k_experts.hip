@@ -1256,12 +1256,14 @@ Path path_of(const Sizes& z, bool keep) {
 // about half on average, else 128.
 int tile_rows(const Sizes& z) { return z.n > 256 * z.E ? 256 : 128; }
 
+// Whether rows of x are kept in 8 bits.  Any other value is one that a caller from before the
+// field may have left there.
+bool keeps_codes(const spgemm_experts_desc& d) { return d.kept_form == SPGEMM_KEPT_E4M3; }
+
 // What the forward pass leaves for the backward pass: the dispatch, and the
 // pre-activations (8 F bytes to an entry) or, by keeps_codes, the rows of x in 8 bits,
 // from which the backward pass makes them again.  8192 tokens with 8 of 64 experts,
 // 2048 x 1024: 538 or 18 MB.
-bool keeps_codes(const spgemm_experts_desc& d) { return d.kept_form == SPGEMM_KEPT_E4M3; }
-
 struct Kept {
   Dispatch d;
   float* g;

@@ -8,10 +8,11 @@
 // L lanes take a row, 8 columns to a lane, so a row is read once and stays in
 // registers; the sum of squares is taken about the mean, which loses nothing in
 // rows whose mean is large.  The gradient from rows in 8 bits does: it takes n at the
-// rounded row, which is 2^-4 |x| off, a whole deviation where the mean is 16 of them.  R rows at once keep enough loads in flight.  The
-// gradient's work groups take rows in turn and keep their share of dw and db in
-// registers; one partial row of each work group is then summed by a second
-// kernel, in an order that the sizes alone fix.  Sums are in 32 bits.
+// rounded row, which is 2^-4 |x| off, a whole deviation where the mean is 16 of them.
+// R rows at once keep enough loads in flight.  The gradient's work groups take rows in
+// turn and keep their share of dw and db in registers; one partial row of each work
+// group is then summed by a second kernel, in an order that the sizes alone fix.  Sums
+// are in 32 bits.
 //
 // Both passes are bound by their bytes: 16384 x 2048 bfloat16 forward 24 us (5.6
 // TB/s; a large copy runs at 4.9), 6000 x 4096 fp32 forward 39 and backward 54 us (5.1
